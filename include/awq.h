@@ -28,7 +28,7 @@
  * Dequantized weight: w(k, n) = fp16_rne(scale(g, n) * (code(k, n) - zero(g, n))).
  * Layer output: y = fp16_rne(sum_k x(m, k) * w(k, n)), accumulated in fp32.
  *
- * Shape rules (AWQ_ERROR_SHAPE otherwise): K, N, G > 0; K % 8 == 0;
+ * Shape rules of a layer (AWQ_ERROR_SHAPE otherwise): K, N, G > 0; K % 8 == 0;
  * N % 8 == 0; G % 8 == 0; K % G == 0; every array below 2^31 elements.
  * Every call that takes an awq_layer takes it in any qweight layout (see
  * AWQ_LAYOUT_*) with the same results, bit for bit where the call is exact.
@@ -334,6 +334,128 @@ awq_status awq_scale_search(const uint16_t *x, int32_t M, const uint16_t *w, int
                             int32_t group_size, int32_t symmetric, const float *alphas,
                             int32_t n_alpha, double *losses, int32_t *best, float *best_scales,
                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The 8-bit paged key/value cache of a block's attention: the half of the
+ * decoder block beside the linear layers that the pages' fused stack puts into
+ * one attention module with the position rotation and the cache (pyshine.com
+ * AutoAWQ tour, the introduction: QuantAttentionFused; unfragile.ai AutoAWQ
+ * page, the fused attention paragraph).  The pages give neither the cache's
+ * type nor its layout; the readings taken are stated here.
+ *
+ * A page holds page_size consecutive tokens of one sequence, for all kv heads:
+ *   k         e4m3 [pages][kv_heads][page_size][head_dim]
+ *   v         e4m3 [pages][kv_heads][head_dim][page_size]   (tokens innermost)
+ *   k_scales  fp32 [pages][kv_heads];  v_scales  fp32 [pages][kv_heads]
+ * e4m3: one byte, sign, 4 exponent bits (bias 7), 3 mantissa bits, largest 448,
+ * 0x7F and 0xFF NaN.  A key or value element is its code times its page's and
+ * head's scale.  Codes of slots that hold no token may be anything.
+ * page_size: a power of two, 16 to 256; head_dim 64, 128 or 256
+ * (AWQ_ERROR_UNSUPPORTED otherwise).  k and v may be of any size (offsets are
+ * 64-bit); pages * kv_heads < 2^31, kv_heads <= 65535.
+ */
+typedef struct awq_kv_cache {
+    uint8_t *k;
+    uint8_t *v;
+    float *k_scales;
+    float *v_scales;
+    int32_t pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+} awq_kv_cache;
+
+/*
+ * What a call works on: `rows` new rows of `seqs` sequences, one after the
+ * other.  Sequence b has rows q_starts[b] .. q_starts[b + 1] - 1 and holds
+ * kv_lens[b] tokens WITH those rows, which are its last ones: its row t stands
+ * at position kv_lens[b] - (q_starts[b + 1] - q_starts[b]) + t.  The token at
+ * position i is in slot i % page_size of page page_table[b][i / page_size].
+ * The three arrays are device memory, read by the kernels only, so one captured
+ * graph serves every step that changes them.  Rows behind q_starts[seqs] (a
+ * padded batch) belong to no sequence: nothing is read or written for them.
+ * A sequence with no rows, or none at all (seqs or rows 0), is fine.  seqs <=
+ * 65535, seqs * table_width < 2^31, table_width * page_size <= 2^30.
+ *
+ * max_q, max_kv: the most rows and tokens of a sequence in this call.  They size
+ * grids and the workspace; smaller than the truth costs time, not correctness.
+ *
+ * The kernels read no memory outside the arrays whatever these hold: a length
+ * counts up to table_width * page_size tokens, rows below position 0 have no
+ * place, and a page number outside 0 .. pages - 1 names no page (its tokens are
+ * not written, and no row sees them).
+ */
+typedef struct awq_kv_batch {
+    const int32_t *page_table;   /* [seqs][table_width] */
+    const int32_t *kv_lens;      /* [seqs] */
+    const int32_t *q_starts;     /* [seqs + 1], ascending */
+    int32_t seqs;
+    int32_t table_width;
+    int32_t rows;                /* rows that the row arrays have */
+    int32_t max_q;
+    int32_t max_kv;
+} awq_kv_batch;
+
+/* Types of the rows (queries, keys, values, outputs). */
+#define AWQ_TYPE_FP16 0
+#define AWQ_TYPE_BF16 1
+
+/*
+ * awq_kv_append: rotates the rows' queries and keys by their positions, and
+ * writes the keys and values into the cache.
+ *   q [rows][q_heads][head_dim], k and v [rows][kv_heads][head_dim] of `type`,
+ *   with q_stride, k_stride, v_stride elements from row to row (slices of a
+ *   fused projection's output will do): at least heads * head_dim, a multiple of
+ *   8.  q_out: dense [rows][q_heads][head_dim].  q and q_out may both be NULL.
+ *   rope: fp32 [rope_positions][rot_dim], per position rot_dim / 2 cosines, then
+ *   as many sines; rot_dim 0 rotates nothing (rope may be NULL), else a multiple
+ *   of 16 up to head_dim: the first rot_dim elements of a head are rotated, in
+ *   the pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved != 0:
+ *     a' = a cos - b sin,  b' = b cos + a sin   in fp32,
+ *   q' is rounded once to `type`, k' goes to its code from fp32.
+ * Scale of a page and head: with e the least integer >= -64 such that the
+ * largest finite magnitude of the call's tokens in it is at most 448 * 2^e, the
+ * scale becomes 2^e if the call's first token there is in slot 0, and otherwise
+ * the larger of 2^e and the scale it has; codes of tokens that are there already
+ * are then moved to the new scale, code = e4m3_rne(code * old / new).  New codes
+ * are e4m3_rne(x / scale), to nearest, ties to even.
+ * A token whose key or value of a head holds a NaN or an infinity gets NaN key
+ * codes there, and zero for the value's non-finite elements: rows that see it
+ * come out NaN, others are not touched by it.
+ * A row at a position without a place (see awq_kv_batch), or behind the
+ * rotation's table, is dropped: its q_out row and the cache stay as they were.
+ * Two sequences may share pages that neither writes in this call.
+ */
+awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                         const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
+                         int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                         int32_t interleaved, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                         void *stream);
+
+/*
+ * awq_attention: attention of the rows over the cache, which holds their own
+ * keys and values already (awq_kv_append).  Query head x reads kv head
+ * x / (q_heads / kv_heads).
+ *   out[row][x] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q . k_j) - max),
+ * over the keys j that the row at position i sees: j <= i and, with a window
+ * > 0, j > i - window or j < sinks (the first tokens stay visible).  window 0:
+ * no window (sinks then say nothing).  A row that sees no key gets zeros.
+ * Products, maxima, sums and outputs are held in fp32; out is rounded once.
+ *   q [rows][q_heads][head_dim] with q_stride as above; out dense.
+ *   scale: finite (1 / sqrt(head_dim) by custom).
+ *   workspace: device scratch of at least awq_attention_workspace_bytes for the
+ *   same arguments, 16-byte aligned, owned by the caller, contents unspecified
+ *   before and after; NULL will do where the query returns 0.  Calls that may
+ *   overlap in time need one each.
+ * Deterministic: the same call gives the same bits.
+ */
+size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
+                                     const awq_kv_cache *cache, const awq_kv_batch *batch);
+
+awq_status awq_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
+                         int32_t type, float scale, int32_t window, int32_t sinks,
+                         const awq_kv_cache *cache, const awq_kv_batch *batch, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,7 +25,8 @@ ENTRY_POINTS = ("awq_status_string", "awq_pack", "awq_pack_zeros", "awq_repack",
                 "awq_gemm", "awq_gemv_gate_up", "awq_quantize", "awq_gemm_gate_up",
                 "awq_gemm_splitk_workspace_bytes", "awq_gemm_splitk", "awq_gemm_splitk_static",
                 "awq_channel_stats_workspace_bytes", "awq_channel_stats",
-                "awq_scale_search_workspace_bytes", "awq_scale_search")
+                "awq_scale_search_workspace_bytes", "awq_scale_search",
+                "awq_kv_append", "awq_attention_workspace_bytes", "awq_attention")
 
 # awq_status values of include/awq.h
 AWQ_SUCCESS = 0
@@ -46,6 +47,10 @@ LAYOUT_INTERLEAVED = 1
 LAYOUT_BLOCKED = 2        # interleaved words, 128-column blocks contiguous (N % 128 == 0)
 
 
+# types of the rows of the attention calls (AWQ_TYPE_* of include/awq.h)
+ROW_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
 class AwqError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(message)
@@ -58,6 +63,24 @@ class CLayer(ctypes.Structure):
     _fields_ = [("qweight", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("qzeros", ctypes.c_void_p), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class CKvCache(ctypes.Structure):
+    """``awq_kv_cache`` of include/awq.h."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class CKvBatch(ctypes.Structure):
+    """``awq_kv_batch`` of include/awq.h."""
+
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
 
 
 _LIB = None
@@ -108,6 +131,14 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.awq_scale_search.restype = ctypes.c_int
     lib.awq_scale_search.argtypes = [vp, i32, vp, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_float),
                                      i32, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    kv = [ctypes.POINTER(CKvCache), ctypes.POINTER(CKvBatch)]
+    lib.awq_kv_append.restype = ctypes.c_int
+    lib.awq_kv_append.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, vp, i32, i32, i32, *kv, vp]
+    lib.awq_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.awq_attention_workspace_bytes.argtypes = [i32, i32, i32, *kv]
+    lib.awq_attention.restype = ctypes.c_int
+    lib.awq_attention.argtypes = [vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, *kv, vp,
+                                  ctypes.c_size_t, vp]
     if path == LIBRARY:
         _LIB = lib
     return lib
@@ -444,3 +475,201 @@ def scale_search(x: torch.Tensor, w: torch.Tensor, group_size: int, alphas, symm
                                 _stream(stream)))
     return best, losses, scales
 
+
+# ---- the 8-bit paged key/value cache ----
+
+def _kv_check(t, dtype, shape, name):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {getattr(t, 'dtype', type(t))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+@dataclass(frozen=True)
+class KvCache:
+    """A paged cache of keys and values held in e4m3 codes, with one fp32 scale for
+    each page and kv head (see ``awq_kv_cache`` in include/awq.h).  Shapes and
+    devices are checked here, once; the calls take the view made here."""
+
+    k: torch.Tensor          # float8_e4m3fn [pages][kv_heads][page_size][head_dim]
+    v: torch.Tensor          # float8_e4m3fn [pages][kv_heads][head_dim][page_size]
+    k_scales: torch.Tensor   # fp32 [pages][kv_heads]
+    v_scales: torch.Tensor
+
+    def __post_init__(self):
+        if self.k.dim() != 4:
+            raise ValueError(f"k must be [pages][kv_heads][page_size][head_dim], got {list(self.k.shape)}")
+        pages, heads, page, dim = self.k.shape
+        _kv_check(self.k, torch.float8_e4m3fn, (pages, heads, page, dim), "k")
+        _kv_check(self.v, torch.float8_e4m3fn, (pages, heads, dim, page), "v")
+        for name, t in (("k_scales", self.k_scales), ("v_scales", self.v_scales)):
+            _kv_check(t, torch.float32, (pages, heads), name)
+        for name in ("v", "k_scales", "v_scales"):
+            if getattr(self, name).device != self.k.device:
+                raise ValueError(f"{name} is on {getattr(self, name).device}, k on {self.k.device}")
+        ptr = [_dev(getattr(self, n), getattr(self, n).dtype, n) for n in ("k", "v", "k_scales", "v_scales")]
+        object.__setattr__(self, "_c", CKvCache(*ptr, pages, page, heads, dim))
+
+    @property
+    def kv_heads(self) -> int:
+        return self._c.kv_heads
+
+    @property
+    def head_dim(self) -> int:
+        return self._c.head_dim
+
+    @property
+    def device(self) -> torch.device:
+        return self.k.device
+
+
+def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> KvCache:
+    """An empty cache (codes and scales of pages that hold no token may be anything)."""
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+    return KvCache(new((pages, kv_heads, page_size, head_dim), torch.float8_e4m3fn),
+                   new((pages, kv_heads, head_dim, page_size), torch.float8_e4m3fn),
+                   new((pages, kv_heads), torch.float32), new((pages, kv_heads), torch.float32))
+
+
+@dataclass(frozen=True)
+class KvBatch:
+    """The sequences of a call (see ``awq_kv_batch`` in include/awq.h): device int32
+    arrays, whose contents may change from call to call (and from replay to replay
+    of a captured graph).  ``max_q`` and ``max_kv``, the most rows and tokens of a
+    sequence, size the grids: smaller than the truth costs time, not correctness."""
+
+    page_table: torch.Tensor   # int32 [seqs][table_width]
+    kv_lens: torch.Tensor      # int32 [seqs]: tokens with this call's rows
+    q_starts: torch.Tensor     # int32 [seqs + 1]
+    max_q: int
+    max_kv: int
+
+    def __post_init__(self):
+        if self.page_table.dim() != 2:
+            raise ValueError(f"page_table must be [seqs][table_width], got {list(self.page_table.shape)}")
+        seqs, width = self.page_table.shape
+        _kv_check(self.page_table, torch.int32, (seqs, width), "page_table")
+        _kv_check(self.kv_lens, torch.int32, (seqs,), "kv_lens")
+        _kv_check(self.q_starts, torch.int32, (seqs + 1,), "q_starts")
+        for name in ("kv_lens", "q_starts"):
+            if getattr(self, name).device != self.page_table.device:
+                raise ValueError(f"{name} is on {getattr(self, name).device}, "
+                                 f"page_table on {self.page_table.device}")
+        for name in ("max_q", "max_kv"):
+            if not 0 <= getattr(self, name) < 1 << 31:
+                raise ValueError(f"{name} must be in [0, 2^31), got {getattr(self, name)}")
+        ptr = [_dev(getattr(self, n), torch.int32, n) for n in ("page_table", "kv_lens", "q_starts")]
+        object.__setattr__(self, "_args", (*ptr, seqs, width))
+
+    def _c(self, rows: int) -> CKvBatch:
+        return CKvBatch(*self._args, rows, self.max_q, self.max_kv)
+
+
+def _rows(t: torch.Tensor, heads: int | None, like: torch.Tensor, cache: KvCache, name: str):
+    """(address, elements from row to row) of rows [rows][heads][head_dim] that may be
+    a slice of wider rows."""
+    if t.dim() != 3 or t.shape[2] != cache._c.head_dim or (heads is not None and t.shape[1] != heads) or \
+            t.shape[0] != like.shape[0]:
+        raise ValueError(f"{name} must be [{like.shape[0]}][{'heads' if heads is None else heads}]"
+                         f"[{cache._c.head_dim}], got {list(t.shape)}")
+    if t.dtype not in ROW_TYPES or t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {'fp16 or bf16' if t is like else like.dtype}, got {t.dtype}")
+    if t.device != cache.k.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
+    rows, width = t.shape[0], t.shape[1] * t.shape[2]
+    s = t.stride()
+    if s[2] != 1 or (t.shape[1] > 1 and s[1] != t.shape[2]):
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows > 1 and not 0 <= s[0] < 1 << 31:
+        raise ValueError(f"{name}: rows too far apart")
+    return t.data_ptr(), s[0] if rows > 1 else width
+
+
+def _kv_call(device: torch.device, stream, call):
+    """call(stream address) with ``device`` current, on ``stream`` or the device's
+    current one."""
+    if device.index == torch.cuda.current_device():
+        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+
+
+def _on(batch: KvBatch, cache: KvCache):
+    if batch.page_table.device != cache.k.device:
+        raise ValueError(f"the batch is on {batch.page_table.device}, the cache on {cache.k.device}")
+
+
+def _heads(q: torch.Tensor, cache: KvCache) -> int:
+    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache._c.kv_heads:
+        raise ValueError(f"q must be [rows][heads][{cache._c.head_dim}] with a multiple of "
+                         f"{cache._c.kv_heads} heads, got {list(q.shape)}")
+    return q.shape[1]
+
+
+def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatch,
+              rope: torch.Tensor | None = None, interleaved: bool = False,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Rotates the rows' queries and keys by their positions and writes the keys and
+    values into the cache.  q [rows][q_heads][head_dim] (or None), k and v
+    [rows][kv_heads][head_dim], fp16 or bf16, rows at any stride; rope fp32
+    [positions][rot_dim] (cosines, then sines) or None.  Returns the rotated q."""
+    _on(batch, cache)
+    kp, ks = _rows(k, cache._c.kv_heads, k, cache, "k")
+    vp, vs = _rows(v, cache._c.kv_heads, k, cache, "v")
+    qp = op = None
+    qs, heads = 0, cache._c.kv_heads
+    if q is not None:
+        heads = _heads(q, cache)
+        qp, qs = _rows(q, heads, k, cache, "q")
+        if out is None:
+            out = _new(tuple(q.shape), q.dtype, q.device, stream)
+        elif tuple(out.shape) != tuple(q.shape) or out.device != q.device:
+            raise ValueError(f"out must be {list(q.shape)} on {q.device}, got {list(out.shape)} on {out.device}")
+        op = _dev(out, q.dtype, "out")
+    rp, positions, rot = None, 0, 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.device != k.device:
+            raise ValueError(f"rope must be [positions][rot_dim] on {k.device}, got {list(rope.shape)} on {rope.device}")
+        rp = _dev(rope, torch.float32, "rope")
+        positions, rot = rope.shape
+    b = batch._c(k.shape[0])
+    _kv_call(k.device, stream, lambda s: load().awq_kv_append(
+        qp, qs, kp, ks, vp, vs, op, heads, ROW_TYPES[k.dtype], rp, positions, rot, int(interleaved),
+        cache._c, b, s))
+    return out
+
+
+def attention_workspace_bytes(rows: int, q_heads: int, cache: KvCache, batch: KvBatch, window: int = 0,
+                              sinks: int = 0) -> int:
+    return load().awq_attention_workspace_bytes(q_heads, window, sinks, cache._c, batch._c(rows))
+
+
+def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | None = None,
+              window: int = 0, sinks: int = 0, out: torch.Tensor | None = None, stream=None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the rows q [rows][q_heads][head_dim] over the cache, which holds
+    their own keys and values already: causal, and with ``window`` > 0 only over the
+    last ``window`` tokens and the first ``sinks``.  scale: 1 / sqrt(head_dim) unless
+    given.  The workspace is allocated here unless one is given."""
+    _on(batch, cache)
+    heads = _heads(q, cache)
+    qp, qs = _rows(q, heads, q, cache, "q")
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError(f"window and sinks must be in [0, 2^31), got {window}, {sinks}")
+    if out is None:
+        out = _new(tuple(q.shape), q.dtype, q.device, stream)
+    elif tuple(out.shape) != tuple(q.shape) or out.device != q.device:
+        raise ValueError(f"out must be {list(q.shape)} on {q.device}, got {list(out.shape)} on {out.device}")
+    op = _dev(out, q.dtype, "out")
+    lib = load()
+    b = batch._c(q.shape[0])
+    if workspace is None:
+        nbytes = lib.awq_attention_workspace_bytes(heads, window, sinks, cache._c, b)
+        if nbytes:
+            workspace = _new(nbytes, torch.uint8, q.device, stream)
+    wp, wn = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    scale = cache._c.head_dim ** -0.5 if scale is None else scale
+    _kv_call(q.device, stream, lambda s: lib.awq_attention(
+        qp, qs, op, heads, ROW_TYPES[q.dtype], scale, window, sinks, cache._c, b, wp, wn, s))
+    return out

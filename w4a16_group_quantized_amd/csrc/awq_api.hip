@@ -9,11 +9,13 @@
 #include <stdlib.h>
 
 #include "awq_internal.h"
+#include "awq_kv.h"
 
 namespace {
 
 constexpr long long kMaxElems = (1LL << 31) - 1;
 constexpr int kMaxSplits = 16;
+constexpr long long kMaxTokens = 1LL << 30;   // of one sequence in the paged cache
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -83,6 +85,54 @@ awq_status check_calibration(const uint16_t *x, int32_t M, const uint16_t *w, in
         return AWQ_ERROR_SHAPE;
     if (!aligned16(x) || !aligned16(w)) return AWQ_ERROR_ALIGNMENT;
     return AWQ_SUCCESS;
+}
+
+// The paged cache and the batch of the attention calls.
+awq_status check_kv(const awq_kv_cache *c, const awq_kv_batch *b) {
+    if (c == nullptr || b == nullptr) return AWQ_ERROR_INVALID_VALUE;
+    if (c->k == nullptr || c->v == nullptr || c->k_scales == nullptr || c->v_scales == nullptr ||
+        (b->seqs > 0 && (b->page_table == nullptr || b->kv_lens == nullptr || b->q_starts == nullptr)))
+        return AWQ_ERROR_INVALID_VALUE;
+    if (c->pages <= 0 || c->page_size <= 0 || c->kv_heads <= 0 || c->head_dim <= 0 || b->seqs < 0 ||
+        b->rows < 0 || b->table_width <= 0 || b->max_q < 0 || b->max_kv < 0)
+        return AWQ_ERROR_INVALID_VALUE;
+    if (c->page_size & (c->page_size - 1) || c->page_size < 16 || c->page_size > 256)
+        return AWQ_ERROR_SHAPE;
+    if (c->kv_heads > 65535 || b->seqs > 65535) return AWQ_ERROR_SHAPE;   // grid dimensions
+    if ((long long)c->pages * c->kv_heads > kMaxElems || (long long)b->seqs * b->table_width > kMaxElems)
+        return AWQ_ERROR_SHAPE;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scales) || !aligned16(c->v_scales) ||
+        !aligned16(b->page_table) || !aligned16(b->kv_lens) || !aligned16(b->q_starts))
+        return AWQ_ERROR_ALIGNMENT;
+    if ((long long)b->table_width * c->page_size > kMaxTokens) return AWQ_ERROR_SHAPE;
+    if (!awq::kv_head_dim_supported(c->head_dim)) return AWQ_ERROR_UNSUPPORTED;
+    return AWQ_SUCCESS;
+}
+
+// Rows [rows][heads][dim] of 16-bit values, `stride` elements from row to row.
+awq_status check_rows(const uint16_t *p, long long rows, int32_t stride, int32_t heads, int32_t dim) {
+    if (p == nullptr || heads <= 0) return AWQ_ERROR_INVALID_VALUE;
+    const long long width = (long long)heads * dim;
+    if (stride < width || stride % 8 || rows * width > kMaxElems) return AWQ_ERROR_SHAPE;
+    if (!aligned16(p)) return AWQ_ERROR_ALIGNMENT;
+    return AWQ_SUCCESS;
+}
+
+awq::KvView kv_view(const awq_kv_cache *c, const awq_kv_batch *b) {
+    int log2_page = 0;
+    while ((1 << log2_page) < c->page_size) ++log2_page;
+    return awq::KvView{c->k, c->v, c->k_scales, c->v_scales, b->page_table, b->kv_lens, b->q_starts,
+                       c->pages, log2_page, c->kv_heads, b->seqs, b->table_width, b->rows};
+}
+
+bool known_type(int32_t t) { return t == AWQ_TYPE_FP16 || t == AWQ_TYPE_BF16; }
+
+// The largest row and token counts of a sequence as they size a grid: within
+// what the arrays can hold.
+int grid_rows(const awq_kv_batch *b) { return b->max_q < 1 ? 1 : b->max_q < b->rows ? b->max_q : b->rows > 0 ? b->rows : 1; }
+int grid_keys(const awq_kv_cache *c, const awq_kv_batch *b) {
+    const long long cap = (long long)b->table_width * c->page_size;
+    return b->max_kv < 1 ? 1 : b->max_kv < cap ? b->max_kv : (int)cap;
 }
 
 }  // namespace
@@ -307,6 +357,65 @@ awq_status awq_scale_search(const uint16_t *x, int32_t M, const uint16_t *w, int
     return done(stream, awq::launch_scale_search(x, M, w, K, N, group_size, symmetric != 0, alphas,
                                              n_alpha, losses, best, best_scales, workspace,
                                              as_stream(stream)));
+}
+
+awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                         const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
+                         int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                         int32_t interleaved, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                         void *stream) {
+    awq_status st = check_kv(cache, batch);
+    if (st != AWQ_SUCCESS) return st;
+    if (!known_type(type) || rot_dim < 0 || q_heads <= 0) return AWQ_ERROR_INVALID_VALUE;
+    if (q_heads % cache->kv_heads || rot_dim % 16 || rot_dim > cache->head_dim) return AWQ_ERROR_SHAPE;
+    if (rot_dim > 0) {
+        if (rope == nullptr || rope_positions <= 0) return AWQ_ERROR_INVALID_VALUE;
+        if (!aligned16(rope)) return AWQ_ERROR_ALIGNMENT;
+    }
+    if (batch->seqs == 0 || batch->rows == 0) return AWQ_SUCCESS;
+    st = check_rows(k, batch->rows, k_stride, cache->kv_heads, cache->head_dim);
+    if (st == AWQ_SUCCESS) st = check_rows(v, batch->rows, v_stride, cache->kv_heads, cache->head_dim);
+    if (st == AWQ_SUCCESS && (q == nullptr) != (q_out == nullptr)) st = AWQ_ERROR_INVALID_VALUE;
+    if (st == AWQ_SUCCESS && q != nullptr)
+        st = check_rows(q, batch->rows, q_stride, q_heads, cache->head_dim);
+    if (st == AWQ_SUCCESS && q_out != nullptr && !aligned16(q_out)) st = AWQ_ERROR_ALIGNMENT;
+    if (st != AWQ_SUCCESS) return st;
+    return done(stream, awq::launch_kv_append(kv_view(cache, batch), cache->head_dim, q, q_stride, k,
+                                              k_stride, v, v_stride, q_out, q_heads, rope,
+                                              rope_positions, rot_dim, interleaved != 0,
+                                              type == AWQ_TYPE_BF16, grid_rows(batch), as_stream(stream)));
+}
+
+size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
+                                     const awq_kv_cache *cache, const awq_kv_batch *batch) {
+    if (check_kv(cache, batch) != AWQ_SUCCESS || q_heads <= 0 || q_heads % cache->kv_heads || window < 0 ||
+        sinks < 0 || batch->seqs == 0 || batch->rows == 0)
+        return 0;
+    return awq::attention_workspace(batch->seqs, batch->rows, q_heads, cache->kv_heads, cache->head_dim,
+                                    grid_rows(batch), grid_keys(cache, batch), window, sinks);
+}
+
+awq_status awq_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
+                         int32_t type, float scale, int32_t window, int32_t sinks,
+                         const awq_kv_cache *cache, const awq_kv_batch *batch, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    awq_status st = check_kv(cache, batch);
+    if (st != AWQ_SUCCESS) return st;
+    if (!known_type(type) || !isfinite(scale) || window < 0 || sinks < 0 || q_heads <= 0)
+        return AWQ_ERROR_INVALID_VALUE;
+    if (q_heads % cache->kv_heads) return AWQ_ERROR_SHAPE;
+    if (batch->seqs == 0 || batch->rows == 0) return AWQ_SUCCESS;
+    st = check_rows(q, batch->rows, q_stride, q_heads, cache->head_dim);
+    if (st == AWQ_SUCCESS && out == nullptr) st = AWQ_ERROR_INVALID_VALUE;
+    if (st == AWQ_SUCCESS && !aligned16(out)) st = AWQ_ERROR_ALIGNMENT;
+    if (st != AWQ_SUCCESS) return st;
+    const size_t need = awq_attention_workspace_bytes(q_heads, window, sinks, cache, batch);
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
+        return AWQ_ERROR_WORKSPACE;
+    return done(stream, awq::launch_attention(kv_view(cache, batch), cache->head_dim, q, q_stride, out,
+                                              q_heads, type == AWQ_TYPE_BF16, scale, window, sinks,
+                                              grid_rows(batch), grid_keys(cache, batch), workspace,
+                                              as_stream(stream)));
 }
 
 }  // extern "C"

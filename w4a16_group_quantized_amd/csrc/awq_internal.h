@@ -65,4 +65,19 @@ hipError_t launch_scale_search(const uint16_t *x, int M, const uint16_t *w, int 
                                bool symmetric, const float *alphas, int n_alpha, double *losses,
                                int32_t *best, float *best_scales, void *workspace, hipStream_t s);
 
+// 8-bit paged key/value cache (KvView: awq_kv.h).  max_q, max_kv: the largest
+// row and token counts of a sequence, which size the grids.
+struct KvView;
+bool kv_head_dim_supported(int head_dim);
+hipError_t launch_kv_append(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
+                            const uint16_t *k, long long k_stride, const uint16_t *v,
+                            long long v_stride, uint16_t *q_out, int q_heads, const float *rope,
+                            int rope_positions, int rot, bool adjacent, bool bf16, int max_q,
+                            hipStream_t s);
+size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
+                           int max_kv, int window, int sinks);
+hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
+                            uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
+                            int max_q, int max_kv, void *workspace, hipStream_t s);
+
 }  // namespace awq
