@@ -51,12 +51,18 @@ def test_cache_refusals(call, c, want):
     (dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(starts=None), INVALID),
     (dict(seqs=-1), INVALID), (dict(rows=-1), INVALID), (dict(width=0), INVALID), (dict(max_q=-1), INVALID),
     (dict(max_kv=-1), INVALID), (dict(seqs=65536), SHAPE), (dict(seqs=65535, width=(1 << 15) + 1), SHAPE),
-    (dict(width=(1 << 24) + 1), SHAPE), (dict(rows=1 << 23), SHAPE),
+(dict(width=(1 << 24) + 1), SHAPE), (dict(rows=1 << 23), SHAPE),
     (dict(table=MISALIGNED), ALIGN), (dict(lens=MISALIGNED), ALIGN), (dict(starts=MISALIGNED), ALIGN),
     (dict(seqs=0, table=None, lens=None, starts=None), 0), (dict(rows=0), 0),        # nothing to do
 ])
 def test_batch_refusals(call, b, want):
     assert call(b=batch(**b)) == want
+
+
+@pytest.mark.parametrize("call", [append, attention])
+def test_too_many_sequences_and_heads(call):
+    wide = dict(qs=512 * 128, ks=512 * 128, vs=512 * 128) if call is append else dict(qs=512 * 128)
+    assert call(c=cache(heads=512), b=batch(seqs=1 << 15), heads=512, **wide) == SHAPE
 
 
 def test_null_views():

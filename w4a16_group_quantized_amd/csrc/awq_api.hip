@@ -98,7 +98,9 @@ awq_status check_kv(const awq_kv_cache *c, const awq_kv_batch *b) {
         return AWQ_ERROR_INVALID_VALUE;
     if (c->page_size & (c->page_size - 1) || c->page_size < 16 || c->page_size > 256)
         return AWQ_ERROR_SHAPE;
-    if (c->kv_heads > 65535 || b->seqs > 65535) return AWQ_ERROR_SHAPE;   // grid dimensions
+    // grid dimensions
+    if (c->kv_heads > 65535 || b->seqs > 65535 || (long long)c->kv_heads * b->seqs >= 1 << 24)
+        return AWQ_ERROR_SHAPE;
     if ((long long)c->pages * c->kv_heads > kMaxElems || (long long)b->seqs * b->table_width > kMaxElems)
         return AWQ_ERROR_SHAPE;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scales) || !aligned16(c->v_scales) ||

@@ -1,0 +1,63 @@
+// Shared by the attention kernels (awq_attention*.hip): arguments, the tiles of
+// keys that rows see, and queries as matrix operands.
+#pragma once
+
+#include "awq_kv.h"
+
+namespace awq {
+
+constexpr int kTile = 64;                  // keys of a tile
+constexpr float kEmpty = -1e30f;           // running maximum of a row that has seen no key
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttnArgs {
+    KvView c;
+    const uint16_t *q;
+    long long q_stride;
+    uint16_t *out;
+    float *part;             // partial results, or null with one chunk
+    int q_heads, group;
+    float scale;             // scale * log2(e)
+    int window, sinks;
+    int splits, chunk;       // chunks of a row tile, and their least length in tiles
+};
+
+// The 64-key tiles that rows at positions lo .. hi see: tiles [0, a) that hold
+// the first tokens and [b, e) that hold the window.
+struct Tiles {
+    int a, b, e;
+    __device__ __forceinline__ int count() const { return a + e - b; }
+    __device__ __forceinline__ int at(int i) const { return i < a ? i : b + i - a; }
+};
+__device__ __forceinline__ Tiles visible_tiles(const AttnArgs &p, int lo, int hi, int len) {
+    Tiles t;
+    const int end = min(hi + 1, len);
+    t.e = end > 0 ? (end + kTile - 1) / kTile : 0;
+    t.b = p.window > 0 ? min(max(lo - p.window + 1, 0) / kTile, t.e) : 0;
+    t.a = p.window > 0 ? min((min(p.sinks, end > 0 ? end : 0) + kTile - 1) / kTile, t.b) : 0;
+    return t;
+}
+
+template <typename T>
+__device__ __forceinline__ half8_t as_row_half(const uint16_t *p, float f) {
+    float x[8];
+    load8<T>(p, x);
+    half8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (half_t)(x[i] * f);
+    return h;
+}
+
+// Four masks of four bytes each: the first `live` of sixteen bytes.
+__device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int n = live - 4 * e;
+        keep[e] = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+    }
+}
+
+// Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
+hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s);
+
+}  // namespace awq

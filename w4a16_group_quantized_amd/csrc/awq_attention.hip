@@ -26,56 +26,15 @@
 // where there is more than one chunk.
 #include <algorithm>
 
+#include "awq_attention.h"
 #include "awq_internal.h"
-#include "awq_kv.h"
 
 namespace awq {
 namespace {
 
-constexpr int kTile = 64;                  // keys of a tile
 constexpr int kRows = 16;                  // rows of a workgroup
 constexpr int kWaves = 4;
-constexpr float kEmpty = -1e30f;           // running maximum of a row that has seen no key
 constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of the formula
-constexpr float kLog2e = 1.44269504088896340736f;
-
-struct AttnArgs {
-    KvView c;
-    const uint16_t *q;
-    long long q_stride;
-    uint16_t *out;
-    float *part;             // partial results, or null with one chunk
-    int q_heads, group;
-    float scale;             // scale * log2(e)
-    int window, sinks;
-    int splits, chunk;       // chunks of a row tile, and their least length in tiles
-};
-
-// The 64-key tiles that rows at positions lo .. hi see: tiles [0, a) that hold
-// the first tokens and [b, e) that hold the window.
-struct Tiles {
-    int a, b, e;
-    __device__ __forceinline__ int count() const { return a + e - b; }
-    __device__ __forceinline__ int at(int i) const { return i < a ? i : b + i - a; }
-};
-__device__ __forceinline__ Tiles visible_tiles(const AttnArgs &p, int lo, int hi, int len) {
-    Tiles t;
-    const int end = min(hi + 1, len);
-    t.e = end > 0 ? (end + kTile - 1) / kTile : 0;
-    t.b = p.window > 0 ? min(max(lo - p.window + 1, 0) / kTile, t.e) : 0;
-    t.a = p.window > 0 ? min((min(p.sinks, end > 0 ? end : 0) + kTile - 1) / kTile, t.b) : 0;
-    return t;
-}
-
-template <typename T>
-__device__ __forceinline__ half8_t as_row_half(const uint16_t *p, float f) {
-    float x[8];
-    load8<T>(p, x);
-    half8_t h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (half_t)(x[i] * f);
-    return h;
-}
 
 // A partial result: D outputs, then the maximum and the sum.
 template <int D>
@@ -191,11 +150,7 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
                 }
                 // codes of slots that hold no token may be anything, NaN among it
                 uint32_t keep[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = live - 4 * e;
-                    keep[e] = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-                }
+                live_bytes(live, keep);
 #pragma unroll
                 for (int t = 0; t < kT; ++t) {
                     vc[t].x &= keep[0];
@@ -381,8 +336,13 @@ hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, int max_q, hipSt
 
 }  // namespace
 
+// Rows of a sequence and kv head from which the prompt kernel takes the call.
+constexpr int kPrefillRows = 128;
+bool prefill_rows(int group, int max_q) { return (long long)max_q * group >= kPrefillRows; }
+
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
                            int max_kv, int window, int sinks) {
+    if (prefill_rows(q_heads / kv_heads, max_q)) return 0;
     const Plan pl = plan(seqs, kv_heads, q_heads / kv_heads, max_q, max_kv, window, sinks);
     if (pl.splits == 1) return 0;
     return (size_t)rows * q_heads * pl.splits * (head_dim + 4) * sizeof(float);
@@ -394,6 +354,7 @@ hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, lo
     const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, max_q, max_kv, window, sinks);
     AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
                q_heads / c.kv_heads, scale * kLog2e, window, sinks, pl.splits, pl.chunk};
+    if (prefill_rows(p.group, max_q)) return launch_attention_prefill(p, head_dim, bf16, max_q, s);
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, max_q, s) : launch_dim<half_t>(p, head_dim, pl, max_q, s);
 }
 

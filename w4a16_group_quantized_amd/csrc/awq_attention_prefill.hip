@@ -1,0 +1,317 @@
+// awq_attention for many rows (prompts, chunks of prompts): see
+// awq_attention.hip for the formula and the transposed products.
+//
+// A workgroup of four waves takes 128 rows (row r of a kv head: token r / group,
+// head r % group) of one kv head and one sequence, 32 to a wave, and goes once
+// over the keys in tiles of 64, held in LDS as codes: 64 D bytes of keys and as
+// many of values, loaded straight into LDS, the next tile while this one is
+// multiplied (two buffers, one barrier a tile).  Products are
+// v_mfma_f32_32x32x16_f16: S^T = K Q^T leaves a lane with one row and 32 scores,
+// O^T = V^T P^T takes them as they lie.  LDS row m of a half tile holds key
+// 16 (m / 4 % 2) + 4 (m / 8) + m % 4, so that lane half hf ends up with the
+// sixteen consecutive keys 16 hf .. 16 hf + 15 of it, one 16-byte piece of a row
+// of V^T.  Pieces are stored xor-swizzled by their row: no bank conflicts.
+//
+// Weights are rounded to fp16 once; the sum takes them before the rounding.
+// They are scaled by 2^11 so that small ones stay normal numbers, and the
+// maximum that they refer to is moved only when a row exceeds it by 2^4, so the
+// largest is 2^15, and rescaling the outputs is rare after the first tiles.
+#include <algorithm>
+
+#include "awq_attention.h"
+#include "awq_internal.h"
+
+namespace awq {
+namespace {
+
+constexpr int kRows = 128, kWaveRows = 32, kWaves = 4;
+constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+// A barrier that waits for no load in flight.
+__device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
+__device__ __forceinline__ void to_lds16(const void *src, uint4 *dst) {
+    __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+}
+// The lane's value and that of its partner in the other half of the wave, the
+// lower half's first.  (The elements go through variables of their own: a bit
+// cast straight from an element of the result takes element 0.)
+__device__ __forceinline__ float2 halves(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float half_max(float x) {
+    const float2 v = halves(x);
+    return fmaxf(v.x, v.y);
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const float2 v = halves(x);
+    return v.x + v.y;
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// LDS piece of (row, 16-byte piece), C pieces a row.
+template <int C>
+__device__ __forceinline__ int piece(int row, int at) {
+    return row * C + (C >= 8 ? at ^ (row & 7) : at ^ ((row >> 1) & 3));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(AttnArgs p) {
+    constexpr int kC = D / 16;                 // pieces of a key
+    constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
+    constexpr int kLoads = D / 64;             // loads of a wave for the keys of a tile, and for the values
+    __shared__ uint4 kbuf0[kTile * kC], vbuf0[kTile * kC], kbuf1[kTile * kC], vbuf1[kTile * kC];
+    const KvView &c = p.c;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m = lane & 31, hf = lane >> 5;
+    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
+    const Seq s = load_seq(c, b);
+    const int P = 1 << c.log2_page;
+    const int total = s.n * p.group;
+    const int row_tiles = (total + kRows - 1) / kRows;
+    const int32_t *table = c.page_table + (long long)b * c.table_width;
+    const int gv = (lane & 3) ^ ((lane >> 3) & 3);         // sixteen-key group whose values this lane loads
+    const long long slab = (long long)P * D;
+
+    // the longest rows first
+    for (int rt = row_tiles - 1 - (int)blockIdx.y; rt >= 0; rt -= gridDim.y) {
+        const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
+        const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
+        const int count = tiles.count();
+        // the wave's rows, and the lane's
+        const int w0 = min(r0 + wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
+        const bool idle = r0 + wave * kWaveRows > r1;
+        const int lo = s.first() + w0 / p.group, hi = s.first() + w1 / p.group;
+        const int r = min(w0 + m, r1);
+        const int token = r / p.group, head = h * p.group + r % p.group;
+        const int pos = s.first() + token;
+        const uint16_t *qrow = p.q + (long long)(s.row0 + token) * p.q_stride + head * D + 16 * hf;
+        float up = p.scale < 0.0f ? -1.0f : 1.0f, down = fabsf(p.scale);
+        if constexpr (!__is_same(T, half_t)) {
+            float big = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[8];
+                    load8<T>(qrow + 32 * i + 8 * e, x);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) big = fmaxf(big, fabsf(x[u]));
+                }
+            big = half_max(big);
+            const int e = min(max((int)(__builtin_bit_cast(uint32_t, big) >> 23) - 127, -100), 126);
+            up *= pow2(min(14 - e, 127));
+            down *= pow2(max(e - 14, -126));
+        }
+        half8_t qf[kP][2];
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qf[i][e] = as_row_half<T>(qrow + 32 * i + 8 * e, up);
+
+        float mx = kEmpty, l = 0.0f, unit = 1.0f;
+        float16_t o[kP];
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = float16_t{};
+
+        // Page numbers run two tiles ahead and scales one, a sixteen-key group to a lane
+        // (group g in lane g): page_of() asks, issue() loads a tile's codes and scales.
+        int next_id = 0;
+        float ks_l = 1.0f, vs_l = 0.0f;
+        uint64_t has = 0;
+        auto page_of = [&](int i) {
+            const int j = tiles.at(min(i, count - 1)) * kTile + 16 * gv;
+            return j < s.len ? table[j >> c.log2_page] : -1;
+        };
+        auto issue = [&](int i, uint4 *kb, uint4 *vb) {
+            const int j0 = tiles.at(i) * kTile;
+            const bool ok = (uint32_t)next_id < (uint32_t)c.pages;
+            const int id = ok ? next_id : 0;
+            has = __ballot(ok);
+            const long long ph = (long long)id * c.kv_heads + h;
+            ks_l = c.k_scales[ph];
+            vs_l = c.v_scales[ph];
+            if (!ok) {
+                ks_l = 1.0f;
+                vs_l = 0.0f;
+            }
+            const int in_page = j0 & (P - 1);
+            const int id0 = __builtin_amdgcn_readlane(id, wave & 2), id1 = __builtin_amdgcn_readlane(id, (wave & 2) + 1);
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
+                const int at = (wave * kLoads + n) * 64 + lane;        // piece of the tile
+                const int row = at / kC, mm = row & 31;
+                const int key = (row & 32) + 16 * ((mm >> 2) & 1) + 4 * (mm >> 3) + (mm & 3);
+                const int pc = kC >= 8 ? (at % kC) ^ (row & 7) : (at % kC) ^ ((row >> 1) & 3);
+                const long long page = ((long long)(((mm >> 2) & 1) ? id1 : id0) * c.kv_heads + h) * slab;
+                to_lds16(c.k + page + (in_page + (key & (P - 1))) * D + 16 * pc, kb + (wave * kLoads + n) * 64);
+            }
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
+                const int d = (wave * kLoads + n) * 16 + (lane >> 2);
+                to_lds16(c.v + ph * slab + d * P + in_page + ((16 * gv) & (P - 1)), vb + (wave * kLoads + n) * 64);
+            }
+        };
+
+        auto multiply = [&](int i, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
+            const int j0 = tiles.at(i) * kTile;
+            if (idle || j0 > hi) return;
+            float16_t acc[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                acc[u] = float16_t{};
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    const uint4 k = kb[piece<kC>(32 * u + m, 2 * e + hf)];
+                    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(k.x, k.y), qf[e][0], acc[u], 0, 0, 0);
+                    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(k.z, k.w), qf[e][1], acc[u], 0, 0, 0);
+                }
+            }
+            const bool whole = (ok & 15) == 15 && j0 + kTile <= lo + 1 &&
+                               (p.window <= 0 || j0 > hi - p.window || j0 + kTile <= p.sinks);
+            uint32_t keep[2][4];
+            if (!whole) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int jg = j0 + 32 * u + 16 * hf;
+                    const int live = (ok >> (2 * u + hf)) & 1 ? min(max(s.len - jg, 0), 16) : 0;
+                    live_bytes(live, keep[u]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = jg + e;
+                        const bool see = e < live && j <= pos && (p.window <= 0 || j > pos - p.window || j < p.sinks);
+                        acc[u][e] = see ? acc[u][e] : -__builtin_inff();
+                    }
+                }
+            }
+            float ks[2], top[2], vs[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float a = lane_value(ksl, 2 * u), d = lane_value(ksl, 2 * u + 1);
+                // never 0, which would turn a hidden key's -inf into NaN
+                ks[u] = fmaxf((hf ? d : a) * down, 0x1p-126f);
+                float t = acc[u][0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e) t = fmaxf(t, acc[u][e]);
+                top[u] = t * ks[u];
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) vs[g] = lane_value(vsl, g);
+            float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+            if (!(vmax > 0.0f)) vmax = unit;
+            const float now = half_max(fmaxf(top[0], top[1]));
+            if (__any(now > mx + kSlack) || vmax != unit) {
+                const float to = fmaxf(mx, now);
+                const float alpha = __builtin_amdgcn_exp2f(mx - to);
+                const float turn = alpha * (unit / vmax);
+                mx = to;
+                l *= alpha;
+                unit = vmax;
+#pragma unroll
+                for (int e = 0; e < kP; ++e) o[e] *= turn;
+            }
+            const float base = kWeightBits - mx;
+            half8_t w[2][2];
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    acc[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                    sum[u] += acc[u][e];
+                }
+            l += sum[0] + sum[1];
+            if (!(vs[0] == vmax && vs[1] == vmax && vs[2] == vmax && vs[3] == vmax)) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) acc[u] *= (hf ? vs[2 * u + 1] : vs[2 * u]) / vmax;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[u][e >> 3][e & 7] = (half_t)acc[u][e];
+#pragma unroll
+            for (int e = 0; e < kP; ++e)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint4 v = vb[piece<4>(32 * e + m, 2 * u + hf)];
+                    if (!whole) {
+                        v.x &= keep[u][0];
+                        v.y &= keep[u][1];
+                        v.z &= keep[u][2];
+                        v.w &= keep[u][3];
+                    }
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(v.x, v.y), w[u][0], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(v.z, v.w), w[u][1], o[e], 0, 0, 0);
+                }
+        };
+
+        if (count > 0) {
+            next_id = page_of(0);
+            issue(0, kbuf0, vbuf0);
+            next_id = page_of(1);
+            auto step = [&](int i, const uint4 *kb, const uint4 *vb, uint4 *kn, uint4 *vn) {
+                // this wave's loads of tile i are in LDS, its reads of tile i - 1 done
+                __builtin_amdgcn_s_waitcnt(0xC07F);
+                wait_vmcnt<0>();
+                barrier_no_fence();            // everyone's are, and tile i - 1 is done with
+                const float ksl = ks_l, vsl = vs_l;
+                const uint64_t ok = has;
+                if (i + 1 < count) {
+                    issue(i + 1, kn, vn);
+                    next_id = page_of(i + 2);
+                }
+                multiply(i, kb, vb, ksl, vsl, ok);
+            };
+            for (int i = 0; i < count; i += 2) {
+                step(i, kbuf0, vbuf0, kbuf1, vbuf1);
+                if (i + 1 < count) step(i + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+            }
+        }
+        l = half_sum(l);
+        if (!idle && w0 + m <= r1) {
+            const float inv = l > 0.0f || !(l == l) ? unit / l : 0.0f;
+            uint16_t *dst = p.out + ((long long)(s.row0 + token) * p.q_heads + head) * D + 4 * hf;
+#pragma unroll
+            for (int e = 0; e < kP; ++e)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint2 y;
+                    y.x = (uint32_t)from_float<T>(o[e][4 * u] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 1] * inv) << 16);
+                    y.y = (uint32_t)from_float<T>(o[e][4 * u + 2] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 3] * inv) << 16);
+                    *reinterpret_cast<uint2 *>(dst + 32 * e + 8 * u) = y;
+                }
+        }
+        __syncthreads();                       // the buffers are free again
+    }
+}
+
+template <typename T>
+hipError_t launch_dim(const AttnArgs &p, int D, const dim3 &grid, hipStream_t s) {
+    switch (D) {
+    case 64: prefill_kernel<T, 64><<<grid, 64 * kWaves, 0, s>>>(p); break;
+    case 128: prefill_kernel<T, 128><<<grid, 64 * kWaves, 0, s>>>(p); break;
+    case 256: prefill_kernel<T, 256><<<grid, 64 * kWaves, 0, s>>>(p); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s) {
+    // (sequence, kv head) fastest: with a multiple of eight of them, the row tiles that read
+    // the same keys meet in one XCD's cache.  The kernel steps on where the grid is cut.
+    const long long tiles = ((long long)max_q * p.group + kRows - 1) / kRows;
+    const dim3 grid(p.c.kv_heads * p.c.seqs, (unsigned)std::min<long long>(tiles, 65535));
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, s) : launch_dim<half_t>(p, head_dim, grid, s);
+}
+
+}  // namespace awq

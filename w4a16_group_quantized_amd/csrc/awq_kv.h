@@ -56,10 +56,8 @@ __device__ __forceinline__ uint16_t from_float<half_t>(float f) {
     return as_u16((half_t)f);
 }
 template <>
-__device__ __forceinline__ uint16_t from_float<bhalf_t>(float f) {   // nearest, ties to even
-    const uint32_t u = __builtin_bit_cast(uint32_t, f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+__device__ __forceinline__ uint16_t from_float<bhalf_t>(float f) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
 template <typename T>
