@@ -53,6 +53,13 @@ __device__ __forceinline__ float half_sum(float x) {
     const float2 v = halves(x);
     return v.x + v.y;
 }
+// The largest of three (NaN only if all are), without the instructions that the
+// compiler puts before fmaxf to quiet NaNs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
 __device__ __forceinline__ float lane_value(float x, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
@@ -63,7 +70,10 @@ __device__ __forceinline__ int piece(int row, int at) {
     return row * C + (C >= 8 ? at ^ (row & 7) : at ^ ((row >> 1) & 3));
 }
 
-template <typename T, int D>
+// BIG: pages of at least a tile, so that a tile's page and scales are the same for
+// all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
+// instructions a tile less).
+template <typename T, int D, bool BIG>
 __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(AttnArgs p) {
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
@@ -80,6 +90,20 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     const int32_t *table = c.page_table + (long long)b * c.table_width;
     const int gv = (lane & 3) ^ ((lane >> 3) & 3);         // sixteen-key group whose values this lane loads
     const long long slab = (long long)P * D;
+
+    // where this lane's pieces of a tile lie in its page or pages, and which of the wave's two
+    // sixteen-key groups the keys' are of
+    uint32_t koff[kLoads], voff[kLoads];
+    bool kodd[kLoads];
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+        const int at = (wave * kLoads + n) * 64 + lane, row = at / kC, mm = row & 31;
+        const int key = (row & 32) + 16 * ((mm >> 2) & 1) + 4 * (mm >> 3) + (mm & 3);
+        const int pc = kC >= 8 ? (at % kC) ^ (row & 7) : (at % kC) ^ ((row >> 1) & 3);
+        koff[n] = (key & (P - 1)) * D + 16 * pc;
+        kodd[n] = (mm >> 2) & 1;
+        voff[n] = ((wave * kLoads + n) * 16 + (lane >> 2)) * P + ((16 * gv) & (P - 1));
+    }
 
     // the longest rows first
     for (int rt = row_tiles - 1 - (int)blockIdx.y; rt >= 0; rt -= gridDim.y) {
@@ -128,66 +152,85 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
         float ks_l = 1.0f, vs_l = 0.0f;
         uint64_t has = 0;
         auto page_of = [&](int i) {
-            const int j = tiles.at(min(i, count - 1)) * kTile + 16 * gv;
+            const int j = tiles.at(min(i, count - 1)) * kTile + (BIG ? 0 : 16 * gv);
             return j < s.len ? table[j >> c.log2_page] : -1;
         };
         auto issue = [&](int i, uint4 *kb, uint4 *vb) {
             const int j0 = tiles.at(i) * kTile;
-            const bool ok = (uint32_t)next_id < (uint32_t)c.pages;
-            const int id = ok ? next_id : 0;
-            has = __ballot(ok);
+            const int want = BIG ? __builtin_amdgcn_readfirstlane(next_id) : next_id;
+            const bool ok = (uint32_t)want < (uint32_t)c.pages;
+            const int id = ok ? want : 0;
+            has = BIG ? (ok ? 15 : 0) : __ballot(ok);
             const long long ph = (long long)id * c.kv_heads + h;
-            ks_l = c.k_scales[ph];
-            vs_l = c.v_scales[ph];
-            if (!ok) {
-                ks_l = 1.0f;
-                vs_l = 0.0f;
-            }
+            ks_l = ok ? c.k_scales[ph] : 1.0f;
+            vs_l = ok ? c.v_scales[ph] : 0.0f;
             const int in_page = j0 & (P - 1);
+            if constexpr (BIG) {
+                const uint8_t *kp = c.k + ph * slab + in_page * D, *vp = c.v + ph * slab + in_page;
+#pragma unroll
+                for (int n = 0; n < kLoads; ++n) to_lds16(kp + koff[n], kb + (wave * kLoads + n) * 64);
+#pragma unroll
+                for (int n = 0; n < kLoads; ++n) to_lds16(vp + voff[n], vb + (wave * kLoads + n) * 64);
+                return;
+            }
             const int id0 = __builtin_amdgcn_readlane(id, wave & 2), id1 = __builtin_amdgcn_readlane(id, (wave & 2) + 1);
+            const long long page0 = ((long long)id0 * c.kv_heads + h) * slab, page1 = ((long long)id1 * c.kv_heads + h) * slab;
 #pragma unroll
-            for (int n = 0; n < kLoads; ++n) {
-                const int at = (wave * kLoads + n) * 64 + lane;        // piece of the tile
-                const int row = at / kC, mm = row & 31;
-                const int key = (row & 32) + 16 * ((mm >> 2) & 1) + 4 * (mm >> 3) + (mm & 3);
-                const int pc = kC >= 8 ? (at % kC) ^ (row & 7) : (at % kC) ^ ((row >> 1) & 3);
-                const long long page = ((long long)(((mm >> 2) & 1) ? id1 : id0) * c.kv_heads + h) * slab;
-                to_lds16(c.k + page + (in_page + (key & (P - 1))) * D + 16 * pc, kb + (wave * kLoads + n) * 64);
-            }
+            for (int n = 0; n < kLoads; ++n)
+                to_lds16(c.k + (kodd[n] ? page1 : page0) + in_page * D + koff[n], kb + (wave * kLoads + n) * 64);
 #pragma unroll
-            for (int n = 0; n < kLoads; ++n) {
-                const int d = (wave * kLoads + n) * 16 + (lane >> 2);
-                to_lds16(c.v + ph * slab + d * P + in_page + ((16 * gv) & (P - 1)), vb + (wave * kLoads + n) * 64);
-            }
+            for (int n = 0; n < kLoads; ++n)
+                to_lds16(c.v + ph * slab + in_page + voff[n], vb + (wave * kLoads + n) * 64);
         };
 
-        auto multiply = [&](int i, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
-            const int j0 = tiles.at(i) * kTile;
-            if (idle || j0 > hi) return;
-            float16_t acc[2];
+        // Codes of slots that hold no token may be anything, NaN among it: those of the values
+        // become zero before a tile that has such slots is used.
+        auto live_keys = [&](int j0, int grp, uint64_t ok) {
+            return (ok >> grp) & 1 ? min(max(s.len - j0 - 16 * grp, 0), 16) : 0;
+        };
+        auto clear_dead = [&](int j0, uint4 *vb, uint64_t ok) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                acc[u] = float16_t{};
-#pragma unroll
-                for (int e = 0; e < kP; ++e) {
-                    const uint4 k = kb[piece<kC>(32 * u + m, 2 * e + hf)];
-                    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(k.x, k.y), qf[e][0], acc[u], 0, 0, 0);
-                    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(k.z, k.w), qf[e][1], acc[u], 0, 0, 0);
-                }
+            for (int n = 0; n < kLoads; ++n) {
+                const int at = n * 64 * kWaves + threadIdx.x;
+                uint32_t keep[4];
+                live_bytes(live_keys(j0, (at & 3) ^ ((at >> 3) & 3), ok), keep);
+                uint4 v = vb[at];
+                vb[at] = make_uint4(v.x & keep[0], v.y & keep[1], v.z & keep[2], v.w & keep[3]);
             }
-            const bool whole = (ok & 15) == 15 && j0 + kTile <= lo + 1 &&
-                               (p.window <= 0 || j0 > hi - p.window || j0 + kTile <= p.sinks);
-            uint32_t keep[2][4];
-            if (!whole) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            barrier_no_fence();
+        };
+
+        auto multiply = [&](int j0, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
+            // the pieces of the next products are read while these run; the barriers keep the
+            // compiler from reading all of them at once, for which there are no registers
+            float16_t acc[2] = {};
+            uint4 k0 = kb[piece<kC>(m, hf)], k1 = kb[piece<kC>(32 + m, hf)];
+#pragma unroll
+            for (int e = 0; e < kP; ++e) {
+                const uint4 a0 = k0, a1 = k1;
+                if (e + 1 < kP) {
+                    k0 = kb[piece<kC>(m, 2 * e + 2 + hf)];
+                    k1 = kb[piece<kC>(32 + m, 2 * e + 2 + hf)];
+                }
+                acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), qf[e][0], acc[0], 0, 0, 0);
+                acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), qf[e][0], acc[1], 0, 0, 0);
+                acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), qf[e][1], acc[0], 0, 0, 0);
+                acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), qf[e][1], acc[1], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // (every row of the wave sees every key of most tiles)
+            if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
+                (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int jg = j0 + 32 * u + 16 * hf;
-                    const int live = (ok >> (2 * u + hf)) & 1 ? min(max(s.len - jg, 0), 16) : 0;
-                    live_bytes(live, keep[u]);
+                    const int live = live_keys(j0, 2 * u + hf, ok);
+                    const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int j = jg + e;
-                        const bool see = e < live && j <= pos && (p.window <= 0 || j > pos - p.window || j < p.sinks);
+                        const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
                         acc[u][e] = see ? acc[u][e] : -__builtin_inff();
                     }
                 }
@@ -195,17 +238,17 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             float ks[2], top[2], vs[4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float a = lane_value(ksl, 2 * u), d = lane_value(ksl, 2 * u + 1);
+                const float a = lane_value(ksl, 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
                 // never 0, which would turn a hidden key's -inf into NaN
                 ks[u] = fmaxf((hf ? d : a) * down, 0x1p-126f);
-                float t = acc[u][0];
+                float t = max3(acc[u][0], acc[u][1], acc[u][2]);
 #pragma unroll
-                for (int e = 1; e < 16; ++e) t = fmaxf(t, acc[u][e]);
-                top[u] = t * ks[u];
+                for (int e = 3; e < 15; e += 2) t = max3(t, acc[u][e], acc[u][e + 1]);
+                top[u] = max3(t, t, acc[u][15]) * ks[u];
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) vs[g] = lane_value(vsl, g);
-            float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+            for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = lane_value(vsl, g);
+            float vmax = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
             if (!(vmax > 0.0f)) vmax = unit;
             const float now = half_max(fmaxf(top[0], top[1]));
             if (__any(now > mx + kSlack) || vmax != unit) {
@@ -229,7 +272,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                     sum[u] += acc[u][e];
                 }
             l += sum[0] + sum[1];
-            if (!(vs[0] == vmax && vs[1] == vmax && vs[2] == vmax && vs[3] == vmax)) {
+            if (!BIG && !(vs[0] == vmax && vs[1] == vmax && vs[2] == vmax && vs[3] == vmax)) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) acc[u] *= (hf ? vs[2 * u + 1] : vs[2 * u]) / vmax;
             }
@@ -237,27 +280,27 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[u][e >> 3][e & 7] = (half_t)acc[u][e];
+            uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
 #pragma unroll
-            for (int e = 0; e < kP; ++e)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint4 v = vb[piece<4>(32 * e + m, 2 * u + hf)];
-                    if (!whole) {
-                        v.x &= keep[u][0];
-                        v.y &= keep[u][1];
-                        v.z &= keep[u][2];
-                        v.w &= keep[u][3];
-                    }
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(v.x, v.y), w[u][0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(v.z, v.w), w[u][1], o[e], 0, 0, 0);
+            for (int e = 0; e < kP; ++e) {
+                const uint4 a0 = v0, a1 = v1;
+                if (e + 1 < kP) {
+                    v0 = vb[piece<4>(32 * e + 32 + m, hf)];
+                    v1 = vb[piece<4>(32 * e + 32 + m, 2 + hf)];
                 }
+                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0][0], o[e], 0, 0, 0);
+                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[0][1], o[e], 0, 0, 0);
+                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), w[1][0], o[e], 0, 0, 0);
+                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), w[1][1], o[e], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
 
         if (count > 0) {
             next_id = page_of(0);
             issue(0, kbuf0, vbuf0);
             next_id = page_of(1);
-            auto step = [&](int i, const uint4 *kb, const uint4 *vb, uint4 *kn, uint4 *vn) {
+            auto step = [&](int i, const uint4 *kb, uint4 *vb, uint4 *kn, uint4 *vn) {
                 // this wave's loads of tile i are in LDS, its reads of tile i - 1 done
                 __builtin_amdgcn_s_waitcnt(0xC07F);
                 wait_vmcnt<0>();
@@ -268,7 +311,9 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                     issue(i + 1, kn, vn);
                     next_id = page_of(i + 2);
                 }
-                multiply(i, kb, vb, ksl, vsl, ok);
+                const int j0 = tiles.at(i) * kTile;
+                if ((ok & 15) != 15 || j0 + kTile > s.len) clear_dead(j0, vb, ok);
+                if (!idle && j0 <= hi) multiply(j0, kb, vb, ksl, vsl, ok);
             };
             for (int i = 0; i < count; i += 2) {
                 step(i, kbuf0, vbuf0, kbuf1, vbuf1);
@@ -293,12 +338,20 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     }
 }
 
+template <typename T, int D>
+void launch_page(const AttnArgs &p, const dim3 &grid, hipStream_t s) {
+    if ((1 << p.c.log2_page) >= kTile)
+        prefill_kernel<T, D, true><<<grid, 64 * kWaves, 0, s>>>(p);
+    else
+        prefill_kernel<T, D, false><<<grid, 64 * kWaves, 0, s>>>(p);
+}
+
 template <typename T>
 hipError_t launch_dim(const AttnArgs &p, int D, const dim3 &grid, hipStream_t s) {
     switch (D) {
-    case 64: prefill_kernel<T, 64><<<grid, 64 * kWaves, 0, s>>>(p); break;
-    case 128: prefill_kernel<T, 128><<<grid, 64 * kWaves, 0, s>>>(p); break;
-    case 256: prefill_kernel<T, 256><<<grid, 64 * kWaves, 0, s>>>(p); break;
+    case 64: launch_page<T, 64>(p, grid, s); break;
+    case 128: launch_page<T, 128>(p, grid, s); break;
+    case 256: launch_page<T, 256>(p, grid, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
