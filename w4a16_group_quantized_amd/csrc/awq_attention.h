@@ -38,6 +38,20 @@ __device__ __forceinline__ Tiles visible_tiles(const AttnArgs &p, int lo, int hi
     return t;
 }
 
+// The sequence with the rank-th most tokens, among up to 64 of them (equal ones in
+// their order); with more the order is as it comes.  All 64 lanes have to ask.
+__device__ __forceinline__ int seq_of_rank(const KvView &c, int rank) {
+    if (c.seqs == 1 || c.seqs > 64) return rank;
+    const int lane = threadIdx.x & 63;
+    const int len = lane < c.seqs ? c.kv_lens[lane] : 0;
+    int above = 0;
+    for (int i = 0; i < c.seqs; ++i) {
+        const int other = __builtin_amdgcn_readlane(len, i);
+        above += other > len || (other == len && i < lane);
+    }
+    return (int)__builtin_ctzll(__ballot(lane < c.seqs && above == rank));
+}
+
 template <typename T>
 __device__ __forceinline__ half8_t as_row_half(const uint16_t *p, float f) {
     float x[8];

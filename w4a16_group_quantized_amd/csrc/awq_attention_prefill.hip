@@ -25,7 +25,7 @@ namespace awq {
 namespace {
 
 constexpr int kRows = 128, kWaveRows = 32, kWaves = 4;
-constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
+constexpr float kWeightBits = 11.0f, kSlack = 4.0f, kLeastUnit = 0x1p-6f;
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -74,7 +74,7 @@ __device__ __forceinline__ int piece(int row, int at) {
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
 template <typename T, int D, bool BIG>
-__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(AttnArgs p) {
+__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
     constexpr int kLoads = D / 64;             // loads of a wave for the keys of a tile, and for the values
@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     const KvView &c = p.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 31, hf = lane >> 5;
-    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
+    const int h = blockIdx.x % c.kv_heads, slot = blockIdx.x / c.kv_heads;
+    const int b = seq_of_rank(c, slot / tiles_per_seq);
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     }
 
     // the longest rows first
-    for (int rt = row_tiles - 1 - (int)blockIdx.y; rt >= 0; rt -= gridDim.y) {
+    for (int rt = row_tiles - 1 - slot % tiles_per_seq; rt >= 0; rt -= tiles_per_seq) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
         const int count = tiles.count();
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             const int id = ok ? want : 0;
             has = BIG ? (ok ? 15 : 0) : __ballot(ok);
             const long long ph = (long long)id * c.kv_heads + h;
-            ks_l = ok ? c.k_scales[ph] : 1.0f;
-            vs_l = ok ? c.v_scales[ph] : 0.0f;
+            ks_l = c.k_scales[ph];             // (of page 0 where there is none: used for no key)
+            vs_l = c.v_scales[ph];
             const int in_page = j0 & (P - 1);
             if constexpr (BIG) {
                 const uint8_t *kp = c.k + ph * slab + in_page * D, *vp = c.v + ph * slab + in_page;
@@ -235,51 +236,61 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                     }
                 }
             }
-            float ks[2], top[2], vs[4];
+            // The scales of the tile's four groups of sixteen keys (with BIG all the same) and, of the
+            // lane's two groups, the keys' scale and what the values' is to the outputs' unit.
+            float ks[2], top[2], vs[4], bits[2], back[2];
+#pragma unroll
+            for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float a = lane_value(ksl, 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
-                // never 0, which would turn a hidden key's -inf into NaN
-                ks[u] = fmaxf((hf ? d : a) * down, 0x1p-126f);
+                const float a = lane_value(ksl, BIG ? 0 : 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
+                // never 0, which would turn a hidden key's -inf into NaN; and where there is no page
+                // the scale may be anything, but no key is seen
+                ks[u] = fminf(fmaxf((hf ? d : a) * down, 0x1p-126f), 0x1p126f);
                 float t = max3(acc[u][0], acc[u][1], acc[u][2]);
 #pragma unroll
                 for (int e = 3; e < 15; e += 2) t = max3(t, acc[u][e], acc[u][e + 1]);
                 top[u] = max3(t, t, acc[u][15]) * ks[u];
             }
-#pragma unroll
-            for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = lane_value(vsl, g);
-            float vmax = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-            if (!(vmax > 0.0f)) vmax = unit;
             const float now = half_max(fmaxf(top[0], top[1]));
-            if (__any(now > mx + kSlack) || vmax != unit) {
-                const float to = fmaxf(mx, now);
+            // The outputs count in units of a values' scale, at least that of every page so far and
+            // at most 2^6 times this tile's: moved with the maximum, which is rare.
+            const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+            if (__any(now > mx + kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
+                const float to = fmaxf(mx, now), to_unit = most > 0.0f ? most : unit;
                 const float alpha = __builtin_amdgcn_exp2f(mx - to);
-                const float turn = alpha * (unit / vmax);
+                const float turn = alpha * (unit / to_unit);
                 mx = to;
                 l *= alpha;
-                unit = vmax;
+                unit = to_unit;
 #pragma unroll
                 for (int e = 0; e < kP; ++e) o[e] *= turn;
             }
-            const float base = kWeightBits - mx;
-            half8_t w[2][2];
-            float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+                if (BIG && u == 1) {
+                    bits[1] = bits[0];
+                    back[1] = back[0];
+                    continue;
+                }
+                const float v = BIG ? vs[0] : hf ? vs[2 * u + 1] : vs[2 * u];
+                const float ratio = v > 0.0f ? v / unit : 1.0f;        // (no weight where there is no page)
+                bits[u] = __builtin_amdgcn_logf(ratio);
+                back[u] = 1.0f / ratio;
+            }
+            half8_t w[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float base = kWeightBits + bits[u] - mx;
+                float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    acc[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
-                    sum[u] += acc[u][e];
+                    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                    sum += f;
+                    w[u][e >> 3][e & 7] = (half_t)f;
                 }
-            l += sum[0] + sum[1];
-            if (!BIG && !(vs[0] == vmax && vs[1] == vmax && vs[2] == vmax && vs[3] == vmax)) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) acc[u] *= (hf ? vs[2 * u + 1] : vs[2 * u]) / vmax;
+                l += sum * back[u];
             }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[u][e >> 3][e & 7] = (half_t)acc[u][e];
             uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
 #pragma unroll
             for (int e = 0; e < kP; ++e) {
@@ -339,19 +350,19 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
 }
 
 template <typename T, int D>
-void launch_page(const AttnArgs &p, const dim3 &grid, hipStream_t s) {
+void launch_page(const AttnArgs &p, int grid, int tiles_per_seq, hipStream_t s) {
     if ((1 << p.c.log2_page) >= kTile)
-        prefill_kernel<T, D, true><<<grid, 64 * kWaves, 0, s>>>(p);
+        prefill_kernel<T, D, true><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
     else
-        prefill_kernel<T, D, false><<<grid, 64 * kWaves, 0, s>>>(p);
+        prefill_kernel<T, D, false><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
 }
 
 template <typename T>
-hipError_t launch_dim(const AttnArgs &p, int D, const dim3 &grid, hipStream_t s) {
+hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hipStream_t s) {
     switch (D) {
-    case 64: launch_page<T, 64>(p, grid, s); break;
-    case 128: launch_page<T, 128>(p, grid, s); break;
-    case 256: launch_page<T, 256>(p, grid, s); break;
+    case 64: launch_page<T, 64>(p, grid, tiles_per_seq, s); break;
+    case 128: launch_page<T, 128>(p, grid, tiles_per_seq, s); break;
+    case 256: launch_page<T, 256>(p, grid, tiles_per_seq, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -360,11 +371,17 @@ hipError_t launch_dim(const AttnArgs &p, int D, const dim3 &grid, hipStream_t s)
 }  // namespace
 
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s) {
-    // (sequence, kv head) fastest: with a multiple of eight of them, the row tiles that read
-    // the same keys meet in one XCD's cache.  The kernel steps on where the grid is cut.
+    // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
+    // keys meet in one XCD's cache.  Then the row tiles of a sequence, and the sequences, the
+    // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
+    // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
+    // the grid is cut.
+    const int pairs = p.c.kv_heads * p.c.seqs;                                   // below 2^24
     const long long tiles = ((long long)max_q * p.group + kRows - 1) / kRows;
-    const dim3 grid(p.c.kv_heads * p.c.seqs, (unsigned)std::min<long long>(tiles, 65535));
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, s) : launch_dim<half_t>(p, head_dim, grid, s);
+    const int tiles_per_seq = (int)std::min<long long>(tiles, ((1 << 24) - 1) / pairs);
+    const int grid = pairs * tiles_per_seq;
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, tiles_per_seq, s)
+                : launch_dim<half_t>(p, head_dim, grid, tiles_per_seq, s);
 }
 
 }  // namespace awq
