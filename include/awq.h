@@ -375,7 +375,7 @@ typedef struct awq_kv_cache {
  * graph serves every step that changes them.  Rows behind q_starts[seqs] (a
  * padded batch) belong to no sequence: nothing is read or written for them.
  * A sequence with no rows, or none at all (seqs or rows 0), is fine.  seqs <=
- * 65535, seqs * kv_heads < 2^24, seqs * table_width < 2^31, table_width *
+ * 65535, seqs * kv_heads < 2^20, seqs * table_width < 2^31, table_width *
  * page_size <= 2^30.
  *
  * max_q, max_kv: the most rows and tokens of a sequence in this call.  They size

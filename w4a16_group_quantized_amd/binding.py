@@ -585,14 +585,17 @@ def _rows(t: torch.Tensor, heads: int | None, like: torch.Tensor, cache: KvCache
     return t.data_ptr(), s[0] if rows > 1 else width
 
 
-def _kv_call(device: torch.device, stream, call):
-    """call(stream address) with ``device`` current, on ``stream`` or the device's
-    current one."""
-    if device.index == torch.cuda.current_device():
-        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream))
+def _kv_call(device: torch.device, stream, fn, *args):
+    """fn(*args, stream address) with ``device`` current, on ``stream`` or the device's
+    current one.  (The raw getters: torch.cuda.current_stream() makes an object of
+    it, 5 us of a call of 18.)"""
+    if device.index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+            status = fn(*args, _stream(stream))
+    if status != AWQ_SUCCESS:
+        _check(status)
 
 
 def _on(batch: KvBatch, cache: KvCache):
@@ -634,9 +637,8 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
         rp = _dev(rope, torch.float32, "rope")
         positions, rot = rope.shape
     b = batch._c(k.shape[0])
-    _kv_call(k.device, stream, lambda s: load().awq_kv_append(
-        qp, qs, kp, ks, vp, vs, op, heads, ROW_TYPES[k.dtype], rp, positions, rot, int(interleaved),
-        cache._c, b, s))
+    _kv_call(k.device, stream, load().awq_kv_append, qp, qs, kp, ks, vp, vs, op, heads, ROW_TYPES[k.dtype],
+             rp, positions, rot, int(interleaved), cache._c, b)
     return out
 
 
@@ -670,6 +672,6 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
             workspace = _new(nbytes, torch.uint8, q.device, stream)
     wp, wn = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
     scale = cache._c.head_dim ** -0.5 if scale is None else scale
-    _kv_call(q.device, stream, lambda s: lib.awq_attention(
-        qp, qs, op, heads, ROW_TYPES[q.dtype], scale, window, sinks, cache._c, b, wp, wn, s))
+    _kv_call(q.device, stream, lib.awq_attention, qp, qs, op, heads, ROW_TYPES[q.dtype], scale, window, sinks,
+             cache._c, b, wp, wn)
     return out

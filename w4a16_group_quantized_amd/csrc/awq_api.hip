@@ -99,7 +99,7 @@ awq_status check_kv(const awq_kv_cache *c, const awq_kv_batch *b) {
     if (c->page_size & (c->page_size - 1) || c->page_size < 16 || c->page_size > 256)
         return AWQ_ERROR_SHAPE;
     // grid dimensions
-    if (c->kv_heads > 65535 || b->seqs > 65535 || (long long)c->kv_heads * b->seqs >= 1 << 24)
+    if (c->kv_heads > 65535 || b->seqs > 65535 || (long long)c->kv_heads * b->seqs >= 1 << 20)
         return AWQ_ERROR_SHAPE;
     if ((long long)c->pages * c->kv_heads > kMaxElems || (long long)b->seqs * b->table_width > kMaxElems)
         return AWQ_ERROR_SHAPE;

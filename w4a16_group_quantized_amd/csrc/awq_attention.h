@@ -19,7 +19,7 @@ struct AttnArgs {
     int q_heads, group;
     float scale;             // scale * log2(e)
     int window, sinks;
-    int splits, chunk;       // chunks of a row tile, and their least length in tiles
+    int splits, target;      // most chunks of a row tile; workgroups that all chunks are dealt to
 };
 
 // The 64-key tiles that rows at positions lo .. hi see: tiles [0, a) that hold
@@ -60,6 +60,46 @@ __device__ __forceinline__ half8_t as_row_half(const uint16_t *p, float f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = (half_t)(x[i] * f);
     return h;
+}
+
+// The lane's value and that of its partner in the other half of the wave, the
+// lower half's first.  (The elements go through variables of their own: a bit
+// cast straight from an element of the result takes element 0.)
+__device__ __forceinline__ float2 halves(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float half_max(float x) {
+    const float2 v = halves(x);
+    return fmaxf(v.x, v.y);
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const float2 v = halves(x);
+    return v.x + v.y;
+}
+// The largest of three (NaN only if all are), without the instructions that the
+// compiler puts before fmaxf to quiet NaNs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+// The same over the four lanes that share lane % 16.
+__device__ __forceinline__ float2 quarters(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float group_max(float x) {
+    const float2 v = quarters(x);
+    return half_max(fmaxf(v.x, v.y));
+}
+__device__ __forceinline__ float group_sum(float x) {
+    const float2 v = quarters(x);
+    return half_sum(v.x + v.y);
 }
 
 // Four masks of four bytes each: the first `live` of sixteen bytes.

@@ -17,14 +17,16 @@
 // dealt to the four 16-key products so that lane group g = lane / 16 ends up
 // with the keys 16 g .. 16 g + 15, which are sixteen consecutive bytes of a row
 // of V^T: every load is 16 bytes a lane, and 16 keys never leave a page.
-// Weights are held to fp16 twice, as a leading part and its remainder: the
-// second product is free beside the loads, and the result keeps fp32's quality.
+// For fp16 outputs weights are held to fp16 twice, as a leading part and its
+// remainder: the second product is free beside the loads, and the result keeps
+// fp32's quality (bf16 outputs round eight times coarser than one fp16 does).
 // Weights are scaled by 2^14 so that the small ones stay normal fp16 numbers.
 // Bound: the bytes of K and V (HBM).
 //
 // combine_kernel joins the chunks' partial results (fp32, in the workspace)
 // where there is more than one chunk.
 #include <algorithm>
+#include <type_traits>
 
 #include "awq_attention.h"
 #include "awq_internal.h"
@@ -34,35 +36,102 @@ namespace {
 
 constexpr int kRows = 16;                  // rows of a workgroup
 constexpr int kWaves = 4;
+constexpr int kXcds = 8;
 constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of the formula
+constexpr float kLeastUnit = 0x1p-6f;
 
-// A partial result: D outputs, then the maximum and the sum.
+// A partial result: D outputs, the maximum, the sum and (of chunk 0) the number of
+// chunks.
 template <int D>
 constexpr int kPart = D + 4;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
+// How a call is cut into chunks of keys, from the number of (sequence, kv head, row
+// tile) groups and, on the device, from the sequences' lengths.  Measured at 32 heads
+// over 8 of 128 elements, pages of 64 (us):
+//   not cut / dealt to 256 / 512 / 1024 workgroups
+//   1 sequence of 300: 8.6 / 11.4 / 11.4 / 11.4;  of 1000: 14.7 / 11.9 / 12.0 / 11.9
+//   1 of 32k: 216 / 23.0 / 22.8 / 28.2;  8 of 4k to 8k: 63 / 33.6 / 34.8 / 41.6
+//   16 of 4k to 8k: 65 / 52.3 / 48.4 / 51.1;  24 of 3k to 6k: 57.5 / 61.0 / 60.3 / 60.9
+//   64 of 1k to 2k: 43.9 / 50.2 / 50.0 / 54.1
+// So: few tiles take no longer than the launch that joins chunks (and the call itself,
+// which is some 4 us shorter for one launch); one workgroup for
+// each CU streams as fast as the memory, while sequences of different lengths need a
+// finer cut; and many groups need no cut, unless sequences may be so long that one
+// among short ones would be the last by far.
+constexpr int kUncutTiles = 12, kManyGroups = 192, kLongTiles = 256, kLeastChunk = 4, kMaxSplits = 256;
+
+// Chunks for a tile: from the tiles that all sequences' rows see, for all kv heads.
+// The host knows no lengths, so each wave adds them up.
+__device__ __forceinline__ float chunks_per_tile(const AttnArgs &p) {
+    const KvView &c = p.c;
+    float sum = 0.0f;
+    for (int b = threadIdx.x & 63; b < c.seqs; b += 64) {
+        const Seq s = load_seq(c, b);
+        if (s.n > 0)
+            sum += (float)visible_tiles(p, s.first(), s.len - 1, s.len).count() * (float)((s.n * p.group + kRows - 1) / kRows);
+    }
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
+    sum *= (float)c.kv_heads;
+    return (float)p.target / fmaxf(sum, 1.0f);
+}
+
+// Codes are read once.  With pages of a tile, whole 128-byte lines at a time: the
+// caches need not keep them (3 to 4% on 4k to 8k tokens; with larger pages, where two
+// waves share the lines of the values, 25% slower).
+template <bool ONCE>
+__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
+    typedef uint32_t words __attribute__((ext_vector_type(4)));
+    const words *w = reinterpret_cast<const words *>(p);
+    const words v = ONCE ? __builtin_nontemporal_load(w) : *w;
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// PAGE: pages of 64 keys (a tile), of more (kLarge), or of fewer (kSmall).  With
+// those of a tile or more, a tile's page and scales are the same for all lanes.
+enum { kSmall, kOne, kLarge };
+template <typename T, int D, int PAGE>
+__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) split_kernel(AttnArgs p, int row_tiles) {
+    constexpr bool BIG = PAGE != kSmall;
+    constexpr bool kRest = __is_same(T, half_t);   // weights keep their remainder
     constexpr int kC = D / 64;             // 64-element pieces of a key
     constexpr int kT = D / 16;             // 16-element pieces of a value
     __shared__ float red_m[kWaves][kRows], red_l[kWaves][kRows];
     __shared__ float red_o[kRows][D + 4];
     const KvView &c = p.c;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x, b = blockIdx.z;
-    const int h = blockIdx.y % c.kv_heads;
+    // Workgroups go to the XCDs in turn.  A chunk of a sequence, with all of its kv heads and row
+    // tiles, stays on one XCD, so that each XCD translates the addresses of its own pages only
+    // (with a head to an XCD: 97 -> 112 us on two sequences of 131k tokens).  Chunks after the
+    // first come last, so that the workgroups that have none do too.
+    const int slot = blockIdx.x / kXcds;
+    const int unit_id = slot / (row_tiles * c.kv_heads) * kXcds + blockIdx.x % kXcds;
+    const int split = unit_id / c.seqs, b = unit_id % c.seqs;
+    const int h = slot / row_tiles % c.kv_heads;
+    if (split >= p.splits) return;
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
-    const int row_tiles = gridDim.y / c.kv_heads;
-    for (int rt = blockIdx.y / c.kv_heads; rt * kRows < total; rt += row_tiles) {
+    const float per_tile = p.part == nullptr ? 0.0f : chunks_per_tile(p);
+    for (int rt = slot % row_tiles; rt * kRows < total; rt += row_tiles) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const int lo = s.first() + r0 / p.group, hi = s.first() + r1 / p.group;
         const Tiles tiles = visible_tiles(p, lo, hi, s.len);
         const int count = tiles.count();
-        const int chunk = max(p.chunk, (count + p.splits - 1) / p.splits);
-        const int t0 = split * chunk, t1 = min(count, t0 + chunk);
-        if (t0 >= t1 && split > 0) continue;
+        // its share of the chunks, rounded down: one more than one for each CU would share a CU
+        const int chunks = __builtin_amdgcn_readfirstlane(
+            max(1, min(min(p.splits, count / kLeastChunk), (int)((float)count * per_tile * 1.0001f))));
+        if (split >= chunks) continue;
+        // Chunks begin at, and waves take, tiles by their number in the sequence modulo the waves:
+        // with pages of 128 and more two tiles share each 128-byte line of the values, which two
+        // waves should read at the same time (131k tokens: 112 -> 97 us).
+        const int shift = tiles.b - tiles.a;
+        const auto border = [&](int k) {
+            const int at = (int)((long long)count * k / chunks);
+            return k == 0 ? 0 : k == chunks ? count : max(0, at - ((at + shift) & (kWaves - 1)));
+        };
+        const int t0 = border(split), t1 = border(split + 1);
+        const int first = t0 + ((wave - t0 - shift) & (kWaves - 1));
         // this lane's row
         const int r = min(r0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
@@ -100,33 +169,58 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
 #pragma unroll
         for (int i = 0; i < kT; ++i) o[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-        for (int i = t0 + wave; i < t1; i += kWaves) {
-            const int j0 = tiles.at(i) * kTile;
-            // the page of the sixteen keys that this lane scores (group g), and of those whose
-            // codes it loads as keys (group m / 4)
-            const int jg = j0 + 16 * g, jk = j0 + 16 * (m >> 2);
-            int idg = 0, idk = 0;
-            if (jg < s.len) idg = c.page_table[(long long)b * c.table_width + (jg >> c.log2_page)];
-            if (jk < s.len) idk = c.page_table[(long long)b * c.table_width + (jk >> c.log2_page)];
-            int live = min(max(s.len - jg, 0), 16);     // keys of group g that exist
-            if (idg < 0 || idg >= c.pages) {
-                idg = 0;
-                live = 0;
-            }
-            if (idk < 0 || idk >= c.pages) idk = 0;
-            const long long pg = (long long)idg * c.kv_heads + h;
-            const uint8_t *kp = c.k + ((long long)idk * c.kv_heads + h) * P * D + (jk & (P - 1)) * D + (m & 3) * D + 16 * g;
-            const uint8_t *vp = c.v + pg * P * D + m * P + (jg & (P - 1));
-            uint4 kc[4][kC], vc[kT];
+        // A tile's page numbers are asked for two tiles ahead, its key codes and scales one, and
+        // its value codes as its scores begin: something is always in flight.  (A second set of
+        // registers for values a tile ahead gained nothing on short calls and lost 17% on long ones.)
+        const int32_t *table = c.page_table + (long long)b * c.table_width;
+        int ask_g = -1, ask_k = -1;            // page numbers of the group that the lane scores (g), and loads (m / 4)
+        int live_n = 0;
+        bool page_n = false;
+        float ks_n = 0.0f, vs_n = 0.0f;
+        const uint8_t *vp_n = nullptr;
+        uint4 kc[4][kC];
+        auto ask = [&](int i) {
+            const int j0 = tiles.at(i) * kTile, jg = j0 + (BIG ? 0 : 16 * g), jk = j0 + 16 * (m >> 2);
+            ask_g = jg < s.len ? table[jg >> c.log2_page] : -1;
+            if (!BIG) ask_k = jk < s.len ? table[jk >> c.log2_page] : -1;
+        };
+        auto fetch = [&](int i) {
+            const int j0 = tiles.at(i) * kTile, jg = j0 + 16 * g, jk = j0 + 16 * (m >> 2);
+            const int want = BIG ? __builtin_amdgcn_readfirstlane(ask_g) : ask_g;
+            const bool ok = (uint32_t)want < (uint32_t)c.pages;
+            const int idg = ok ? want : 0, idk = BIG ? idg : (uint32_t)ask_k < (uint32_t)c.pages ? ask_k : 0;
+            page_n = ok;
+            live_n = ok ? min(max(s.len - jg, 0), 16) : 0;      // keys of group g that exist
+            const long long pg = (long long)idg * c.kv_heads + h, pk = BIG ? pg : (long long)idk * c.kv_heads + h;
+            const int at_g = BIG ? (j0 & (P - 1)) + 16 * g : jg & (P - 1), at_k = BIG ? (j0 & (P - 1)) + 16 * (m >> 2) : jk & (P - 1);
+            const uint8_t *kp = c.k + pk * P * D + (uint32_t)(at_k * D + (m & 3) * D + 16 * g);
+            vp_n = c.v + pg * P * D + (uint32_t)(m * P + at_g);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int e = 0; e < kC; ++e) kc[t][e] = *reinterpret_cast<const uint4 *>(kp + 4 * t * D + 64 * e);
+                for (int e = 0; e < kC; ++e) kc[t][e] = load_codes<PAGE == kOne>(kp + 4 * t * D + 64 * e);
+            ks_n = c.k_scales[pg];
+            vs_n = c.v_scales[pg];
+        };
+        if (first < t1) {
+            ask(first);
+            fetch(first);
+            ask(min(first + kWaves, t1 - 1));
+        }
+        // One tile, with the next one's loads or without: a condition around the loads would make
+        // the products wait for all of them.
+        auto tile = [&](int i, auto more) {
+            const int j0 = tiles.at(i) * kTile, jg = j0 + 16 * g;
+            uint4 vc[kT];
 #pragma unroll
-            for (int t = 0; t < kT; ++t) vc[t] = *reinterpret_cast<const uint4 *>(vp + 16 * t * P);
-            const float ks = live ? c.k_scales[pg] * down : 0.0f;
-            float vs = live ? c.v_scales[pg] : 0.0f;
-
+            for (int t = 0; t < kT; ++t) vc[t] = load_codes<PAGE == kOne>(vp_n + 16 * t * P);
+            __builtin_amdgcn_sched_barrier(0);         // now, not between the products
+            // (a page's scales, whether or not all of its keys exist: with BIG the same in all lanes)
+            float ks = page_n ? ks_n * down : 0.0f, vs = page_n ? vs_n : 0.0f;
+            int live = live_n;
+            // taken here, so that the next tile's can be loaded into the same registers (copies of
+            // them would wait for every load)
+            asm volatile("" : "+v"(ks), "+v"(vs), "+v"(live));
             float x[16];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -139,13 +233,19 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[4 * t + e] = acc[e] * ks;
             }
+            if constexpr (decltype(more)::value) {
+                fetch(i + kWaves);
+                ask(min(i + 2 * kWaves, t1 - 1));
+                __builtin_amdgcn_sched_barrier(0);
+            }
             const bool whole = live == 16 && j0 + kTile <= lo + 1 &&
                                (p.window <= 0 || j0 > hi - p.window || j0 + kTile <= p.sinks);
             if (!__all(whole)) {
+                const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = jg + e;
-                    const bool see = e < live && j <= pos && (p.window <= 0 || j > pos - p.window || j < p.sinks);
+                    const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
                     x[e] = see ? x[e] : -__builtin_inff();
                 }
                 // codes of slots that hold no token may be anything, NaN among it
@@ -159,51 +259,54 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
                     vc[t].w &= keep[3];
                 }
             }
-            float top = x[0];
+            float top = max3(x[0], x[1], x[2]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float now = fmaxf(mx, top);
-            // the values of this tile count in units of its largest scale
-            float vmax = fmaxf(vs, __shfl_xor(vs, 16));
-            vmax = fmaxf(vmax, __shfl_xor(vmax, 32));
-            if (!(vmax > 0.0f)) vmax = unit;
-            const float ratio = vs / vmax;
-            const float alpha = __builtin_amdgcn_exp2f(mx - now);
-            const float turn = alpha * (unit / vmax);
-            unit = vmax;
-            mx = now;
-            const float base = now - kWeightBits;
+            for (int e = 3; e < 15; e += 2) top = max3(top, x[e], x[e + 1]);
+            top = group_max(max3(top, top, x[15]));
+            // The outputs count in units of a values' scale, at least that of every page so far and
+            // at most 2^6 times this tile's; what a page's is to it goes into the exponent.
+            const float most = BIG ? vs : group_max(vs);
+            const float now = fmaxf(mx, top), to_unit = most > unit || most < unit * kLeastUnit ? most : unit;
+            const float next_unit = most > 0.0f ? to_unit : unit;
+            if (__any(now != mx) || next_unit != unit) {
+                const float alpha = __builtin_amdgcn_exp2f(mx - now);
+                const float turn = alpha * (unit / next_unit);
+                l *= alpha;
+#pragma unroll
+                for (int t = 0; t < kT; ++t) o[t] *= turn;
+                unit = next_unit;
+                mx = now;
+            }
+            const float ratio = vs > 0.0f ? vs / unit : 1.0f;         // (no weight where there is no page)
+            const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - mx;
             float sum = 0.0f;
             half8_t ph[2], pl[2];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float w = __builtin_amdgcn_exp2f(x[e] - base);
+                const float w = __builtin_amdgcn_exp2f(x[e] + base);
                 sum += w;
-                const float wv = w * ratio;
-                const half_t lead = (half_t)wv;
+                const half_t lead = (half_t)w;
                 ph[e >> 3][e & 7] = lead;
-                pl[e >> 3][e & 7] = (half_t)(wv - (float)lead);
+                if constexpr (kRest) pl[e >> 3][e & 7] = (half_t)(w - (float)lead);
             }
-            l = l * alpha + sum;
-            if (__any(turn != 1.0f)) {
-#pragma unroll
-                for (int t = 0; t < kT; ++t) o[t] *= turn;
-            }
+            l += sum / ratio;
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
                 const half8_t v0 = e4m3x8_to_half(vc[t].x, vc[t].y), v1 = e4m3x8_to_half(vc[t].z, vc[t].w);
                 o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, ph[0], o[t], 0, 0, 0);
                 o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, ph[1], o[t], 0, 0, 0);
-                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[0], o[t], 0, 0, 0);
-                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[1], o[t], 0, 0, 0);
+                if constexpr (kRest) {
+                    o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[0], o[t], 0, 0, 0);
+                    o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[1], o[t], 0, 0, 0);
+                }
             }
-        }
+        };
+        int i = first;
+        for (; i + kWaves < t1; i += kWaves) tile(i, std::true_type{});
+        if (i < t1) tile(i, std::false_type{});
 
         // join the four waves
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+        l = group_sum(l);
         if (g == 0) {
             red_m[wave][m] = mx;
             red_l[wave][m] = l;
@@ -226,7 +329,7 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
             }
             __syncthreads();
         }
-        if (p.part == nullptr) {
+        if (chunks == 1) {
             // a row of D outputs by 16 lanes
             const int rr = threadIdx.x >> 4;
             if (r0 + rr <= r1) {
@@ -252,75 +355,110 @@ __global__ void __launch_bounds__(64 * kWaves) split_kernel(AttnArgs p) {
                 if ((threadIdx.x & 15) == 0) {
                     dst[D] = total_m;
                     dst[D + 1] = total_l;
+                    dst[D + 2] = (float)chunks;
                 }
+            }
+        }
+        if (chunks == 1 && p.part != nullptr) {
+            const int rr = threadIdx.x;
+            if (rr < kRows && r0 + rr <= r1) {
+                const int tok = (r0 + rr) / p.group, hd = h * p.group + (r0 + rr) % p.group;
+                p.part[((long long)(s.row0 + tok) * p.q_heads + hd) * p.splits * kPart<D> + D + 2] = 1.0f;
             }
         }
         __syncthreads();                    // red_* are free again
     }
 }
 
-// One wave joins the chunks of one (row, head).
+// A workgroup joins the chunks of one (row, head): D / 4 threads to a chunk, as many
+// chunks at once as that leaves room for, then the threads' sums through LDS.
+// Bound: latency (a few loads in a row), and the launch.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
+    constexpr int kLanes = D / 4, kAtOnce = 256 / kLanes;
+    __shared__ float weight[kMaxSplits], red[2][4];
+    __shared__ float4_t part[kAtOnce][kLanes];
     const KvView &c = p.c;
-    const int lane = threadIdx.x & 63;
-    const int b = blockIdx.z;
+    const int tid = threadIdx.x, b = blockIdx.y;
     const Seq s = load_seq(c, b);
-    const int waves = gridDim.x * 4;
-    for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < s.n * p.q_heads; i += waves) {
+    for (int i = blockIdx.x; i < s.n * p.q_heads; i += gridDim.x) {
         const int token = i / p.q_heads, head = i % p.q_heads;
-        // the chunks that the split kernel made of this row's tile
-        const int r = token * p.group + head % p.group;
-        const int r0 = r / kRows * kRows, r1 = min(r0 + kRows, s.n * p.group) - 1;
-        const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
-        const int count = tiles.count();
-        const int chunk = max(p.chunk, (count + p.splits - 1) / p.splits);
-        const int n = max(1, (count + chunk - 1) / chunk);
         const float *src = p.part + ((long long)(s.row0 + token) * p.q_heads + head) * p.splits * kPart<D>;
-        float mx = kEmpty;
-        for (int k = 0; k < n; ++k) mx = fmaxf(mx, src[k * kPart<D> + D]);
-        float o[D / 64] = {}, l = 0.0f;
-        for (int k = 0; k < n; ++k) {
-            const float f = __builtin_amdgcn_exp2f(src[k * kPart<D> + D] - mx);
-            l += f * src[k * kPart<D> + D + 1];
-#pragma unroll
-            for (int e = 0; e < D / 64; ++e) o[e] += f * src[k * kPart<D> + 64 * e + lane];
+        const int n = min((int)src[D + 2], kMaxSplits);
+        if (n <= 1) continue;                  // the one chunk has written its outputs
+        // one chunk's maximum and sum to a thread
+        float own = kEmpty, l = 0.0f;
+        if (tid < n) {
+            own = src[tid * kPart<D> + D];
+            l = src[tid * kPart<D> + D + 1];
         }
-        const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
-        uint16_t *dst = p.out + ((long long)(s.row0 + token) * p.q_heads + head) * D;
+        float mx = own;
+        for (int k = 32; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
+        if ((tid & 63) == 0) red[0][tid >> 6] = mx;
+        __syncthreads();
+        mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+        const float f = __builtin_amdgcn_exp2f(own - mx);
+        if (tid < n) weight[tid] = f;
+        l = tid < n ? l * f : 0.0f;
+        for (int k = 32; k > 0; k >>= 1) l += __shfl_xor(l, k);
+        if ((tid & 63) == 0) red[1][tid >> 6] = l;
+        __syncthreads();
+        l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+        const int lane = tid % kLanes, at = tid / kLanes;
+        float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int k = at; k < n; k += kAtOnce)
+            o += weight[k] * *reinterpret_cast<const float4_t *>(src + k * kPart<D> + 4 * lane);
+        part[at][lane] = o;
+        __syncthreads();
+        if (at == 0) {
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) dst[64 * e + lane] = from_float<T>(o[e] * inv);
+            for (int k = 1; k < kAtOnce; ++k) o += part[k][lane];
+            const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
+            uint2 y;
+            y.x = (uint32_t)from_float<T>(o[0] * inv) | ((uint32_t)from_float<T>(o[1] * inv) << 16);
+            y.y = (uint32_t)from_float<T>(o[2] * inv) | ((uint32_t)from_float<T>(o[3] * inv) << 16);
+            *reinterpret_cast<uint2 *>(p.out + ((long long)(s.row0 + token) * p.q_heads + head) * D + 4 * lane) = y;
+        }
+        __syncthreads();                       // the LDS arrays are free again
     }
 }
 
-// How a call is cut: chunks and their least length.  Enough workgroups for the
-// 256 CUs, but no chunk below eight tiles (two for each wave).
-constexpr int kWantGroups = 1024, kLeastChunk = 8, kMaxSplits = 256;
-
+// The grid of a call: the most chunks, whose number is found on the device, and the
+// workgroups that they are dealt to.
 struct Plan {
-    int row_tiles, splits, chunk;
+    int row_tiles, splits, target;
 };
 Plan plan(int seqs, int kv_heads, int group, int max_q, int max_kv, int window, int sinks) {
     Plan pl;
     // (the kernel steps on where the grid is cut)
-    pl.row_tiles = (int)std::min<long long>(((long long)max_q * group + kRows - 1) / kRows, 65535 / kv_heads);
+    const int units = (seqs + kXcds - 1) / kXcds * kXcds;
+    pl.row_tiles = (int)std::min<long long>(((long long)max_q * group + kRows - 1) / kRows,
+                                            std::max(1, ((1 << 24) - 1) / (units * kv_heads)));
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
-    const int tiles = (int)((keys + kTile - 1) / kTile);
-    const long long groups = (long long)seqs * kv_heads * pl.row_tiles;
-    const int want = (int)std::min<long long>(kMaxSplits, std::max<long long>(1, kWantGroups / groups));
-    pl.chunk = std::max(kLeastChunk, (tiles + want - 1) / want);
-    pl.splits = std::max(1, (tiles + pl.chunk - 1) / pl.chunk);
+    const long long tiles = (keys + kTile - 1) / kTile, groups = (long long)seqs * kv_heads * pl.row_tiles;
+    pl.target = groups <= 64 ? 256 : 512;
+    long long want = std::max(8ll, 4 * ((pl.target + groups - 1) / groups));     // lengths may differ by much
+    if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
+    pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
     return pl;
 }
 
 template <typename T, int D>
 hipError_t launch(AttnArgs p, const Plan &pl, int max_q, hipStream_t s) {
-    const dim3 grid(pl.splits, pl.row_tiles * p.c.kv_heads, p.c.seqs);
-    split_kernel<T, D><<<grid, 64 * kWaves, 0, s>>>(p);
+    const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
+    const int grid = units * p.c.kv_heads * pl.row_tiles;
+    const int page = 1 << p.c.log2_page;
+    if (page == kTile)
+        split_kernel<T, D, kOne><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+    else if (page > kTile)
+        split_kernel<T, D, kLarge><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+    else
+        split_kernel<T, D, kSmall><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.part == nullptr) return e;
-    combine_kernel<T, D><<<dim3((max_q * p.q_heads + 3) / 4, 1, p.c.seqs), 256, 0, s>>>(p);
+    combine_kernel<T, D><<<dim3(max_q * p.q_heads, p.c.seqs), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -353,7 +491,7 @@ hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, lo
                             int max_q, int max_kv, void *workspace, hipStream_t s) {
     const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, max_q, max_kv, window, sinks);
     AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
-               q_heads / c.kv_heads, scale * kLog2e, window, sinks, pl.splits, pl.chunk};
+               q_heads / c.kv_heads, scale * kLog2e, window, sinks, pl.splits, pl.target};
     if (prefill_rows(p.group, max_q)) return launch_attention_prefill(p, head_dim, bf16, max_q, s);
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, max_q, s) : launch_dim<half_t>(p, head_dim, pl, max_q, s);
 }

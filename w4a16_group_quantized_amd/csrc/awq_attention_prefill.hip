@@ -36,30 +36,6 @@ __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::
 __device__ __forceinline__ void to_lds16(const void *src, uint4 *dst) {
     __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
 }
-// The lane's value and that of its partner in the other half of the wave, the
-// lower half's first.  (The elements go through variables of their own: a bit
-// cast straight from an element of the result takes element 0.)
-__device__ __forceinline__ float2 halves(float x) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const uint32_t a = r[0], b = r[1];
-    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
-}
-__device__ __forceinline__ float half_max(float x) {
-    const float2 v = halves(x);
-    return fmaxf(v.x, v.y);
-}
-__device__ __forceinline__ float half_sum(float x) {
-    const float2 v = halves(x);
-    return v.x + v.y;
-}
-// The largest of three (NaN only if all are), without the instructions that the
-// compiler puts before fmaxf to quiet NaNs.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
-}
 __device__ __forceinline__ float lane_value(float x, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
