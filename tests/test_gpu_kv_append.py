@@ -162,6 +162,17 @@ def test_dense_rows_no_queries_and_a_side_stream():
     assert torch.equal(cache.k_scales.cpu().double(), wks) and torch.equal(cache.v_scales.cpu().double(), wvs)
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
+@pytest.mark.parametrize("held", [0, 1, 3, 6, 13])
+@pytest.mark.parametrize("n", [2, 15, 16, 29, 30, 33, 64, 115])
+def test_odd_places(max_q, held, n):
+    """Rows that begin and end anywhere in a word, a store or a page, whatever the hint."""
+    t = kc.Batch(40 + n, "fp16", [n], [held + n], 2, 1, 128, 128).fill([held])
+    cache, batch, q, k, v = t.device(max_q=max_q)
+    got = binding.kv_append(q, k, v, cache, batch)
+    compare(t, (got.cpu(), cache.k.cpu(), cache.v.cpu(), cache.k_scales.cpu(), cache.v_scales.cpu()))
+
+
 def test_empty_calls():
     t = kc.Batch(2, "fp16", [0, 0], [5, 0], 2, 2, 64, 16).fill()
     got = run(t)

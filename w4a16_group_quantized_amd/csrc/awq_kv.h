@@ -61,14 +61,17 @@ __device__ __forceinline__ uint16_t from_float<bhalf_t>(float f) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const uint16_t *p, float f[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void unpack8(uint4 u, float f[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f[2 * i] = to_float<T>((uint16_t)w[i]);
         f[2 * i + 1] = to_float<T>((uint16_t)(w[i] >> 16));
     }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const uint16_t *p, float f[8]) {
+    unpack8<T>(*reinterpret_cast<const uint4 *>(p), f);
 }
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float f[8]) {

@@ -24,16 +24,14 @@
 // a row that sees the token comes out NaN, and a row that does not see it is
 // not disturbed, since values never hold a NaN.
 //
-// One workgroup owns one (page, kv head) and the query heads that share the
-// head, for the page's new tokens: nobody else writes that slab or its scales,
-// so no atomics.  Bound: HBM for prompts, launch latency for single tokens.
+// One workgroup owns one (page, kv head), for the page's new tokens: nobody else
+// writes that slab or its scales, so no atomics.  Bound: HBM for prompts, launch latency for single tokens.
 #include "awq_internal.h"
 #include "awq_kv.h"
 
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxPage = 256;
 constexpr int kMinExp = -64;
 
@@ -57,50 +55,101 @@ __device__ __forceinline__ float scale_for(float amax) {
     return pow2(max(e, kMinExp));
 }
 
-// Sixteen elements of a head row: those of unit `u` of the D / 16 units, as two
-// chunks of eight at element c0 and c1.  Rotated units in half pairing hold
-// elements i.. and i + R/2..; all others are 16 consecutive elements.
-template <bool ADJ>
+// Sixteen elements of a head row: those of unit u of the D / 16 units, as two chunks
+// of eight, at elements c0 and c1.  The first and the second chunks of a row's units
+// each lie side by side, so that a wave's loads and stores are of whole lines.
+template <int D, bool ADJ>
 __device__ __forceinline__ void unit_chunks(int u, int rot, int &c0, int &c1) {
-    if (!ADJ && 16 * u < rot) {
+    if (ADJ) {
+        c0 = 8 * u;
+        c1 = 8 * u + D / 2;
+    } else if (16 * u < rot) {                         // pairs (i, i + rot / 2)
         c0 = 8 * u;
         c1 = 8 * u + rot / 2;
     } else {
-        c0 = 16 * u;
-        c1 = 16 * u + 8;
+        c0 = 8 * u + rot / 2;
+        c1 = 8 * u + D / 2;
     }
 }
 
-// Rotates a unit in place.  row: the table's row of the position.
-template <bool ADJ>
-__device__ __forceinline__ void rotate_unit(float a[8], float b[8], int u, int rot, const float *row) {
-    if (16 * u >= rot) return;
-    const float4 *cp = reinterpret_cast<const float4 *>(row + 8 * u);
-    const float4 *sp = reinterpret_cast<const float4 *>(row + rot / 2 + 8 * u);
-    const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
-    const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma clang fp contract(off)   // each product and sum is rounded once, as the formula says
-        float &x = ADJ ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
-        float &y = ADJ ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-        const float p = x * cs[i] - y * sn[i];
-        const float q = y * cs[i] + x * sn[i];
-        x = p;
-        y = q;
-    }
+// Queries of a prompt are read and written once, and are more than the caches hold:
+// past them (8192 tokens of 32 heads: 58 -> 49 us; 16384 of 64: 161 -> 146 us).
+typedef uint32_t words_t __attribute__((ext_vector_type(4)));
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16(const uint16_t *p) {
+    const words_t *w = reinterpret_cast<const words_t *>(p);
+    const words_t v = ONCE ? __builtin_nontemporal_load(w) : *w;
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <bool ONCE>
+__device__ __forceinline__ void store16(uint16_t *p, uint4 u) {
+    words_t *w = reinterpret_cast<words_t *>(p);
+    const words_t v = {u.x, u.y, u.z, u.w};
+    if (ONCE)
+        __builtin_nontemporal_store(v, w);
+    else
+        *w = v;
 }
 
 __device__ __forceinline__ bool finite(float f) {
     return (__builtin_bit_cast(uint32_t, f) & 0x7F800000u) != 0x7F800000u;
 }
 
-template <typename T, int D, bool ADJ>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs p) {
-    constexpr int kUnits = D / 16;
+// Sums up one element: whether it is finite, and the largest finite magnitude.
+__device__ __forceinline__ void take(float x, float &most, bool &ok) {
+    const bool f = finite(x);
+    ok = ok && f;
+    most = fmaxf(most, f ? fabsf(x) : 0.0f);
+}
+
+// A unit's elements x[0..7] of its first chunk and x[8..15] of the second, turned by
+// the table's row of the position (cosines, then sines).
+template <bool ADJ>
+__device__ __forceinline__ void turn_unit(float x[16], int c0, int c1, int rot, const float *row) {
+    const auto turn = [](float &a, float &b, float c, float s) {
+#pragma clang fp contract(off)   // each product and sum is rounded once, as the formula says
+        const float p = a * c - b * s;
+        const float q = b * c + a * s;
+        a = p;
+        b = q;
+    };
+    if (ADJ) {                                         // pairs (2 i, 2 i + 1): four in a chunk
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int at = k ? c1 : c0;
+            if (at >= rot) continue;
+            const float4 c = *reinterpret_cast<const float4 *>(row + at / 2), s = *reinterpret_cast<const float4 *>(row + (rot + at) / 2);
+            turn(x[8 * k], x[8 * k + 1], c.x, s.x);
+            turn(x[8 * k + 2], x[8 * k + 3], c.y, s.y);
+            turn(x[8 * k + 4], x[8 * k + 5], c.z, s.z);
+            turn(x[8 * k + 6], x[8 * k + 7], c.w, s.w);
+        }
+    } else if (c0 < rot / 2) {                         // pairs (i, i + rot / 2): a chunk and the other
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 c = reinterpret_cast<const float4 *>(row + c0)[k], s = reinterpret_cast<const float4 *>(row + rot / 2 + c0)[k];
+            turn(x[4 * k], x[4 * k + 8], c.x, s.x);
+            turn(x[4 * k + 1], x[4 * k + 9], c.y, s.y);
+            turn(x[4 * k + 2], x[4 * k + 10], c.z, s.z);
+            turn(x[4 * k + 3], x[4 * k + 11], c.w, s.w);
+        }
+    }
+}
+
+// kThreads: 256 for prompts, 128 for a few tokens.  kKeys: units of keys that a thread
+// can hold (and half as many tiles of values): 2, or 4 where pages of 128 tokens of
+// 128 elements need it (there 146 -> 140 us against reading them twice; with 4 for
+// pages of 64 the registers cost 45.6 -> 49 us).  Workgroups 0 .. pages - 1 of a
+// (sequence, kv head) take its pages, the others its queries: those are two thirds
+// of a prompt's bytes at four query heads to a kv head, and with them in the pages'
+// workgroups the last round of these was long.
+template <typename T, int D, bool ADJ, int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int pages) {
+    constexpr int U = D / 16;                          // units of a head row
+    constexpr int kValues = kKeys / 2;                 // tiles of values, 4 slots by 8 elements, a thread holds
     __shared__ float red[2][kThreads / 64];
     __shared__ int bad[kMaxPage];
+    __shared__ __align__(16) uint32_t turned[8 * kValues * kThreads + D];    // value codes [D][words + 1], four slots to a word
     const KvView &c = p.c;
     const int tid = threadIdx.x;
     const int h = blockIdx.y, b = blockIdx.z;
@@ -112,59 +161,154 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs p) {
     const int from = max(first, 0);
     const int to = p.rot ? min(s.len, p.rope_positions) : s.len;
     if (from >= to) return;
-    const int j0 = from >> c.log2_page, j1 = (to - 1) >> c.log2_page;
-    for (int j = j0 + blockIdx.x; j <= j1; j += gridDim.x) {
-        const int base = j << c.log2_page;
-        const int lo = max(from, base), hi = min(to, base + P);
-        const int count = hi - lo;
-        const long long row = s.row0 + (lo - first);
-        // queries of this page's tokens and this head's group
-        if (p.q != nullptr) {
-            for (int i = tid; i < count * group * kUnits; i += kThreads) {
-                const int u = i % kUnits, g = (i / kUnits) % group, t = i / (kUnits * group);
-                const int head = h * group + g;
-                const uint16_t *src = p.q + (row + t) * p.q_stride + head * D;
-                uint16_t *dst = p.q_out + ((row + t) * p.q_heads + head) * D;
-                int c0, c1;
-                unit_chunks<ADJ>(u, p.rot, c0, c1);
-                float x[8], y[8];
-                load8<T>(src + c0, x);
-                load8<T>(src + c1, y);
-                rotate_unit<ADJ>(x, y, u, p.rot, p.rope + (long long)(lo + t) * p.rot);
-                *reinterpret_cast<uint4 *>(dst + c0) = pack8<T>(x);
-                *reinterpret_cast<uint4 *>(dst + c1) = pack8<T>(y);
+    if ((int)blockIdx.x >= pages) {
+        if (p.q == nullptr) return;
+        // queries: kTokens tokens at a time, with their rows of the table in LDS; a wave's units lie
+        // side by side, and each thread has kAhead of them on the way
+        constexpr int kTokens = 8 * kThreads / D, kAhead = 4;
+        constexpr bool kOnce = kThreads == 256;
+        float *rows = reinterpret_cast<float *>(turned);
+        const int width = group * U;
+        for (int pos = from + ((int)blockIdx.x - pages) * kTokens; pos < to; pos += ((int)gridDim.x - pages) * kTokens) {
+            const int items = min(kTokens, to - pos) * width;
+            const long long row = s.row0 + (pos - first);
+            uint4 r[kAhead][2];
+            auto load = [&](int i0) {
+#pragma unroll
+                for (int n = 0; n < kAhead; ++n) {
+                    const int i = i0 + tid + n * kThreads;
+                    if (i < items) {
+                        const int t = i / width, g = i % width / U;
+                        int c0, c1;
+                        unit_chunks<D, ADJ>(i % U, p.rot, c0, c1);
+                        const uint16_t *src = p.q + (row + t) * p.q_stride + (h * group + g) * D;
+                        r[n][0] = load16<kOnce>(src + c0);
+                        r[n][1] = load16<kOnce>(src + c1);
+                    }
+                }
+            };
+            load(0);
+            __syncthreads();                           // the rows of the step before are done with
+            if (p.rot) {
+                const float4 *from_row = reinterpret_cast<const float4 *>(p.rope + (long long)pos * p.rot);
+                for (int i = tid; i < items / width * p.rot / 4; i += kThreads) reinterpret_cast<float4 *>(rows)[i] = from_row[i];
+            }
+            __syncthreads();
+            for (int i0 = 0; i0 < items; i0 += kAhead * kThreads) {
+                if (i0 > 0) load(i0);
+#pragma unroll
+                for (int n = 0; n < kAhead; ++n) {
+                    const int i = i0 + tid + n * kThreads;
+                    if (i < items) {
+                        const int t = i / width, g = i % width / U, u = i % U;
+                        int c0, c1;
+                        unit_chunks<D, ADJ>(u, p.rot, c0, c1);
+                        float x[16];
+                        unpack8<T>(r[n][0], x);
+                        unpack8<T>(r[n][1], x + 8);
+                        if (p.rot) turn_unit<ADJ>(x, c0, c1, p.rot, rows + t * p.rot);
+                        uint16_t *dst = p.q_out + ((row + t) * p.q_heads + h * group + g) * D;
+                        store16<kOnce>(dst + c0, pack8<T>(x));
+                        store16<kOnce>(dst + c1, pack8<T>(x + 8));
+                    }
+                }
             }
         }
+        return;
+    }
+    const int j0 = from >> c.log2_page, j1 = (to - 1) >> c.log2_page;
+    for (int j = j0 + blockIdx.x; j <= j1; j += pages) {
+        const int base = j << c.log2_page;
+        const int lo = max(from, base), hi = min(to, base + P);
+        const int count = hi - lo, held = lo - base;   // new tokens; slots that hold tokens from before
+        const int items = count * U;
+        const long long row = s.row0 + (lo - first);
         const int id = c.page_table[(long long)b * c.table_width + j];
         if (id < 0 || id >= c.pages) continue;         // names no page: nothing is appended
         const uint16_t *krow = p.k + row * p.k_stride + h * D;
         const uint16_t *vrow = p.v + row * p.v_stride + h * D;
         for (int i = tid; i < count; i += kThreads) bad[i] = 0;
+        const long long ph = (long long)id * c.kv_heads + h;
+        const float ks0 = c.k_scales[ph], vs0 = c.v_scales[ph];
+
+        // values, in tiles of four slots by eight elements; the page's words that hold new slots
+        const int w0 = held >> 2, w1 = (held + count + 3) >> 2, tiles = (w1 - w0) * (D / 8);
+        // keys and values stay in registers between the passes, if they are few enough
+        const bool once = items <= kKeys * kThreads && tiles <= kValues * kThreads;
+        uint4 vr[kValues][4];
+        auto load_values = [&](int i, uint4 (&r)[4]) {
+            const int u = i % (D / 8), w = w0 + i / (D / 8);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int slot = 4 * w + t - held;
+                r[t] = slot >= 0 && slot < count ? *reinterpret_cast<const uint4 *>(vrow + slot * p.v_stride + 8 * u) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        if (once) {
+#pragma unroll
+            for (int n = 0; n < kValues; ++n)
+                if (tid + n * kThreads < tiles) load_values(tid + n * kThreads, vr[n]);
+        }
+        auto load_keys = [&](int i, uint4 (&r)[2]) {
+            int c0, c1;
+            unit_chunks<D, ADJ>(i % U, p.rot, c0, c1);
+            const uint16_t *src = krow + i / U * p.k_stride;
+            r[0] = *reinterpret_cast<const uint4 *>(src + c0);
+            r[1] = *reinterpret_cast<const uint4 *>(src + c1);
+        };
+        auto rotated = [&](int i, const uint4 (&r)[2], float (&x)[16]) {
+            unpack8<T>(r[0], x);
+            unpack8<T>(r[1], x + 8);
+            int c0, c1;
+            unit_chunks<D, ADJ>(i % U, p.rot, c0, c1);
+            if (p.rot) turn_unit<ADJ>(x, c0, c1, p.rot, p.rope + (long long)(lo + i / U) * p.rot);
+        };
+        uint4 kr[kKeys][2];
+        if (once) {
+#pragma unroll
+            for (int n = 0; n < kKeys; ++n)
+                if (tid + n * kThreads < items) load_keys(tid + n * kThreads, kr[n]);
+        }
         __syncthreads();
         // largest finite magnitudes
         float ka = 0.0f, va = 0.0f;
-        for (int i = tid; i < count * kUnits; i += kThreads) {
-            const int u = i % kUnits, t = i / kUnits;
-            int c0, c1;
-            unit_chunks<ADJ>(u, p.rot, c0, c1);
-            float x[8], y[8];
-            load8<T>(krow + t * p.k_stride + c0, x);
-            load8<T>(krow + t * p.k_stride + c1, y);
-            rotate_unit<ADJ>(x, y, u, p.rot, p.rope + (long long)(lo + t) * p.rot);
+        auto take_keys = [&](int i, const uint4 (&r)[2]) {
+            float x[16];
             bool ok = true;
+            rotated(i, r, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ok = ok && finite(x[e]) && finite(y[e]);
-                ka = fmaxf(ka, fmaxf(finite(x[e]) ? fabsf(x[e]) : 0.0f, finite(y[e]) ? fabsf(y[e]) : 0.0f));
-            }
-            load8<T>(vrow + t * p.v_stride + 16 * u, x);
-            load8<T>(vrow + t * p.v_stride + 16 * u + 8, y);
+            for (int e = 0; e < 16; ++e) take(x[e], ka, ok);
+            if (!ok) bad[i / U] = 1;
+        };
+        if (once) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ok = ok && finite(x[e]) && finite(y[e]);
-                va = fmaxf(va, fmaxf(finite(x[e]) ? fabsf(x[e]) : 0.0f, finite(y[e]) ? fabsf(y[e]) : 0.0f));
+            for (int n = 0; n < kKeys; ++n)
+                if (tid + n * kThreads < items) take_keys(tid + n * kThreads, kr[n]);
+        } else {
+            for (int i = tid; i < items; i += kThreads) {
+                load_keys(i, kr[0]);
+                take_keys(i, kr[0]);
             }
-            if (!ok) bad[t] = 1;
+        }
+        auto take_values = [&](int i, const uint4 (&r)[4]) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                bool ok = true;
+                const uint32_t w[4] = {r[t].x, r[t].y, r[t].z, r[t].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) take(to_float<T>((uint16_t)(w[e / 2] >> (16 * (e & 1)))), va, ok);
+                if (!ok) bad[4 * (w0 + i / (D / 8)) + t - held] = 1;       // (a slot of none is 0, finite)
+            }
+        };
+        if (once) {
+#pragma unroll
+            for (int n = 0; n < kValues; ++n)
+                if (tid + n * kThreads < tiles) take_values(tid + n * kThreads, vr[n]);
+        } else {
+            for (int i = tid; i < tiles; i += kThreads) {
+                load_values(i, vr[0]);
+                take_values(i, vr[0]);
+            }
         }
         for (int m = 32; m > 0; m >>= 1) {
             ka = fmaxf(ka, __shfl_xor(ka, m));
@@ -181,13 +325,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs p) {
             ka = fmaxf(ka, red[0][w]);
             va = fmaxf(va, red[1][w]);
         }
-        const long long ph = (long long)id * c.kv_heads + h;
-        const int held = lo - base;                    // slots that hold tokens from before
-        const float ks0 = c.k_scales[ph], vs0 = c.v_scales[ph];
         float ks = scale_for(ka), vs = scale_for(va);
         if (held > 0) {
             ks = fmaxf(ks, ks0);
             vs = fmaxf(vs, vs0);
+        }
+        if (tid == 0) {                                // (everyone has read the old ones)
+            c.k_scales[ph] = ks;
+            c.v_scales[ph] = vs;
         }
         const float ki = 1.0f / ks, vi = 1.0f / vs;    // exact
         uint8_t *kslab = c.k + ph * P * D;
@@ -201,79 +346,127 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs p) {
                 *w = to_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
             }
         }
-        for (int i = tid; i < count * kUnits; i += kThreads) {
-            const int u = i % kUnits, t = i / kUnits;
+        auto write_keys = [&](int i, const uint4 (&r)[2]) {
+            float x[16];
+            rotated(i, r, x);
+            const int u = i % U, t = i / U;
             int c0, c1;
-            unit_chunks<ADJ>(u, p.rot, c0, c1);
-            float x[8], y[8];
-            load8<T>(krow + t * p.k_stride + c0, x);
-            load8<T>(krow + t * p.k_stride + c1, y);
-            rotate_unit<ADJ>(x, y, u, p.rot, p.rope + (long long)(lo + t) * p.rot);
+            unit_chunks<D, ADJ>(u, p.rot, c0, c1);
             uint32_t w[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
             if (!bad[t]) {
-                w[0] = to_e4m3x4(x[0] * ki, x[1] * ki, x[2] * ki, x[3] * ki);
-                w[1] = to_e4m3x4(x[4] * ki, x[5] * ki, x[6] * ki, x[7] * ki);
-                w[2] = to_e4m3x4(y[0] * ki, y[1] * ki, y[2] * ki, y[3] * ki);
-                w[3] = to_e4m3x4(y[4] * ki, y[5] * ki, y[6] * ki, y[7] * ki);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = to_e4m3x4(x[4 * e] * ki, x[4 * e + 1] * ki, x[4 * e + 2] * ki, x[4 * e + 3] * ki);
             }
             uint8_t *dst = kslab + (held + t) * D;
             *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(w[0], w[1]);
             *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(w[2], w[3]);
+        };
+        if (once) {
+#pragma unroll
+            for (int n = 0; n < kKeys; ++n)
+                if (tid + n * kThreads < items) write_keys(tid + n * kThreads, kr[n]);
+        } else {
+            for (int i = tid; i < items; i += kThreads) {
+                load_keys(i, kr[0]);
+                write_keys(i, kr[0]);
+            }
         }
-        // values: a thread takes eight elements of four slots, one word of each of eight rows
+        // values: eight words of four slots each from a tile
         const bool moved = held > 0 && vs != vs0;
         const float f = vs0 * vi;
-        const int s0 = (moved ? 0 : held) >> 2, s1 = (held + count + 3) >> 2;
-        for (int i = tid; i < (s1 - s0) * (D / 8); i += kThreads) {
-            const int u = i % (D / 8), sg = s0 + i / (D / 8);
-            float x[4][8];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int slot = 4 * sg + t;
-                if (slot >= held && slot < held + count) load8<T>(vrow + (slot - held) * p.v_stride + 8 * u, x[t]);
-            }
+        auto words = [&](int i, const uint4 (&r)[4], auto put) {
+            const int u = i % (D / 8), w = w0 + i / (D / 8);
+            const int live = held + count - 4 * w;     // slots behind the last token stay as they were
+            const bool all = 4 * w >= held && live >= 4;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(vslab + (8 * u + e) * P) + sg;
-                const uint32_t was = (4 * sg >= held && 4 * sg + 4 <= held + count) ? 0u : *w;
+                const uint32_t was = all ? 0u : reinterpret_cast<const uint32_t *>(vslab + (8 * u + e) * P)[w];
                 float o[4], n[4];
                 from_e4m3x4(was, o);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const int slot = 4 * sg + t;
-                    n[t] = slot < held ? (moved ? o[t] * f : o[t]) : slot < held + count ? (finite(x[t][e]) ? x[t][e] * vi : 0.0f) : 0.0f;
+                    const uint32_t v[4] = {r[t].x, r[t].y, r[t].z, r[t].w};
+                    const float x = to_float<T>((uint16_t)(v[e / 2] >> (16 * (e & 1))));
+                    n[t] = 4 * w + t < held ? (moved ? o[t] * f : o[t]) : finite(x) ? x * vi : 0.0f;
                 }
                 const uint32_t now = to_e4m3x4(n[0], n[1], n[2], n[3]);
-                // slots behind the last token stay as they were
-                const int live = held + count - 4 * sg;
                 const uint32_t keep = live >= 4 ? 0u : 0xFFFFFFFFu << (8 * live);
-                *w = (now & ~keep) | (was & keep);
+                put(8 * u + e, w, (now & ~keep) | (was & keep));
+            }
+        };
+        // words that hold old slots only
+        if (moved) {
+            for (int i = tid; i < w0 * D; i += kThreads) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(vslab + (i / w0) * P) + i % w0;
+                float x[4];
+                from_e4m3x4(*w, x);
+                *w = to_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
             }
         }
-        __syncthreads();                               // everyone has read the old scales
-        if (tid == 0) {
-            c.k_scales[ph] = ks;
-            c.v_scales[ph] = vs;
+        if (once && count >= 16) {
+            // by way of LDS, so that sixteen slots of an element go out as one store
+            const int pitch = w1 - w0 + 1;
+#pragma unroll
+            for (int n = 0; n < kValues; ++n)
+                if (tid + n * kThreads < tiles)
+                    words(tid + n * kThreads, vr[n], [&](int d, int w, uint32_t x) { turned[d * pitch + w - w0] = x; });
+            __syncthreads();
+            const int q0 = w0 >> 2, q1 = (w1 + 3) >> 2;
+            for (int i = tid; i < D * (q1 - q0); i += kThreads) {
+                const int d = i / (q1 - q0), q = q0 + i % (q1 - q0);
+                uint32_t *to = reinterpret_cast<uint32_t *>(vslab + d * P) + 4 * q;
+                const int at = d * pitch + 4 * q - w0;
+                if (4 * q >= w0 && 4 * q + 4 <= w1) {
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(turned[at], turned[at + 1], turned[at + 2], turned[at + 3]);
+                } else {
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * q + e >= w0 && 4 * q + e < w1) to[e] = turned[at + e];
+                }
+            }
+        } else {
+            const auto put = [&](int d, int w, uint32_t x) { reinterpret_cast<uint32_t *>(vslab + d * P)[w] = x; };
+            if (once) {
+#pragma unroll
+                for (int n = 0; n < kValues; ++n)
+                    if (tid + n * kThreads < tiles) words(tid + n * kThreads, vr[n], put);
+            } else {
+                for (int i = tid; i < tiles; i += kThreads) {
+                    load_values(i, vr[0]);
+                    words(i, vr[0], put);
+                }
+            }
         }
+        __syncthreads();                               // bad and the words in LDS are free again
     }
 }
 
 template <typename T, int D>
-hipError_t launch(const AppendArgs &p, bool adjacent, int touched, hipStream_t s) {
-    const dim3 grid(touched, p.c.kv_heads, p.c.seqs);
-    if (adjacent)
-        append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(p);
+hipError_t launch(const AppendArgs &p, bool adjacent, bool few, int most, int touched, hipStream_t s) {
+    const int threads = few ? 128 : 256, tokens = 8 * threads / D;       // of a workgroup of queries
+    const dim3 grid(touched + (p.q ? (most + tokens - 1) / tokens : 0), p.c.kv_heads, p.c.seqs);
+    const int elements = D << p.c.log2_page;
+    if (few && adjacent)
+        append_kernel<T, D, true, 128, 2><<<grid, threads, 0, s>>>(p, touched);
+    else if (few)
+        append_kernel<T, D, false, 128, 2><<<grid, threads, 0, s>>>(p, touched);
+    else if (elements > 8192 && elements <= 16384 && adjacent)
+        append_kernel<T, D, true, 256, 4><<<grid, threads, 0, s>>>(p, touched);
+    else if (elements > 8192 && elements <= 16384)
+        append_kernel<T, D, false, 256, 4><<<grid, threads, 0, s>>>(p, touched);
+    else if (adjacent)
+        append_kernel<T, D, true, 256, 2><<<grid, threads, 0, s>>>(p, touched);
     else
-        append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(p);
+        append_kernel<T, D, false, 256, 2><<<grid, threads, 0, s>>>(p, touched);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_dim(const AppendArgs &p, int D, bool adjacent, int touched, hipStream_t s) {
+hipError_t launch_dim(const AppendArgs &p, int D, bool adjacent, bool few, int most, int touched, hipStream_t s) {
     switch (D) {
-    case 64: return launch<T, 64>(p, adjacent, touched, s);
-    case 128: return launch<T, 128>(p, adjacent, touched, s);
-    case 256: return launch<T, 256>(p, adjacent, touched, s);
+    case 64: return launch<T, 64>(p, adjacent, few, most, touched, s);
+    case 128: return launch<T, 128>(p, adjacent, few, most, touched, s);
+    case 256: return launch<T, 256>(p, adjacent, few, most, touched, s);
     }
     return hipErrorInvalidValue;
 }
@@ -291,8 +484,9 @@ hipError_t launch_kv_append(const KvView &c, int head_dim, const uint16_t *q, lo
     // pages that a sequence's rows can touch (the kernel steps on if there are more)
     const int most = max_q < 1 ? 1 : max_q > c.rows ? c.rows : max_q;
     const int touched = most == 1 ? 1 : ((most - 2) >> c.log2_page) + 2;
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, adjacent, touched, s)
-                : launch_dim<half_t>(p, head_dim, adjacent, touched, s);
+    const bool few = (long long)most * head_dim <= 2 * 128 * 16;
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, adjacent, few, most, touched, s)
+                : launch_dim<half_t>(p, head_dim, adjacent, few, most, touched, s);
 }
 
 }  // namespace awq
