@@ -111,7 +111,13 @@ __device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
     }
 }
 
+// A partial result of a chunk of keys, in the workspace: D outputs, the maximum, the
+// sum and (of chunk 0) the number of chunks.
+template <int D>
+constexpr int kPart = D + 4;
+
 // Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
+int prefill_splits(int seqs, int kv_heads, int group, int head_dim, int max_q, long long key_tiles);
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s);
 
 }  // namespace awq

@@ -40,11 +40,6 @@ constexpr int kXcds = 8;
 constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of the formula
 constexpr float kLeastUnit = 0x1p-6f;
 
-// A partial result: D outputs, the maximum, the sum and (of chunk 0) the number of
-// chunks.
-template <int D>
-constexpr int kPart = D + 4;
-
 // How a call is cut into chunks of keys, from the number of (sequence, kv head, row
 // tile) groups and, on the device, from the sequences' lengths.  Measured at 32 heads
 // over 8 of 128 elements, pages of 64 (us):
@@ -424,20 +419,39 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
     }
 }
 
+// Rows of a sequence and kv head from which the prompt kernel takes a call, by the
+// tiles of keys of all sequences and kv heads.  The split kernel reads keys and values
+// again for every sixteen rows, the prompt kernel is slower to start.  Measured (us,
+// split / prompt, 4 query heads to each of 8 kv heads of 128 elements, 20, 32, 64, 96, 128
+// rows): 1 sequence of 500 keys 9 / 15, 9 / 15, 11 / 18, 14 / 19, 14 / 20; of 4000 14 / 19,
+// 14 / 20, 16 / 21, 23 / 22, 27 / 24; of 16k 20 / 22, 21 / 23, 27 / 25, 53 / 27, 63 / 31;
+// 16 of 4000: 34 / 37, 35 / 38, 53 / 48, 82 / 53, 96 / 59; of 16k 122 / 101, 118 / 102, 180 / 111.
+int prompt_rows(long long all_tiles) {
+    return all_tiles >= 16384 ? kRows + 1 : all_tiles >= 2048 ? 64 : all_tiles >= 512 ? 96 : 128;
+}
+
 // The grid of a call: the most chunks, whose number is found on the device, and the
 // workgroups that they are dealt to.
 struct Plan {
+    bool prompt;
     int row_tiles, splits, target;
 };
-Plan plan(int seqs, int kv_heads, int group, int max_q, int max_kv, int window, int sinks) {
+Plan plan(int seqs, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks) {
     Plan pl;
+    long long keys = max_kv;
+    if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
+    const long long tiles = (keys + kTile - 1) / kTile;
+    pl.prompt = (long long)max_q * group >= prompt_rows((long long)seqs * kv_heads * tiles);
+    if (pl.prompt) {
+        pl.row_tiles = pl.target = 0;
+        pl.splits = prefill_splits(seqs, kv_heads, group, head_dim, max_q, tiles);
+        return pl;
+    }
     // (the kernel steps on where the grid is cut)
     const int units = (seqs + kXcds - 1) / kXcds * kXcds;
     pl.row_tiles = (int)std::min<long long>(((long long)max_q * group + kRows - 1) / kRows,
                                             std::max(1, ((1 << 24) - 1) / (units * kv_heads)));
-    long long keys = max_kv;
-    if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
-    const long long tiles = (keys + kTile - 1) / kTile, groups = (long long)seqs * kv_heads * pl.row_tiles;
+    const long long groups = (long long)seqs * kv_heads * pl.row_tiles;
     pl.target = groups <= 64 ? 256 : 512;
     long long want = std::max(8ll, 4 * ((pl.target + groups - 1) / groups));     // lengths may differ by much
     if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
@@ -446,7 +460,18 @@ Plan plan(int seqs, int kv_heads, int group, int max_q, int max_kv, int window, 
 }
 
 template <typename T, int D>
-hipError_t launch(AttnArgs p, const Plan &pl, int max_q, hipStream_t s) {
+hipError_t launch_combine(const AttnArgs &p, int max_q, hipStream_t s) {
+    combine_kernel<T, D><<<dim3(max_q * p.q_heads, p.c.seqs), 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch(AttnArgs p, const Plan &pl, bool bf16, int max_q, hipStream_t s) {
+    if (pl.prompt) {
+        const hipError_t e = launch_attention_prefill(p, D, bf16, max_q, s);
+        if (e != hipSuccess || p.part == nullptr) return e;
+        return launch_combine<T, D>(p, max_q, s);
+    }
     const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
     const int grid = units * p.c.kv_heads * pl.row_tiles;
     const int page = 1 << p.c.log2_page;
@@ -456,32 +481,26 @@ hipError_t launch(AttnArgs p, const Plan &pl, int max_q, hipStream_t s) {
         split_kernel<T, D, kLarge><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
     else
         split_kernel<T, D, kSmall><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.part == nullptr) return e;
-    combine_kernel<T, D><<<dim3(max_q * p.q_heads, p.c.seqs), 256, 0, s>>>(p);
-    return hipGetLastError();
+    return launch_combine<T, D>(p, max_q, s);
 }
 
 template <typename T>
-hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, int max_q, hipStream_t s) {
+hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, bool bf16, int max_q, hipStream_t s) {
     switch (D) {
-    case 64: return launch<T, 64>(p, pl, max_q, s);
-    case 128: return launch<T, 128>(p, pl, max_q, s);
-    case 256: return launch<T, 256>(p, pl, max_q, s);
+    case 64: return launch<T, 64>(p, pl, bf16, max_q, s);
+    case 128: return launch<T, 128>(p, pl, bf16, max_q, s);
+    case 256: return launch<T, 256>(p, pl, bf16, max_q, s);
     }
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-// Rows of a sequence and kv head from which the prompt kernel takes the call.
-constexpr int kPrefillRows = 128;
-bool prefill_rows(int group, int max_q) { return (long long)max_q * group >= kPrefillRows; }
-
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
                            int max_kv, int window, int sinks) {
-    if (prefill_rows(q_heads / kv_heads, max_q)) return 0;
-    const Plan pl = plan(seqs, kv_heads, q_heads / kv_heads, max_q, max_kv, window, sinks);
+    const Plan pl = plan(seqs, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks);
     if (pl.splits == 1) return 0;
     return (size_t)rows * q_heads * pl.splits * (head_dim + 4) * sizeof(float);
 }
@@ -489,11 +508,10 @@ size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int he
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
                             int max_q, int max_kv, void *workspace, hipStream_t s) {
-    const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, max_q, max_kv, window, sinks);
+    const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
     AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
                q_heads / c.kv_heads, scale * kLog2e, window, sinks, pl.splits, pl.target};
-    if (prefill_rows(p.group, max_q)) return launch_attention_prefill(p, head_dim, bf16, max_q, s);
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, max_q, s) : launch_dim<half_t>(p, head_dim, pl, max_q, s);
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, bf16, max_q, s) : launch_dim<half_t>(p, head_dim, pl, bf16, max_q, s);
 }
 
 }  // namespace awq

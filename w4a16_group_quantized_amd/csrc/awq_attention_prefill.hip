@@ -25,6 +25,10 @@ namespace awq {
 namespace {
 
 constexpr int kRows = 128, kWaveRows = 32, kWaves = 4;
+// Least tiles of a chunk, most chunks of a row tile.  5 rows of 32 heads over 16k, 4k and
+// 500 keys, one sequence: 33 / 38 / 16 us at 16 tiles, 23 / 22 / 16 at 8, 21 / 17 / 14 at 4;
+// 16 sequences of 500: 17 / 17 / 21.
+constexpr int kLeastChunk = 6, kMostSplits = 32;
 constexpr float kWeightBits = 11.0f, kSlack = 4.0f, kLeastUnit = 0x1p-6f;
 
 template <int N>
@@ -58,7 +62,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     const KvView &c = p.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 31, hf = lane >> 5;
-    const int h = blockIdx.x % c.kv_heads, slot = blockIdx.x / c.kv_heads;
+    const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.splits;
+    const int slot = blockIdx.x / (c.kv_heads * p.splits);
     const int b = seq_of_rank(c, slot / tiles_per_seq);
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
@@ -86,7 +91,11 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
     for (int rt = row_tiles - 1 - slot % tiles_per_seq; rt >= 0; rt -= tiles_per_seq) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
-        const int count = tiles.count();
+        // this workgroup's chunk of them
+        const int every = tiles.count(), chunks = max(1, min(p.splits, every / kLeastChunk));
+        if (split >= chunks) continue;
+        const int start = (int)((long long)every * split / chunks);
+        const int count = (int)((long long)every * (split + 1) / chunks) - start;
         // the wave's rows, and the lane's
         const int w0 = min(r0 + wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
         const bool idle = r0 + wave * kWaveRows > r1;
@@ -129,11 +138,11 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
         float ks_l = 1.0f, vs_l = 0.0f;
         uint64_t has = 0;
         auto page_of = [&](int i) {
-            const int j = tiles.at(min(i, count - 1)) * kTile + (BIG ? 0 : 16 * gv);
+            const int j = tiles.at(start + min(i, count - 1)) * kTile + (BIG ? 0 : 16 * gv);
             return j < s.len ? table[j >> c.log2_page] : -1;
         };
         auto issue = [&](int i, uint4 *kb, uint4 *vb) {
-            const int j0 = tiles.at(i) * kTile;
+            const int j0 = tiles.at(start + i) * kTile;
             const int want = BIG ? __builtin_amdgcn_readfirstlane(next_id) : next_id;
             const bool ok = (uint32_t)want < (uint32_t)c.pages;
             const int id = ok ? want : 0;
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                     issue(i + 1, kn, vn);
                     next_id = page_of(i + 2);
                 }
-                const int j0 = tiles.at(i) * kTile;
+                const int j0 = tiles.at(start + i) * kTile;
                 if ((ok & 15) != 15 || j0 + kTile > s.len) clear_dead(j0, vb, ok);
                 if (!idle && j0 <= hi) multiply(j0, kb, vb, ksl, vsl, ok);
             };
@@ -309,17 +318,34 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
         }
         l = half_sum(l);
         if (!idle && w0 + m <= r1) {
-            const float inv = l > 0.0f || !(l == l) ? unit / l : 0.0f;
-            uint16_t *dst = p.out + ((long long)(s.row0 + token) * p.q_heads + head) * D + 4 * hf;
+            const long long at = (long long)(s.row0 + token) * p.q_heads + head;
+            if (chunks > 1) {
+                float *dst = p.part + (at * p.splits + split) * kPart<D> + 4 * hf;
 #pragma unroll
-            for (int e = 0; e < kP; ++e)
+                for (int e = 0; e < kP; ++e)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint2 y;
-                    y.x = (uint32_t)from_float<T>(o[e][4 * u] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 1] * inv) << 16);
-                    y.y = (uint32_t)from_float<T>(o[e][4 * u + 2] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 3] * inv) << 16);
-                    *reinterpret_cast<uint2 *>(dst + 32 * e + 8 * u) = y;
+                    for (int u = 0; u < 4; ++u)
+                        *reinterpret_cast<float4_t *>(dst + 32 * e + 8 * u) =
+                            float4_t{o[e][4 * u], o[e][4 * u + 1], o[e][4 * u + 2], o[e][4 * u + 3]} * unit;
+                if (hf == 0) {
+                    dst[D] = mx;
+                    dst[D + 1] = l;
+                    dst[D + 2] = (float)chunks;
                 }
+            } else {
+                if (p.part != nullptr && hf == 0) p.part[at * p.splits * kPart<D> + D + 2] = 1.0f;
+                const float inv = l > 0.0f || !(l == l) ? unit / l : 0.0f;
+                uint16_t *dst = p.out + at * D + 4 * hf;
+#pragma unroll
+                for (int e = 0; e < kP; ++e)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        uint2 y;
+                        y.x = (uint32_t)from_float<T>(o[e][4 * u] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 1] * inv) << 16);
+                        y.y = (uint32_t)from_float<T>(o[e][4 * u + 2] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 3] * inv) << 16);
+                        *reinterpret_cast<uint2 *>(dst + 32 * e + 8 * u) = y;
+                    }
+            }
         }
         __syncthreads();                       // the buffers are free again
     }
@@ -344,7 +370,21 @@ hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hip
     return hipGetLastError();
 }
 
+// Row tiles of a sequence that the grid has.
+int prefill_tiles(int seqs, int kv_heads, int group, int max_q) {
+    const long long tiles = ((long long)max_q * group + kRows - 1) / kRows;
+    return (int)std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * kv_heads * seqs));
+}
+
 }  // namespace
+
+// Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a
+// CU, one with 256 elements).
+int prefill_splits(int seqs, int kv_heads, int group, int head_dim, int max_q, long long key_tiles) {
+    const long long groups = (long long)seqs * kv_heads * prefill_tiles(seqs, kv_heads, group, max_q);
+    const long long room = (head_dim > 128 ? 256 : 512) / groups;
+    return (int)std::max<long long>(1, std::min<long long>({room, key_tiles / kLeastChunk, kMostSplits}));
+}
 
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s) {
     // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
@@ -352,10 +392,8 @@ hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, 
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
     // the grid is cut.
-    const int pairs = p.c.kv_heads * p.c.seqs;                                   // below 2^24
-    const long long tiles = ((long long)max_q * p.group + kRows - 1) / kRows;
-    const int tiles_per_seq = (int)std::min<long long>(tiles, ((1 << 24) - 1) / pairs);
-    const int grid = pairs * tiles_per_seq;
+    const int tiles_per_seq = prefill_tiles(p.c.seqs, p.c.kv_heads, p.group, max_q);
+    const int grid = p.c.kv_heads * p.c.seqs * tiles_per_seq * p.splits;
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, tiles_per_seq, s)
                 : launch_dim<half_t>(p, head_dim, grid, tiles_per_seq, s);
 }
