@@ -73,6 +73,26 @@ def test_long_split(new):
     check(kc.Batch(5, "bf16", [new], [9001], 16, 2, 64, 16).fill(), window=8000, sinks=70)
 
 
+@pytest.mark.parametrize("dim,page,heads", [(256, 64, (4, 2)), (128, 16, (5, 1)), (64, 256, (8, 1))])
+@pytest.mark.parametrize("new", [1, 40, 130])
+def test_long_split_of_other_shapes(dim, page, heads, new):
+    check(kc.Batch(18, "bf16", [new, 3], [3001, 2500], *heads, dim, page).fill())
+    check(kc.Batch(19, "fp16", [new], [3001], *heads, dim, page).fill(), window=2000, sinks=130)
+
+
+@pytest.mark.parametrize("dim,heads", [(64, (10, 2)), (128, (4, 1)), (256, (6, 2))])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("window", [0, 100])
+def test_few_rows_of_a_call_that_may_be_long(dim, heads, page, window):
+    """A wide page table and a large max_kv choose the kernels of long calls, and most of
+    their chunks turn out empty."""
+    t = kc.Batch(22, "fp16", [9, 1, 0, 30], [900, 64, 5, 31], *heads, dim, page).fill()
+    t.width = (1 << 20) // page
+    t.table = torch.cat([t.table, torch.full((4, t.width - t.table.shape[1]), -1, dtype=torch.int32)], 1)
+    check(t, max_kv=1 << 20, window=window, sinks=7)
+    check(t, max_q=1, max_kv=1 << 20, window=window, sinks=7)
+
+
 @pytest.mark.parametrize("new", [[1, 1, 1], [20, 3, 7], [150, 200, 90]])
 @pytest.mark.parametrize("max_q,max_kv", [(1, 1), (0, 0), (3, 10), (10 ** 6, 10 ** 6)])
 def test_wrong_hints(new, max_q, max_kv):

@@ -508,15 +508,17 @@ class KvCache:
             if getattr(self, name).device != self.k.device:
                 raise ValueError(f"{name} is on {getattr(self, name).device}, k on {self.k.device}")
         ptr = [_dev(getattr(self, n), getattr(self, n).dtype, n) for n in ("k", "v", "k_scales", "v_scales")]
-        object.__setattr__(self, "_c", CKvCache(*ptr, pages, page, heads, dim))
+        for name, value in (("_c", CKvCache(*ptr, pages, page, heads, dim)), ("_heads", heads), ("_dim", dim),
+                            ("_device", self.k.device)):
+            object.__setattr__(self, name, value)
 
     @property
     def kv_heads(self) -> int:
-        return self._c.kv_heads
+        return self._heads
 
     @property
     def head_dim(self) -> int:
-        return self._c.head_dim
+        return self._dim
 
     @property
     def device(self) -> torch.device:
@@ -560,29 +562,38 @@ class KvBatch:
                 raise ValueError(f"{name} must be in [0, 2^31), got {getattr(self, name)}")
         ptr = [_dev(getattr(self, n), torch.int32, n) for n in ("page_table", "kv_lens", "q_starts")]
         object.__setattr__(self, "_args", (*ptr, seqs, width))
+        object.__setattr__(self, "_device", self.page_table.device)
 
     def _c(self, rows: int) -> CKvBatch:
         return CKvBatch(*self._args, rows, self.max_q, self.max_kv)
 
 
-def _rows(t: torch.Tensor, heads: int | None, like: torch.Tensor, cache: KvCache, name: str):
+def _rows(t: torch.Tensor, rows: int, heads: int, dtype: torch.dtype, cache: KvCache, name: str):
     """(address, elements from row to row) of rows [rows][heads][head_dim] that may be
     a slice of wider rows."""
-    if t.dim() != 3 or t.shape[2] != cache._c.head_dim or (heads is not None and t.shape[1] != heads) or \
-            t.shape[0] != like.shape[0]:
-        raise ValueError(f"{name} must be [{like.shape[0]}][{'heads' if heads is None else heads}]"
-                         f"[{cache._c.head_dim}], got {list(t.shape)}")
-    if t.dtype not in ROW_TYPES or t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {'fp16 or bf16' if t is like else like.dtype}, got {t.dtype}")
-    if t.device != cache.k.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
-    rows, width = t.shape[0], t.shape[1] * t.shape[2]
-    s = t.stride()
-    if s[2] != 1 or (t.shape[1] > 1 and s[1] != t.shape[2]):
+    shape, step, dim = t.shape, t.stride(), cache._dim
+    if len(shape) != 3 or shape[0] != rows or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [{rows}][{heads}][{dim}], got {list(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != cache._device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache._device}")
+    if step[2] != 1 or (heads > 1 and step[1] != dim):
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if rows > 1 and not 0 <= s[0] < 1 << 31:
+    if rows <= 1:
+        return t.data_ptr(), heads * dim
+    if not 0 <= step[0] < 1 << 31:
         raise ValueError(f"{name}: rows too far apart")
-    return t.data_ptr(), s[0] if rows > 1 else width
+    return t.data_ptr(), step[0]
+
+
+def _kv_out(out: torch.Tensor | None, q: torch.Tensor, stream) -> torch.Tensor:
+    """A dense output like q, or ``out`` if it is one."""
+    if out is None:
+        return _new(q.shape, q.dtype, q.device, stream)
+    if out.shape != q.shape or out.device != q.device:
+        raise ValueError(f"out must be {list(q.shape)} on {q.device}, got {list(out.shape)} on {out.device}")
+    return out
 
 
 def _kv_call(device: torch.device, stream, fn, *args):
@@ -598,16 +609,21 @@ def _kv_call(device: torch.device, stream, fn, *args):
         _check(status)
 
 
-def _on(batch: KvBatch, cache: KvCache):
-    if batch.page_table.device != cache.k.device:
-        raise ValueError(f"the batch is on {batch.page_table.device}, the cache on {cache.k.device}")
+def _kv_type(t: torch.Tensor, batch: KvBatch, cache: KvCache, name: str) -> int:
+    """AWQ_TYPE_* of rows, after checking that batch and cache sit on one device."""
+    if batch._device != cache._device:
+        raise ValueError(f"the batch is on {batch._device}, the cache on {cache._device}")
+    if t.dtype not in ROW_TYPES or t.dim() != 3:
+        raise TypeError(f"{name} must be fp16 or bf16 [rows][heads][{cache._dim}], got {t.dtype} {list(t.shape)}")
+    return ROW_TYPES[t.dtype]
 
 
 def _heads(q: torch.Tensor, cache: KvCache) -> int:
-    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache._c.kv_heads:
-        raise ValueError(f"q must be [rows][heads][{cache._c.head_dim}] with a multiple of "
-                         f"{cache._c.kv_heads} heads, got {list(q.shape)}")
-    return q.shape[1]
+    heads = q.shape[1] if q.dim() == 3 else 0
+    if heads < 1 or heads % cache._heads:
+        raise ValueError(f"q must be [rows][heads][{cache._dim}] with a multiple of {cache._heads} heads, "
+                         f"got {list(q.shape)}")
+    return heads
 
 
 def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatch,
@@ -617,18 +633,16 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
     values into the cache.  q [rows][q_heads][head_dim] (or None), k and v
     [rows][kv_heads][head_dim], fp16 or bf16, rows at any stride; rope fp32
     [positions][rot_dim] (cosines, then sines) or None.  Returns the rotated q."""
-    _on(batch, cache)
-    kp, ks = _rows(k, cache._c.kv_heads, k, cache, "k")
-    vp, vs = _rows(v, cache._c.kv_heads, k, cache, "v")
+    kind = _kv_type(k, batch, cache, "k")
+    rows, heads = k.shape[0], cache._heads
+    kp, ks = _rows(k, rows, heads, k.dtype, cache, "k")
+    vp, vs = _rows(v, rows, heads, k.dtype, cache, "v")
     qp = op = None
-    qs, heads = 0, cache._c.kv_heads
+    qs = 0
     if q is not None:
         heads = _heads(q, cache)
-        qp, qs = _rows(q, heads, k, cache, "q")
-        if out is None:
-            out = _new(tuple(q.shape), q.dtype, q.device, stream)
-        elif tuple(out.shape) != tuple(q.shape) or out.device != q.device:
-            raise ValueError(f"out must be {list(q.shape)} on {q.device}, got {list(out.shape)} on {out.device}")
+        qp, qs = _rows(q, rows, heads, k.dtype, cache, "q")
+        out = _kv_out(out, q, stream)
         op = _dev(out, q.dtype, "out")
     rp, positions, rot = None, 0, 0
     if rope is not None:
@@ -636,9 +650,8 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
             raise ValueError(f"rope must be [positions][rot_dim] on {k.device}, got {list(rope.shape)} on {rope.device}")
         rp = _dev(rope, torch.float32, "rope")
         positions, rot = rope.shape
-    b = batch._c(k.shape[0])
-    _kv_call(k.device, stream, load().awq_kv_append, qp, qs, kp, ks, vp, vs, op, heads, ROW_TYPES[k.dtype],
-             rp, positions, rot, int(interleaved), cache._c, b)
+    _kv_call(cache._device, stream, load().awq_kv_append, qp, qs, kp, ks, vp, vs, op, heads, kind, rp, positions,
+             rot, int(interleaved), cache._c, batch._c(rows))
     return out
 
 
@@ -654,24 +667,23 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
     their own keys and values already: causal, and with ``window`` > 0 only over the
     last ``window`` tokens and the first ``sinks``.  scale: 1 / sqrt(head_dim) unless
     given.  The workspace is allocated here unless one is given."""
-    _on(batch, cache)
-    heads = _heads(q, cache)
-    qp, qs = _rows(q, heads, q, cache, "q")
+    kind = _kv_type(q, batch, cache, "q")
+    rows, heads = q.shape[0], _heads(q, cache)
+    qp, qs = _rows(q, rows, heads, q.dtype, cache, "q")
     if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
         raise ValueError(f"window and sinks must be in [0, 2^31), got {window}, {sinks}")
-    if out is None:
-        out = _new(tuple(q.shape), q.dtype, q.device, stream)
-    elif tuple(out.shape) != tuple(q.shape) or out.device != q.device:
-        raise ValueError(f"out must be {list(q.shape)} on {q.device}, got {list(out.shape)} on {out.device}")
+    out = _kv_out(out, q, stream)
     op = _dev(out, q.dtype, "out")
-    lib = load()
-    b = batch._c(q.shape[0])
+    lib, c, b = load(), cache._c, batch._c(rows)
     if workspace is None:
-        nbytes = lib.awq_attention_workspace_bytes(heads, window, sinks, cache._c, b)
+        nbytes = lib.awq_attention_workspace_bytes(heads, window, sinks, c, b)
         if nbytes:
             workspace = _new(nbytes, torch.uint8, q.device, stream)
-    wp, wn = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    scale = cache._c.head_dim ** -0.5 if scale is None else scale
-    _kv_call(q.device, stream, lib.awq_attention, qp, qs, op, heads, ROW_TYPES[q.dtype], scale, window, sinks,
-             cache._c, b, wp, wn)
+    wp, wn = None, 0
+    if workspace is not None:
+        wp, wn = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+        if workspace.device != cache._device:
+            raise ValueError(f"workspace is on {workspace.device}, the cache on {cache._device}")
+    _kv_call(cache._device, stream, lib.awq_attention, qp, qs, op, heads, kind,
+             cache._dim ** -0.5 if scale is None else scale, window, sinks, c, b, wp, wn)
     return out

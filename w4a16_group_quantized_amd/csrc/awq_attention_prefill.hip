@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                     }
                 }
             }
+            // (read here, they are there when the weights are: 1 to 2%)
+            uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
             // The scales of the tile's four groups of sixteen keys (with BIG all the same) and, of the
             // lane's two groups, the keys' scale and what the values' is to the outputs' unit.
             float ks[2], top[2], vs[4], bits[2], back[2];
@@ -276,7 +278,6 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                 }
                 l += sum * back[u];
             }
-            uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
 #pragma unroll
             for (int e = 0; e < kP; ++e) {
                 const uint4 a0 = v0, a1 = v1;
@@ -373,7 +374,8 @@ hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hip
 // Row tiles of a sequence that the grid has.
 int prefill_tiles(int seqs, int kv_heads, int group, int max_q) {
     const long long tiles = ((long long)max_q * group + kRows - 1) / kRows;
-    return (int)std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * kv_heads * seqs));
+    const long long pairs = (long long)kv_heads * seqs;                          // below 2^20
+    return (int)std::max<long long>(1, std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * pairs)));
 }
 
 }  // namespace
