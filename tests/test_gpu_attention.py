@@ -11,7 +11,7 @@ from w4a16_group_quantized_amd import binding
 pytestmark = pytest.mark.gpu
 
 
-def check(t, scale=None, window=0, sinks=0, max_q=None, max_kv=None):
+def check(t, scale=None, window=0, sinks=0, max_q=None, max_kv=None, exact_scores=False):
     cache, batch, q, _, _ = t.device(max_q, max_kv)
     out = torch.full(q.shape, 7.0, dtype=t.dtype, device="cuda:0")
     need = binding.attention_workspace_bytes(q.shape[0], t.q_heads, cache, batch, window, sinks)
@@ -25,7 +25,7 @@ def check(t, scale=None, window=0, sinks=0, max_q=None, max_kv=None):
     assert torch.equal(got[n:], torch.full_like(got[n:], 7.0))       # rows of no sequence
     have, want = got[:n].double(), want[:n]
     assert torch.equal(have.isnan(), want.isnan())
-    tol = kc.attention_tolerance(t, want, size[:n], reach[:n])
+    tol = kc.attention_tolerance(t, want, size[:n], reach[:n] * (not exact_scores))
     off = ((have - want).abs() - tol).nan_to_num(0.0)
     at = int(off.argmax()) if off.numel() else 0
     assert not off.numel() or float(off.max()) <= 0, (at, float(have.flatten()[at]), float(want.flatten()[at]))
@@ -166,6 +166,31 @@ def test_scale_argument_and_types_of_any_size():
     t.x.mul_(2.0 ** 60)                    # bf16 beyond fp16's range: peaked to one key
     t.ks.mul_(2.0 ** -60)
     check(t)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("page,new,lens", [(64, [1, 1], [300, 40]), (16, [5, 2], [200, 70]), (64, [140], [300]),
+                                           (16, [90, 40], [90, 150])])
+def test_scores_of_any_size(dtype, page, new, lens):
+    """Scores q k of one product, a power of two and its half: equal ones get equal weights
+    whatever fp32 makes of them, and the others are 2^16 and more below: no weight.  So
+    nothing of the scores' size comes into the tolerance."""
+    t = kc.Batch(23, dtype, new, lens, 4, 2, 64, page).fill()
+    code = lambda f: torch.tensor(f).to(kc.F8).view(torch.uint8)  # noqa: E731
+    t.k.zero_()
+    t.k[..., 0] = torch.where(torch.rand(t.k.shape[:3], generator=t.g) < 0.1, code(1.0), code(0.5))
+    t.x.zero_()
+    t.x.view(-1, t.dim)[:, 0] = 2.0 ** 10
+    for level in [*range(17, 34), 60, 110]:
+        t.ks.fill_(2.0 ** (level - 10))
+        check(t, scale=1.0, exact_scores=True)
+        check(t, scale=-1.0, exact_scores=True)
+
+
+@pytest.mark.parametrize("new,lens", [([9], [4]), ([70], [20]), ([300], [130])])
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1])
+def test_widest_window_over_rows_without_a_place(new, lens, window):
+    check(kc.Batch(24, "fp16", new, lens, 4, 2, 64, 16).fill(), window=window)
 
 
 def test_same_bits_twice_and_on_a_side_stream():

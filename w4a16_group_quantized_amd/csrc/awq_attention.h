@@ -7,7 +7,11 @@
 namespace awq {
 
 constexpr int kTile = 64;                  // keys of a tile
-constexpr float kEmpty = -1e30f;           // running maximum of a row that has seen no key
+constexpr float kEmpty = -0x1.fffffep127f; // running maximum of a row that has seen no key
+// From here on a maximum is taken off the scores before anything is added: its steps are
+// half an exponent's and more, and a sum with it would lose the rest.
+constexpr float kFar = 0x1p23f;
+constexpr int kWidest = 1 << 30;           // a window of this many tokens sees all: no position is past it
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttnArgs {

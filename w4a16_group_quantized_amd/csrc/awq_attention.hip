@@ -273,7 +273,13 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
                 mx = now;
             }
             const float ratio = vs > 0.0f ? vs / unit : 1.0f;         // (no weight where there is no page)
-            const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - mx;
+            float shift = mx;
+            if (__any(fabsf(mx) >= kFar)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] -= mx;
+                shift = 0.0f;
+            }
+            const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - shift;
             float sum = 0.0f;
             half8_t ph[2], pl[2];
 #pragma unroll
@@ -510,7 +516,7 @@ hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, lo
                             int max_q, int max_kv, void *workspace, hipStream_t s) {
     const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
     AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
-               q_heads / c.kv_heads, scale * kLog2e, window, sinks, pl.splits, pl.target};
+               q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, pl.splits, pl.target};
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, bf16, max_q, s) : launch_dim<half_t>(p, head_dim, pl, bf16, max_q, s);
 }
 

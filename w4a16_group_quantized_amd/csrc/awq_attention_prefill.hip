@@ -265,10 +265,21 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
                 bits[u] = __builtin_amdgcn_logf(ratio);
                 back[u] = 1.0f / ratio;
             }
+            float shift = mx;
+            if (__any(fabsf(mx) >= kFar)) {
+#pragma clang fp contract(off)   // the products as the maximum was taken of them
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[u][e] = acc[u][e] * ks[u] - mx;
+                    ks[u] = 1.0f;
+                }
+                shift = 0.0f;
+            }
             half8_t w[2][2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float base = kWeightBits + bits[u] - mx;
+                const float base = kWeightBits + bits[u] - shift;
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
