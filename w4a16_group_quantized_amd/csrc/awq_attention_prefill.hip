@@ -1,7 +1,7 @@
 // awq_attention for many rows (prompts, chunks of prompts): see
 // awq_attention.hip for the formula and the transposed products.
 //
-// A workgroup of four waves takes 128 rows (row r of a kv head: token r / group,
+// A workgroup of four waves takes 128 rows (64 with heads of 256; row r of a kv head: token r / group,
 // head r % group) of one kv head and one sequence, 32 to a wave, and goes once
 // over the keys in tiles of 64, held in LDS as codes: 64 D bytes of keys and as
 // many of values, loaded straight into LDS, the next tile while this one is
@@ -11,6 +11,21 @@
 // 16 (m / 4 % 2) + 4 (m / 8) + m % 4, so that lane half hf ends up with the
 // sixteen consecutive keys 16 hf .. 16 hf + 15 of it, one 16-byte piece of a row
 // of V^T.  Pieces are stored xor-swizzled by their row: no bank conflicts.
+//
+// Heads of 256 elements: queries, outputs and scores of 32 rows are 224 registers of
+// a wave, which leaves one wave to a SIMD and nothing beside its vector instructions
+// while its products run, and the other way round.  There two waves share 32 rows (a
+// workgroup has 64): each has the scores of 32 of a tile's 64 keys and sums up one half
+// of the outputs; the rows' maxima and the weights go from one to the other through LDS, lane
+// by lane as they lie.  A tile's scores run beside the outputs of the tile before, so
+// two barriers a tile do.  Two waves to a SIMD: 8192 rows under a window of 1024, 250
+// -> 191 us (680 TFLOP/s).  With 128 elements, where two waves fit as it is, 163 against
+// 180 us on 4096 rows: not there.
+//
+// Bound: vector instructions (half of the issue slots; the codes' conversion is a third
+// of them) and matrix instructions, which overlap in part, under the power limit.
+//
+// Few row tiles over many keys are cut into chunks of keys, joined by combine_kernel.
 //
 // Weights are rounded to fp16 once; the sum takes them before the rounding.
 // They are scaled by 2^11 so that small ones stay normal numbers, and the
@@ -24,12 +39,16 @@
 namespace awq {
 namespace {
 
-constexpr int kRows = 128, kWaveRows = 32, kWaves = 4;
+constexpr int kWaveRows = 32, kWaves = 4;
 // Least tiles of a chunk, most chunks of a row tile.  5 rows of 32 heads over 16k, 4k and
 // 500 keys, one sequence: 33 / 38 / 16 us at 16 tiles, 23 / 22 / 16 at 8, 21 / 17 / 14 at 4;
 // 16 sequences of 500: 17 / 17 / 21.
 constexpr int kLeastChunk = 6, kMostSplits = 32;
 constexpr float kWeightBits = 11.0f, kSlack = 4.0f, kLeastUnit = 0x1p-6f;
+
+// Heads of 256 elements: two waves share 32 rows.  Elsewhere a wave has 32 rows to itself.
+constexpr bool in_pairs(int head_dim) { return head_dim > 128; }
+constexpr int rows_of(int head_dim) { return kWaveRows * (in_pairs(head_dim) ? kWaves / 2 : kWaves); }
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -54,14 +73,21 @@ __device__ __forceinline__ int piece(int row, int at) {
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
 template <typename T, int D, bool BIG>
-__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {
+__global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
+    constexpr bool kPairs = in_pairs(D);
+    constexpr int kRows = rows_of(D);          // rows of a workgroup
+    constexpr int kO = kPairs ? kP / 2 : kP;   // 32-element blocks of a value that a wave sums up
     constexpr int kLoads = D / 64;             // loads of a wave for the keys of a tile, and for the values
+    __shared__ uint4 weights[kWaves][2][64];   // (with pairs)
+    __shared__ float tops[kWaves][64];
     __shared__ uint4 kbuf0[kTile * kC], vbuf0[kTile * kC], kbuf1[kTile * kC], vbuf1[kTile * kC];
     const KvView &c = p.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 31, hf = lane >> 5;
+    // with pairs: which 32 keys of a tile, and which half of the outputs, are the wave's
+    const int side = kPairs ? wave & 1 : 0, row_wave = kPairs ? wave >> 1 : wave;
     const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.splits;
     const int slot = blockIdx.x / (c.kv_heads * p.splits);
     const int b = seq_of_rank(c, slot / tiles_per_seq);
@@ -97,8 +123,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
         const int start = (int)((long long)every * split / chunks);
         const int count = (int)((long long)every * (split + 1) / chunks) - start;
         // the wave's rows, and the lane's
-        const int w0 = min(r0 + wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
-        const bool idle = r0 + wave * kWaveRows > r1;
+        const int w0 = min(r0 + row_wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
+        const bool idle = r0 + row_wave * kWaveRows > r1;
         const int lo = s.first() + w0 / p.group, hi = s.first() + w1 / p.group;
         const int r = min(w0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
@@ -128,9 +154,9 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             for (int e = 0; e < 2; ++e) qf[i][e] = as_row_half<T>(qrow + 32 * i + 8 * e, up);
 
         float mx = kEmpty, l = 0.0f, unit = 1.0f;
-        float16_t o[kP];
+        float16_t o[kO];
 #pragma unroll
-        for (int i = 0; i < kP; ++i) o[i] = float16_t{};
+        for (int i = 0; i < kO; ++i) o[i] = float16_t{};
 
         // Page numbers run two tiles ahead and scales one, a sixteen-key group to a lane
         // (group g in lane g): page_of() asks, issue() loads a tile's codes and scales.
@@ -141,7 +167,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             const int j = tiles.at(start + min(i, count - 1)) * kTile + (BIG ? 0 : 16 * gv);
             return j < s.len ? table[j >> c.log2_page] : -1;
         };
-        auto issue = [&](int i, uint4 *kb, uint4 *vb) {
+        const uint8_t *v_from = nullptr;       // the next tile's values, as this lane loads them
+        auto issue_keys = [&](int i, uint4 *kb) {
             const int j0 = tiles.at(start + i) * kTile;
             const int want = BIG ? __builtin_amdgcn_readfirstlane(next_id) : next_id;
             const bool ok = (uint32_t)want < (uint32_t)c.pages;
@@ -151,12 +178,11 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             ks_l = c.k_scales[ph];             // (of page 0 where there is none: used for no key)
             vs_l = c.v_scales[ph];
             const int in_page = j0 & (P - 1);
+            v_from = c.v + ph * slab + in_page;
             if constexpr (BIG) {
-                const uint8_t *kp = c.k + ph * slab + in_page * D, *vp = c.v + ph * slab + in_page;
+                const uint8_t *kp = c.k + ph * slab + in_page * D;
 #pragma unroll
                 for (int n = 0; n < kLoads; ++n) to_lds16(kp + koff[n], kb + (wave * kLoads + n) * 64);
-#pragma unroll
-                for (int n = 0; n < kLoads; ++n) to_lds16(vp + voff[n], vb + (wave * kLoads + n) * 64);
                 return;
             }
             const int id0 = __builtin_amdgcn_readlane(id, wave & 2), id1 = __builtin_amdgcn_readlane(id, (wave & 2) + 1);
@@ -164,9 +190,10 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
 #pragma unroll
             for (int n = 0; n < kLoads; ++n)
                 to_lds16(c.k + (kodd[n] ? page1 : page0) + in_page * D + koff[n], kb + (wave * kLoads + n) * 64);
+        };
+        auto issue_values = [&](uint4 *vb) {
 #pragma unroll
-            for (int n = 0; n < kLoads; ++n)
-                to_lds16(c.v + ph * slab + in_page + voff[n], vb + (wave * kLoads + n) * 64);
+            for (int n = 0; n < kLoads; ++n) to_lds16(v_from + voff[n], vb + (wave * kLoads + n) * 64);
         };
 
         // Codes of slots that hold no token may be anything, NaN among it: those of the values
@@ -187,169 +214,324 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) prefill_kernel(A
             barrier_no_fence();
         };
 
-        auto multiply = [&](int j0, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
-            // the pieces of the next products are read while these run; the barriers keep the
-            // compiler from reading all of them at once, for which there are no registers
-            float16_t acc[2] = {};
-            uint4 k0 = kb[piece<kC>(m, hf)], k1 = kb[piece<kC>(32 + m, hf)];
+        if constexpr (kPairs) {
+            // the scores of a tile: the wave's 32 keys
+            float16_t acc;
+            float ks = 1.0f, vmost = 0.0f, vown = 0.0f, top = 0.0f;
+            auto scores = [&](int j0, const uint4 *kb, float ksl, float vsl, uint64_t ok) {
+                acc = float16_t{};
+                uint4 k0 = kb[piece<kC>(32 * side + m, hf)];
 #pragma unroll
-            for (int e = 0; e < kP; ++e) {
-                const uint4 a0 = k0, a1 = k1;
-                if (e + 1 < kP) {
-                    k0 = kb[piece<kC>(m, 2 * e + 2 + hf)];
-                    k1 = kb[piece<kC>(32 + m, 2 * e + 2 + hf)];
+                for (int e = 0; e < kP; ++e) {
+                    const uint4 a0 = k0;
+                    if (e + 1 < kP) k0 = kb[piece<kC>(32 * side + m, 2 * e + 2 + hf)];
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), qf[e][0], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), qf[e][1], acc, 0, 0, 0);
                 }
-                acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), qf[e][0], acc[0], 0, 0, 0);
-                acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), qf[e][0], acc[1], 0, 0, 0);
-                acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), qf[e][1], acc[0], 0, 0, 0);
-                acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), qf[e][1], acc[1], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            // (every row of the wave sees every key of most tiles)
-            if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
-                (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int jg = j0 + 32 * u + 16 * hf;
-                    const int live = live_keys(j0, 2 * u + hf, ok);
+                // (every row of the wave sees every key of most tiles)
+                if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
+                    (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
+                    const int jg = j0 + 32 * side + 16 * hf;
+                    const int live = live_keys(j0, 2 * side + hf, ok);
                     const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int j = jg + e;
                         const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
-                        acc[u][e] = see ? acc[u][e] : -__builtin_inff();
+                        acc[e] = see ? acc[e] : -__builtin_inff();
                     }
                 }
-            }
-            // (read here, they are there when the weights are: 1 to 2%)
-            uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
-            // The scales of the tile's four groups of sixteen keys (with BIG all the same) and, of the
-            // lane's two groups, the keys' scale and what the values' is to the outputs' unit.
-            float ks[2], top[2], vs[4], bits[2], back[2];
+                float vs[4];
 #pragma unroll
-            for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float a = lane_value(ksl, BIG ? 0 : 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
+                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
+                const float k_lo = lane_value(ksl, BIG ? 0 : 2 * side), k_hi = BIG ? k_lo : lane_value(ksl, 2 * side + 1);
                 // never 0, which would turn a hidden key's -inf into NaN; and where there is no page
                 // the scale may be anything, but no key is seen
-                ks[u] = fminf(fmaxf((hf ? d : a) * down, 0x1p-126f), 0x1p126f);
-                float t = max3(acc[u][0], acc[u][1], acc[u][2]);
+                ks = fminf(fmaxf((hf ? k_hi : k_lo) * down, 0x1p-126f), 0x1p126f);
+                vmost = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+                vown = BIG ? vs[0] : side ? (hf ? vs[3] : vs[2]) : (hf ? vs[1] : vs[0]);
+                float a = max3(acc[0], acc[1], acc[2]);
 #pragma unroll
-                for (int e = 3; e < 15; e += 2) t = max3(t, acc[u][e], acc[u][e + 1]);
-                top[u] = max3(t, t, acc[u][15]) * ks[u];
-            }
-            const float now = half_max(fmaxf(top[0], top[1]));
-            // The outputs count in units of a values' scale, at least that of every page so far and
-            // at most 2^6 times this tile's: moved with the maximum, which is rare.
-            const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-            if (__any(now > mx + kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
-                const float to = fmaxf(mx, now), to_unit = most > 0.0f ? most : unit;
-                const float alpha = __builtin_amdgcn_exp2f(mx - to);
-                const float turn = alpha * (unit / to_unit);
-                mx = to;
-                l *= alpha;
-                unit = to_unit;
+                for (int e = 3; e < 15; e += 2) a = max3(a, acc[e], acc[e + 1]);
+                top = half_max(max3(a, a, acc[15]) * ks);
+                tops[wave][lane] = top;
+            };
+            // the weights, of the maximum of both waves
+            half8_t w[2];
+            auto weigh = [&]() {
+                const float now = fmaxf(top, tops[wave ^ 1][lane]);
+                // The outputs count in units of a values' scale, at least that of every page so far and
+                // at most 2^6 times this tile's: moved with the maximum, which is rare.
+                if (__any(now > mx + kSlack) || vmost > unit || (vmost > 0.0f && vmost < unit * kLeastUnit)) {
+                    const float to = fmaxf(mx, now), to_unit = vmost > 0.0f ? vmost : unit;
+                    const float alpha = __builtin_amdgcn_exp2f(mx - to);
+                    const float turn = alpha * (unit / to_unit);
+                    mx = to;
+                    l *= alpha;
+                    unit = to_unit;
 #pragma unroll
-                for (int e = 0; e < kP; ++e) o[e] *= turn;
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (BIG && u == 1) {
-                    bits[1] = bits[0];
-                    back[1] = back[0];
-                    continue;
+                    for (int e = 0; e < kO; ++e) o[e] *= turn;
                 }
-                const float v = BIG ? vs[0] : hf ? vs[2 * u + 1] : vs[2 * u];
-                const float ratio = v > 0.0f ? v / unit : 1.0f;        // (no weight where there is no page)
-                bits[u] = __builtin_amdgcn_logf(ratio);
-                back[u] = 1.0f / ratio;
-            }
-            float shift = mx;
-            if (__any(fabsf(mx) >= kFar)) {
+                const float ratio = vown > 0.0f ? vown / unit : 1.0f;          // (no weight where there is no page)
+                float shift = mx;
+                if (__any(fabsf(mx) >= kFar)) {
 #pragma clang fp contract(off)   // the products as the maximum was taken of them
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[u][e] = acc[u][e] * ks[u] - mx;
-                    ks[u] = 1.0f;
+                    for (int e = 0; e < 16; ++e) acc[e] = acc[e] * ks - mx;
+                    ks = 1.0f;
+                    shift = 0.0f;
                 }
-                shift = 0.0f;
-            }
-            half8_t w[2][2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float base = kWeightBits + bits[u] - shift;
+                const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - shift;
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e], ks, base));
                     sum += f;
-                    w[u][e >> 3][e & 7] = (half_t)f;
+                    w[e >> 3][e & 7] = (half_t)f;
                 }
-                l += sum * back[u];
-            }
+                l += sum * (1.0f / ratio);
+                weights[wave][0][lane] = __builtin_bit_cast(uint4, w[0]);
+                weights[wave][1][lane] = __builtin_bit_cast(uint4, w[1]);
+            };
+            auto add_values = [&](const uint4 *vb) {
+                const half8_t x0 = __builtin_bit_cast(half8_t, weights[wave ^ 1][0][lane]), x1 = __builtin_bit_cast(half8_t, weights[wave ^ 1][1][lane]);
+                const int row = 32 * kO * side + m;
+                uint4 v0 = vb[piece<4>(row, 2 * side + hf)], v1 = vb[piece<4>(row, 2 * (side ^ 1) + hf)];
 #pragma unroll
-            for (int e = 0; e < kP; ++e) {
-                const uint4 a0 = v0, a1 = v1;
-                if (e + 1 < kP) {
-                    v0 = vb[piece<4>(32 * e + 32 + m, hf)];
-                    v1 = vb[piece<4>(32 * e + 32 + m, 2 + hf)];
+                for (int e = 0; e < kO; ++e) {
+                    const uint4 a0 = v0, a1 = v1;
+                    if (e + 1 < kO) {
+                        v0 = vb[piece<4>(row + 32 * e + 32, 2 * side + hf)];
+                        v1 = vb[piece<4>(row + 32 * e + 32, 2 * (side ^ 1) + hf)];
+                    }
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[1], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), x0, o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), x1, o[e], 0, 0, 0);
                 }
-                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0][0], o[e], 0, 0, 0);
-                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[0][1], o[e], 0, 0, 0);
-                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), w[1][0], o[e], 0, 0, 0);
-                o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), w[1][1], o[e], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
+            };
 
-        if (count > 0) {
-            next_id = page_of(0);
-            issue(0, kbuf0, vbuf0);
-            next_id = page_of(1);
-            auto step = [&](int i, const uint4 *kb, uint4 *vb, uint4 *kn, uint4 *vn) {
-                // this wave's loads of tile i are in LDS, its reads of tile i - 1 done
+            if (count > 0) {
+                next_id = page_of(0);
+                issue_keys(0, kbuf0);
+                next_id = page_of(1);
+                issue_values(vbuf0);
+                bool before = false, dead = false;         // of the tile before: whether it is the wave's; slots of no token
+                int j_before = 0;
+                uint64_t ok_before = 0;
+                // A tile's scores beside the sums of the tile before, then its weights.  Keys are loaded a
+                // tile ahead, values as the keys' tile begins its weights.
+                auto step = [&](int i, const uint4 *kb, uint4 *vb, uint4 *kn, uint4 *vn) {
+                    // this wave's loads of the keys of tile i, and of the values of tile i - 1, are in LDS,
+                    // its reads and writes of LDS done
+                    __builtin_amdgcn_s_waitcnt(0xC07F);
+                    wait_vmcnt<kLoads>();
+                    barrier_no_fence();            // and everyone's
+                    const float ksl = ks_l, vsl = vs_l;
+                    const uint64_t ok = has;
+                    if (dead) clear_dead(j_before, vn, ok_before);
+                    // (unconditionally, the last tile again behind it: around a condition the compiler
+                    // waits for all loads)
+                    issue_keys(min(i + 1, count - 1), kn);
+                    next_id = page_of(i + 2);
+                    const int j0 = tiles.at(start + i) * kTile;
+                    const bool mine = !idle && j0 <= hi;
+                    __builtin_amdgcn_s_setprio(1);     // products before the other workgroup's weights: 1%
+                    if (before) add_values(vn);
+                    if (mine) scores(j0, kb, ksl, vsl, ok);
+                    __builtin_amdgcn_s_waitcnt(0xC07F);
+                    __builtin_amdgcn_s_setprio(0);
+                    barrier_no_fence();            // the maxima are there; the values of tile i - 1 are done with
+                    issue_values(vn);
+                    if (mine) weigh();
+                    before = mine;
+                    dead = (ok & 15) != 15 || j0 + kTile > s.len;
+                    j_before = j0;
+                    ok_before = ok;
+                };
+                for (int i = 0; i < count; i += 2) {
+                    step(i, kbuf0, vbuf0, kbuf1, vbuf1);
+                    if (i + 1 < count) step(i + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+                }
+                uint4 *last = count & 1 ? vbuf0 : vbuf1;
                 __builtin_amdgcn_s_waitcnt(0xC07F);
                 wait_vmcnt<0>();
-                barrier_no_fence();            // everyone's are, and tile i - 1 is done with
-                const float ksl = ks_l, vsl = vs_l;
-                const uint64_t ok = has;
-                if (i + 1 < count) {
-                    issue(i + 1, kn, vn);
-                    next_id = page_of(i + 2);
+                barrier_no_fence();
+                if (dead) clear_dead(j_before, last, ok_before);
+                if (before) add_values(last);
+            }
+        } else {
+            auto multiply = [&](int j0, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
+                // the pieces of the next products are read while these run; the barriers keep the
+                // compiler from reading all of them at once, for which there are no registers
+                float16_t acc[2] = {};
+                uint4 k0 = kb[piece<kC>(m, hf)], k1 = kb[piece<kC>(32 + m, hf)];
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    const uint4 a0 = k0, a1 = k1;
+                    if (e + 1 < kP) {
+                        k0 = kb[piece<kC>(m, 2 * e + 2 + hf)];
+                        k1 = kb[piece<kC>(32 + m, 2 * e + 2 + hf)];
+                    }
+                    acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), qf[e][0], acc[0], 0, 0, 0);
+                    acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), qf[e][0], acc[1], 0, 0, 0);
+                    acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), qf[e][1], acc[0], 0, 0, 0);
+                    acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), qf[e][1], acc[1], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                const int j0 = tiles.at(start + i) * kTile;
-                if ((ok & 15) != 15 || j0 + kTile > s.len) clear_dead(j0, vb, ok);
-                if (!idle && j0 <= hi) multiply(j0, kb, vb, ksl, vsl, ok);
+                // (every row of the wave sees every key of most tiles)
+                if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
+                    (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int jg = j0 + 32 * u + 16 * hf;
+                        const int live = live_keys(j0, 2 * u + hf, ok);
+                        const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int j = jg + e;
+                            const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
+                            acc[u][e] = see ? acc[u][e] : -__builtin_inff();
+                        }
+                    }
+                }
+                // (read here, they are there when the weights are: 1 to 2%)
+                uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
+                // The scales of the tile's four groups of sixteen keys (with BIG all the same) and, of the
+                // lane's two groups, the keys' scale and what the values' is to the outputs' unit.
+                float ks[2], top[2], vs[4], bits[2], back[2];
+#pragma unroll
+                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float a = lane_value(ksl, BIG ? 0 : 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
+                    // never 0, which would turn a hidden key's -inf into NaN; and where there is no page
+                    // the scale may be anything, but no key is seen
+                    ks[u] = fminf(fmaxf((hf ? d : a) * down, 0x1p-126f), 0x1p126f);
+                    float t = max3(acc[u][0], acc[u][1], acc[u][2]);
+#pragma unroll
+                    for (int e = 3; e < 15; e += 2) t = max3(t, acc[u][e], acc[u][e + 1]);
+                    top[u] = max3(t, t, acc[u][15]) * ks[u];
+                }
+                const float now = half_max(fmaxf(top[0], top[1]));
+                // The outputs count in units of a values' scale, at least that of every page so far and
+                // at most 2^6 times this tile's: moved with the maximum, which is rare.
+                const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+                if (__any(now > mx + kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
+                    const float to = fmaxf(mx, now), to_unit = most > 0.0f ? most : unit;
+                    const float alpha = __builtin_amdgcn_exp2f(mx - to);
+                    const float turn = alpha * (unit / to_unit);
+                    mx = to;
+                    l *= alpha;
+                    unit = to_unit;
+#pragma unroll
+                    for (int e = 0; e < kO; ++e) o[e] *= turn;
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (BIG && u == 1) {
+                        bits[1] = bits[0];
+                        back[1] = back[0];
+                        continue;
+                    }
+                    const float v = BIG ? vs[0] : hf ? vs[2 * u + 1] : vs[2 * u];
+                    const float ratio = v > 0.0f ? v / unit : 1.0f;        // (no weight where there is no page)
+                    bits[u] = __builtin_amdgcn_logf(ratio);
+                    back[u] = 1.0f / ratio;
+                }
+                float shift = mx;
+                if (__any(fabsf(mx) >= kFar)) {
+#pragma clang fp contract(off)   // the products as the maximum was taken of them
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[u][e] = acc[u][e] * ks[u] - mx;
+                        ks[u] = 1.0f;
+                    }
+                    shift = 0.0f;
+                }
+                half8_t w[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float base = kWeightBits + bits[u] - shift;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                        sum += f;
+                        w[u][e >> 3][e & 7] = (half_t)f;
+                    }
+                    l += sum * back[u];
+                }
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    const uint4 a0 = v0, a1 = v1;
+                    if (e + 1 < kP) {
+                        v0 = vb[piece<4>(32 * e + 32 + m, hf)];
+                        v1 = vb[piece<4>(32 * e + 32 + m, 2 + hf)];
+                    }
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0][0], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[0][1], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), w[1][0], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), w[1][1], o[e], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             };
-            for (int i = 0; i < count; i += 2) {
-                step(i, kbuf0, vbuf0, kbuf1, vbuf1);
-                if (i + 1 < count) step(i + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+
+            if (count > 0) {
+                next_id = page_of(0);
+                issue_keys(0, kbuf0);
+                issue_values(vbuf0);
+                next_id = page_of(1);
+                auto step = [&](int i, const uint4 *kb, uint4 *vb, uint4 *kn, uint4 *vn) {
+                    // this wave's loads of tile i are in LDS, its reads of tile i - 1 done
+                    __builtin_amdgcn_s_waitcnt(0xC07F);
+                    wait_vmcnt<0>();
+                    barrier_no_fence();            // everyone's are, and tile i - 1 is done with
+                    const float ksl = ks_l, vsl = vs_l;
+                    const uint64_t ok = has;
+                    if (i + 1 < count) {
+                        issue_keys(i + 1, kn);
+                        issue_values(vn);
+                        next_id = page_of(i + 2);
+                    }
+                    const int j0 = tiles.at(start + i) * kTile;
+                    if ((ok & 15) != 15 || j0 + kTile > s.len) clear_dead(j0, vb, ok);
+                    if (!idle && j0 <= hi) multiply(j0, kb, vb, ksl, vsl, ok);
+                };
+                for (int i = 0; i < count; i += 2) {
+                    step(i, kbuf0, vbuf0, kbuf1, vbuf1);
+                    if (i + 1 < count) step(i + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+                }
             }
         }
         l = half_sum(l);
+        if constexpr (kPairs) {
+            tops[wave][lane] = l;
+            __syncthreads();
+            l += tops[wave ^ 1][lane];
+        }
         if (!idle && w0 + m <= r1) {
             const long long at = (long long)(s.row0 + token) * p.q_heads + head;
             if (chunks > 1) {
-                float *dst = p.part + (at * p.splits + split) * kPart<D> + 4 * hf;
+                float *dst = p.part + (at * p.splits + split) * kPart<D> + 32 * kO * side + 4 * hf;
 #pragma unroll
-                for (int e = 0; e < kP; ++e)
+                for (int e = 0; e < kO; ++e)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         *reinterpret_cast<float4_t *>(dst + 32 * e + 8 * u) =
                             float4_t{o[e][4 * u], o[e][4 * u + 1], o[e][4 * u + 2], o[e][4 * u + 3]} * unit;
-                if (hf == 0) {
+                if (hf == 0 && side == 0) {
                     dst[D] = mx;
                     dst[D + 1] = l;
                     dst[D + 2] = (float)chunks;
                 }
             } else {
-                if (p.part != nullptr && hf == 0) p.part[at * p.splits * kPart<D> + D + 2] = 1.0f;
+                if (p.part != nullptr && hf == 0 && side == 0) p.part[at * p.splits * kPart<D> + D + 2] = 1.0f;
                 const float inv = l > 0.0f || !(l == l) ? unit / l : 0.0f;
-                uint16_t *dst = p.out + at * D + 4 * hf;
+                uint16_t *dst = p.out + at * D + 32 * kO * side + 4 * hf;
 #pragma unroll
-                for (int e = 0; e < kP; ++e)
+                for (int e = 0; e < kO; ++e)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         uint2 y;
@@ -383,19 +565,18 @@ hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hip
 }
 
 // Row tiles of a sequence that the grid has.
-int prefill_tiles(int seqs, int kv_heads, int group, int max_q) {
-    const long long tiles = ((long long)max_q * group + kRows - 1) / kRows;
+int prefill_tiles(int seqs, int kv_heads, int group, int head_dim, int max_q) {
+    const long long tiles = ((long long)max_q * group + rows_of(head_dim) - 1) / rows_of(head_dim);
     const long long pairs = (long long)kv_heads * seqs;                          // below 2^20
     return (int)std::max<long long>(1, std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * pairs)));
 }
 
 }  // namespace
 
-// Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a
-// CU, one with 256 elements).
+// Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a CU).
 int prefill_splits(int seqs, int kv_heads, int group, int head_dim, int max_q, long long key_tiles) {
-    const long long groups = (long long)seqs * kv_heads * prefill_tiles(seqs, kv_heads, group, max_q);
-    const long long room = (head_dim > 128 ? 256 : 512) / groups;
+    const long long groups = (long long)seqs * kv_heads * prefill_tiles(seqs, kv_heads, group, head_dim, max_q);
+    const long long room = 512 / groups;
     return (int)std::max<long long>(1, std::min<long long>({room, key_tiles / kLeastChunk, kMostSplits}));
 }
 
@@ -405,7 +586,7 @@ hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, 
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
     // the grid is cut.
-    const int tiles_per_seq = prefill_tiles(p.c.seqs, p.c.kv_heads, p.group, max_q);
+    const int tiles_per_seq = prefill_tiles(p.c.seqs, p.c.kv_heads, p.group, head_dim, max_q);
     const int grid = p.c.kv_heads * p.c.seqs * tiles_per_seq * p.splits;
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, tiles_per_seq, s)
                 : launch_dim<half_t>(p, head_dim, grid, tiles_per_seq, s);
