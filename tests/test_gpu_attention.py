@@ -237,3 +237,13 @@ def test_no_rows():
     check(t)
     cache, batch, q, _, _ = t.device()
     assert binding.attention(q[:0], cache, batch).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("seqs,max_kv", [(70, 1 << 15), (300, 1 << 15), (2100, 1 << 16)])
+def test_many_sequences_of_a_call_that_may_be_long(seqs, max_kv):
+    """Short sequences, some without tokens or rows, and a long one among them."""
+    lens = [(7 * b) % 40 for b in range(seqs)]
+    lens[seqs // 2] = 3300
+    new = [min(1, n) * (b % 5 != 3) for b, n in enumerate(lens)]
+    t = kc.Batch(25, "bf16", new, lens, 2, 1 if seqs < 1000 else 2, 64, 64).fill()
+    check(t, max_kv=max_kv)

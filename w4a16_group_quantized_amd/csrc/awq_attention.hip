@@ -54,16 +54,30 @@ constexpr float kLeastUnit = 0x1p-6f;
 // finer cut; and many groups need no cut, unless sequences may be so long that one
 // among short ones would be the last by far.
 constexpr int kUncutTiles = 12, kManyGroups = 192, kLongTiles = 256, kLeastChunk = 4, kMaxSplits = 256;
+constexpr int kJoinGroups = 8192;          // workgroups that join chunks
 
 // Chunks for a tile: from the tiles that all sequences' rows see, for all kv heads.
-// The host knows no lengths, so each wave adds them up.
+// The host knows no lengths, so each wave adds them up, with more than 64 sequences four
+// to a lane at a time.
 __device__ __forceinline__ float chunks_per_tile(const AttnArgs &p) {
     const KvView &c = p.c;
     float sum = 0.0f;
-    for (int b = threadIdx.x & 63; b < c.seqs; b += 64) {
-        const Seq s = load_seq(c, b);
+    const auto add = [&](const Seq &s) {
         if (s.n > 0)
             sum += (float)visible_tiles(p, s.first(), s.len - 1, s.len).count() * (float)((s.n * p.group + kRows - 1) / kRows);
+    };
+    const int lane = threadIdx.x & 63;
+    if (c.seqs <= 64) {
+        if (lane < c.seqs) add(load_seq(c, lane));
+    } else {
+        for (int b = lane; b < c.seqs; b += 256) {
+            Seq s[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] = load_seq(c, min(b + 64 * k, c.seqs - 1));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (b + 64 * k < c.seqs) add(s[k]);
+        }
     }
     for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
     sum *= (float)c.kv_heads;
@@ -107,7 +121,18 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
-    const float per_tile = p.part == nullptr ? 0.0f : chunks_per_tile(p);
+    float per_tile = 0.0f;
+    if (p.part != nullptr) {
+        // With many sequences only those who may be cut ask: 1024 of 300 tokens in a call that may
+        // have 64k, 760 -> 180 us (138 uncut).  With few, asking at once saves a load's time (0.6 us).
+        bool ask = c.seqs < 64;
+        if (!ask) {
+            const int most = min(p.splits, visible_tiles(p, s.first(), s.len - 1, s.len).count() / kLeastChunk);
+            if (split >= max(1, most)) return;
+            ask = most > 1;
+        }
+        if (ask) per_tile = chunks_per_tile(p);
+    }
     for (int rt = slot % row_tiles; rt * kRows < total; rt += row_tiles) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const int lo = s.first() + r0 / p.group, hi = s.first() + r1 / p.group;
@@ -459,15 +484,23 @@ Plan plan(int seqs, int kv_heads, int group, int head_dim, int max_q, int max_kv
                                             std::max(1, ((1 << 24) - 1) / (units * kv_heads)));
     const long long groups = (long long)seqs * kv_heads * pl.row_tiles;
     pl.target = groups <= 64 ? 256 : 512;
-    long long want = std::max(8ll, 4 * ((pl.target + groups - 1) / groups));     // lengths may differ by much
+    // lengths may differ by much; but a workgroup that has no chunk takes its launch
+    // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
+    // 1126 at eight, 692 at two)
+    long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
     if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
     pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
+    // (a launch has less than 2^32 threads)
+    const long long once = (long long)(units + kXcds) * pl.splits * kv_heads;
+    pl.row_tiles = (int)std::max<long long>(1, std::min<long long>(pl.row_tiles, ((1 << 24) - 1) / once));
     return pl;
 }
 
 template <typename T, int D>
 hipError_t launch_combine(const AttnArgs &p, int max_q, hipStream_t s) {
-    combine_kernel<T, D><<<dim3(max_q * p.q_heads, p.c.seqs), 256, 0, s>>>(p);
+    // (most rows of many sequences have one chunk and nothing to join)
+    const int each = (int)std::max<long long>(1, std::min<long long>((long long)max_q * p.q_heads, kJoinGroups / p.c.seqs));
+    combine_kernel<T, D><<<dim3(each, p.c.seqs), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
