@@ -247,3 +247,14 @@ def test_many_sequences_of_a_call_that_may_be_long(seqs, max_kv):
     new = [min(1, n) * (b % 5 != 3) for b, n in enumerate(lens)]
     t = kc.Batch(25, "bf16", new, lens, 2, 1 if seqs < 1000 else 2, 64, 64).fill()
     check(t, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,page,heads", [(64, 16, (8, 2)), (128, 64, (8, 2)), (256, 128, (3, 1))])
+@pytest.mark.parametrize("window", [0, 500])
+def test_prompts_among_single_tokens(dtype, dim, page, heads, window):
+    """Each sequence by the kernel that its own rows call for, in one call; cut keys or not."""
+    new = [200, 1, 3, 0, 60, 1, 1, 9, 31, 32, 33, 1]
+    lens = [3001, 1500, 2, 7, 60, 1, 900, 400, 31, 700, 33, 64]
+    check(kc.Batch(26, dtype, new, lens, *heads, dim, page, extra_rows=2).fill(), window=window, sinks=5)
+    check(kc.Batch(27, dtype, [700] + [1, 0, 2] * 30, [900] + [80, 5, 2] * 30, *heads, dim, page).fill(), window=window)

@@ -177,3 +177,23 @@ def test_empty_calls():
     t = kc.Batch(2, "fp16", [0, 0], [5, 0], 2, 2, 64, 16).fill()
     got = run(t)
     assert torch.equal(kc.bytes_of(got[1]), t.k) and torch.equal(kc.bytes_of(got[2]), t.v)
+
+
+@pytest.mark.parametrize("dtype,dim,page", [("fp16", 128, 16), ("bf16", 64, 64)])
+@pytest.mark.parametrize("rope", [None, 310])
+def test_prompts_among_single_tokens(dtype, dim, page, rope):
+    """So many sequences, of such different rows, that workgroups look for their work; some
+    without rows, places, pages or rows of the table."""
+    new, lens = [300, 2], [340, 1]
+    for i in range(160):
+        new.append((1, 0, 5, 1, 17)[i % 5])
+        lens.append((1, 7, 3, 65 + i, 33)[i % 5])
+    t = kc.Batch(31, dtype, new, lens, 4, 2, dim, page, extra_rows=1).fill([n - m for n, m in zip(lens, new)])
+    t.table[6, :] = -1
+    compare(t, run(t, None if rope is None else kc.rope_table(rope, dim // 2)), None if rope is None else kc.rope_table(rope, dim // 2))
+    cache, batch, q, k, v = t.device()
+    alone, _, _, _, _ = t.device()
+    binding.kv_append(q, k, v, cache, batch)
+    binding.kv_append(None, k, v, alone, batch)
+    assert torch.equal(cache.k.view(torch.uint8), alone.k.view(torch.uint8))
+    assert torch.equal(cache.v.view(torch.uint8), alone.v.view(torch.uint8))

@@ -24,6 +24,7 @@ struct AttnArgs {
     float scale;             // scale * log2(e)
     int window, sinks;
     int splits, target;      // most chunks of a row tile; workgroups that all chunks are dealt to
+    int few;                 // rows (times query heads of a kv head) of a sequence from which the prompt kernel takes it
 };
 
 // The 64-key tiles that rows at positions lo .. hi see: tiles [0, a) that hold
@@ -121,7 +122,9 @@ template <int D>
 constexpr int kPart = D + 4;
 
 // Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
-int prefill_splits(int seqs, int kv_heads, int group, int head_dim, int max_q, long long key_tiles);
-hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s);
+// row_tiles: of each sequence, or with `flat` of all of them, one after the other.
+int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat);
+int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
+hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
 
 }  // namespace awq

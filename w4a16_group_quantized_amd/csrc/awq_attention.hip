@@ -63,7 +63,7 @@ __device__ __forceinline__ float chunks_per_tile(const AttnArgs &p) {
     const KvView &c = p.c;
     float sum = 0.0f;
     const auto add = [&](const Seq &s) {
-        if (s.n > 0)
+        if (s.n > 0 && s.n * p.group < p.few)
             sum += (float)visible_tiles(p, s.first(), s.len - 1, s.len).count() * (float)((s.n * p.group + kRows - 1) / kRows);
     };
     const int lane = threadIdx.x & 63;
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
+    if (total >= p.few) return;                // the prompt kernel's
     float per_tile = 0.0f;
     if (p.part != nullptr) {
         // With many sequences only those who may be cut ask: 1024 of 300 tokens in a call that may
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
     }
 }
 
-// A workgroup joins the chunks of one (row, head): D / 4 threads to a chunk, as many
+// A workgroup joins the chunks of one (row, head) after the other: D / 4 threads to a chunk, as many
 // chunks at once as that leaves room for, then the threads' sums through LDS.
 // Bound: latency (a few loads in a row), and the launch.
 template <typename T, int D>
@@ -405,12 +406,11 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
     __shared__ float weight[kMaxSplits], red[2][4];
     __shared__ float4_t part[kAtOnce][kLanes];
     const KvView &c = p.c;
-    const int tid = threadIdx.x, b = blockIdx.y;
-    const Seq s = load_seq(c, b);
-    for (int i = blockIdx.x; i < s.n * p.q_heads; i += gridDim.x) {
-        const int token = i / p.q_heads, head = i % p.q_heads;
-        const float *src = p.part + ((long long)(s.row0 + token) * p.q_heads + head) * p.splits * kPart<D>;
-        const int n = min((int)src[D + 2], kMaxSplits);
+    const int tid = threadIdx.x;
+    const int row0 = min(max(c.q_starts[0], 0), c.rows), row1 = min(max(c.q_starts[c.seqs], 0), c.rows);
+    for (int i = row0 * p.q_heads + blockIdx.x; i < row1 * p.q_heads; i += gridDim.x) {
+        const float *src = p.part + (long long)i * p.splits * kPart<D>;
+        const int n = min((int)src[D + 2], p.splits);
         if (n <= 1) continue;                  // the one chunk has written its outputs
         // one chunk's maximum and sum to a thread
         float own = kEmpty, l = 0.0f;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
             uint2 y;
             y.x = (uint32_t)from_float<T>(o[0] * inv) | ((uint32_t)from_float<T>(o[1] * inv) << 16);
             y.y = (uint32_t)from_float<T>(o[2] * inv) | ((uint32_t)from_float<T>(o[3] * inv) << 16);
-            *reinterpret_cast<uint2 *>(p.out + ((long long)(s.row0 + token) * p.q_heads + head) * D + 4 * lane) = y;
+            *reinterpret_cast<uint2 *>(p.out + (long long)i * D + 4 * lane) = y;
         }
         __syncthreads();                       // the LDS arrays are free again
     }
@@ -463,33 +463,43 @@ int prompt_rows(long long all_tiles) {
 
 // The grid of a call: the most chunks, whose number is found on the device, and the
 // workgroups that they are dealt to.
+// Where most sequences have far fewer rows than the longest, each kernel takes those that
+// suit it (one sequence of 2048 rows, 63 of one, all over 4k keys: 810 us with the prompt
+// kernel alone, 235 with both; 255 of one: 1854 and 476).
 struct Plan {
-    bool prompt;
+    bool prompt, mixed;      // whether the prompt kernel is needed, and both are
+    int few, prompt_tiles;
     int row_tiles, splits, target;
 };
-Plan plan(int seqs, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks) {
+Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks) {
     Plan pl;
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
     const long long tiles = (keys + kTile - 1) / kTile;
-    pl.prompt = (long long)max_q * group >= prompt_rows((long long)seqs * kv_heads * tiles);
+    pl.few = prompt_rows((long long)seqs * kv_heads * tiles);
+    pl.prompt = (long long)max_q * group >= pl.few;
+    pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
+    pl.row_tiles = pl.target = 0;
     if (pl.prompt) {
-        pl.row_tiles = pl.target = 0;
-        pl.splits = prefill_splits(seqs, kv_heads, group, head_dim, max_q, tiles);
-        return pl;
+        pl.prompt_tiles = prefill_row_tiles(seqs, rows, kv_heads, group, head_dim, max_q, pl.few, pl.mixed);
+        pl.splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
+        if (!pl.mixed) return pl;
     }
     // (the kernel steps on where the grid is cut)
     const int units = (seqs + kXcds - 1) / kXcds * kXcds;
-    pl.row_tiles = (int)std::min<long long>(((long long)max_q * group + kRows - 1) / kRows,
+    const long long some = pl.mixed ? std::min((rows - max_q) / (seqs - 1) + 1, (pl.few - 1) / group + 1) : max_q;
+    pl.row_tiles = (int)std::min<long long>((some * group + kRows - 1) / kRows,
                                             std::max(1, ((1 << 24) - 1) / (units * kv_heads)));
     const long long groups = (long long)seqs * kv_heads * pl.row_tiles;
     pl.target = groups <= 64 ? 256 : 512;
-    // lengths may differ by much; but a workgroup that has no chunk takes its launch
-    // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
-    // 1126 at eight, 692 at two)
-    long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
-    if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
-    pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
+    if (!pl.mixed) {
+        // lengths may differ by much; but a workgroup that has no chunk takes its launch
+        // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
+        // 1126 at eight, 692 at two)
+        long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
+        if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
+        pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
+    }
     // (a launch has less than 2^32 threads)
     const long long once = (long long)(units + kXcds) * pl.splits * kv_heads;
     pl.row_tiles = (int)std::max<long long>(1, std::min<long long>(pl.row_tiles, ((1 << 24) - 1) / once));
@@ -497,40 +507,37 @@ Plan plan(int seqs, int kv_heads, int group, int head_dim, int max_q, int max_kv
 }
 
 template <typename T, int D>
-hipError_t launch_combine(const AttnArgs &p, int max_q, hipStream_t s) {
-    // (most rows of many sequences have one chunk and nothing to join)
-    const int each = (int)std::max<long long>(1, std::min<long long>((long long)max_q * p.q_heads, kJoinGroups / p.c.seqs));
-    combine_kernel<T, D><<<dim3(each, p.c.seqs), 256, 0, s>>>(p);
+hipError_t launch(AttnArgs p, const Plan &pl, bool bf16, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (pl.prompt) {
+        p.few = pl.mixed ? pl.few : 0;
+        e = launch_attention_prefill(p, D, bf16, pl.prompt_tiles, pl.mixed, s);
+        if (e != hipSuccess) return e;
+    }
+    if (!pl.prompt || pl.mixed) {
+        p.few = pl.mixed ? pl.few : 0x7FFFFFFF;
+        const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
+        const int grid = units * p.c.kv_heads * pl.row_tiles;
+        const int page = 1 << p.c.log2_page;
+        if (page == kTile)
+            split_kernel<T, D, kOne><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+        else if (page > kTile)
+            split_kernel<T, D, kLarge><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+        else
+            split_kernel<T, D, kSmall><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess || p.part == nullptr) return e;
+    combine_kernel<T, D><<<(int)std::min<long long>((long long)p.c.rows * p.q_heads, kJoinGroups), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
-template <typename T, int D>
-hipError_t launch(AttnArgs p, const Plan &pl, bool bf16, int max_q, hipStream_t s) {
-    if (pl.prompt) {
-        const hipError_t e = launch_attention_prefill(p, D, bf16, max_q, s);
-        if (e != hipSuccess || p.part == nullptr) return e;
-        return launch_combine<T, D>(p, max_q, s);
-    }
-    const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
-    const int grid = units * p.c.kv_heads * pl.row_tiles;
-    const int page = 1 << p.c.log2_page;
-    if (page == kTile)
-        split_kernel<T, D, kOne><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-    else if (page > kTile)
-        split_kernel<T, D, kLarge><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-    else
-        split_kernel<T, D, kSmall><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.part == nullptr) return e;
-    return launch_combine<T, D>(p, max_q, s);
-}
-
 template <typename T>
-hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, bool bf16, int max_q, hipStream_t s) {
+hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, bool bf16, hipStream_t s) {
     switch (D) {
-    case 64: return launch<T, 64>(p, pl, bf16, max_q, s);
-    case 128: return launch<T, 128>(p, pl, bf16, max_q, s);
-    case 256: return launch<T, 256>(p, pl, bf16, max_q, s);
+    case 64: return launch<T, 64>(p, pl, bf16, s);
+    case 128: return launch<T, 128>(p, pl, bf16, s);
+    case 256: return launch<T, 256>(p, pl, bf16, s);
     }
     return hipErrorInvalidValue;
 }
@@ -539,7 +546,7 @@ hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, bool bf16, int m
 
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
                            int max_kv, int window, int sinks) {
-    const Plan pl = plan(seqs, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks);
+    const Plan pl = plan(seqs, rows, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks);
     if (pl.splits == 1) return 0;
     return (size_t)rows * q_heads * pl.splits * (head_dim + 4) * sizeof(float);
 }
@@ -547,10 +554,10 @@ size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int he
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
                             int max_q, int max_kv, void *workspace, hipStream_t s) {
-    const Plan pl = plan(c.seqs, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
+    const Plan pl = plan(c.seqs, c.rows, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
     AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
-               q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, pl.splits, pl.target};
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, bf16, max_q, s) : launch_dim<half_t>(p, head_dim, pl, bf16, max_q, s);
+               q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, pl.splits, pl.target, 0};
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, bf16, s) : launch_dim<half_t>(p, head_dim, pl, bf16, s);
 }
 
 }  // namespace awq

@@ -73,7 +73,7 @@ __device__ __forceinline__ int piece(int row, int at) {
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
 template <typename T, int D, bool BIG>
-__global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {
+__global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {      // 0: flat
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
     constexpr bool kPairs = in_pairs(D);
@@ -90,7 +90,19 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     const int side = kPairs ? wave & 1 : 0, row_wave = kPairs ? wave >> 1 : wave;
     const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.splits;
     const int slot = blockIdx.x / (c.kv_heads * p.splits);
-    const int b = seq_of_rank(c, slot / tiles_per_seq);
+    int b, tile, tile_step = tiles_per_seq;
+    if (tiles_per_seq > 0) {
+        b = seq_of_rank(c, slot / tiles_per_seq);
+        tile = slot % tiles_per_seq;
+    } else {
+        const int2 at = seq_of_piece(c, slot, [&](const Seq &s) {
+            return s.n * p.group >= p.few ? (s.n * p.group + kRows - 1) / kRows : 0;
+        });
+        if (at.x >= c.seqs) return;
+        b = at.x;
+        tile = at.y;
+        tile_step = 1 << 30;
+    }
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     }
 
     // the longest rows first
-    for (int rt = row_tiles - 1 - slot % tiles_per_seq; rt >= 0; rt -= tiles_per_seq) {
+    for (int rt = row_tiles - 1 - tile; rt >= 0; rt -= tile_step) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
         // this workgroup's chunk of them
@@ -564,32 +576,33 @@ hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hip
     return hipGetLastError();
 }
 
-// Row tiles of a sequence that the grid has.
-int prefill_tiles(int seqs, int kv_heads, int group, int head_dim, int max_q) {
-    const long long tiles = ((long long)max_q * group + rows_of(head_dim) - 1) / rows_of(head_dim);
+}  // namespace
+
+int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat) {
+    const int each = rows_of(head_dim);
+    if (flat)                                  // all that there can be
+        return (int)((long long)rows * group / each + std::min<long long>(seqs, (long long)rows * group / few));
+    const long long tiles = ((long long)max_q * group + each - 1) / each;
     const long long pairs = (long long)kv_heads * seqs;                          // below 2^20
     return (int)std::max<long long>(1, std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * pairs)));
 }
 
-}  // namespace
-
 // Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a CU).
-int prefill_splits(int seqs, int kv_heads, int group, int head_dim, int max_q, long long key_tiles) {
-    const long long groups = (long long)seqs * kv_heads * prefill_tiles(seqs, kv_heads, group, head_dim, max_q);
-    const long long room = 512 / groups;
-    return (int)std::max<long long>(1, std::min<long long>({room, key_tiles / kLeastChunk, kMostSplits}));
+int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles) {
+    const long long groups = std::max<long long>(1, (long long)(flat ? 1 : seqs) * kv_heads * row_tiles);
+    return (int)std::max<long long>(1, std::min<long long>({512 / groups, key_tiles / kLeastChunk, kMostSplits}));
 }
 
-hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int max_q, hipStream_t s) {
+hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
     // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
     // keys meet in one XCD's cache.  Then the row tiles of a sequence, and the sequences, the
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
-    // the grid is cut.
-    const int tiles_per_seq = prefill_tiles(p.c.seqs, p.c.kv_heads, p.group, head_dim, max_q);
-    const int grid = p.c.kv_heads * p.c.seqs * tiles_per_seq * p.splits;
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, tiles_per_seq, s)
-                : launch_dim<half_t>(p, head_dim, grid, tiles_per_seq, s);
+    // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
+    const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.splits;
+    if (grid == 0) return hipSuccess;
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, flat ? 0 : row_tiles, s)
+                : launch_dim<half_t>(p, head_dim, grid, flat ? 0 : row_tiles, s);
 }
 
 }  // namespace awq

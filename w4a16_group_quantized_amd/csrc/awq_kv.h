@@ -37,6 +37,35 @@ __device__ __forceinline__ Seq load_seq(const KvView &c, int b) {
     return s;
 }
 
+// The n-th of the pieces of work that the sequences have, one sequence after the other:
+// its sequence (or seqs, if there are fewer) and its number there.  All lanes of a wave
+// have to ask, for the same n.
+template <typename F>
+__device__ __forceinline__ int2 seq_of_piece(const KvView &c, int n, F pieces) {
+    const int lane = threadIdx.x & 63;
+    for (int b = 0; b < c.seqs; b += 64) {
+        const int own = b + lane < c.seqs ? pieces(load_seq(c, b + lane)) : 0;
+        int upto = own;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+            const int other = __shfl_up(upto, k);
+            upto += lane >= k ? other : 0;
+        }
+        const int all = __builtin_amdgcn_readlane(upto, 63);
+        if (n < all) {
+            const int at = (int)__builtin_ctzll(__ballot(upto > n));
+            return make_int2(b + at, n - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(own, at)));
+        }
+        n -= all;
+    }
+    return make_int2(c.seqs, 0);
+}
+// A call whose sequences have, but for the longest, less than half its rows on average
+// (prompts among single tokens): grids for the longest would be mostly empty.
+inline bool rows_differ(int seqs, int rows, int max_q) {
+    return seqs > 1 && 2ll * (rows - max_q) < (long long)(seqs - 1) * max_q;
+}
+
 // Activation types: fp16 (T = half_t) and bf16 (T = bhalf_t), as 16-bit patterns.
 struct bhalf_t {};
 template <typename T>

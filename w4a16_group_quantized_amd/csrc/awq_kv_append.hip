@@ -26,6 +26,8 @@
 //
 // One workgroup owns one (page, kv head), for the page's new tokens: nobody else
 // writes that slab or its scales, so no atomics.  Bound: HBM for prompts, launch latency for single tokens.
+#include <algorithm>
+
 #include "awq_internal.h"
 #include "awq_kv.h"
 
@@ -144,32 +146,48 @@ __device__ __forceinline__ void turn_unit(float x[16], int c0, int c1, int rot, 
 // of a prompt's bytes at four query heads to a kv head, and with them in the pages'
 // workgroups the last round of these was long.
 template <typename T, int D, bool ADJ, int kThreads, int kKeys>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int pages) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int pages) {     // 0: flat
     constexpr int U = D / 16;                          // units of a head row
     constexpr int kValues = kKeys / 2;                 // tiles of values, 4 slots by 8 elements, a thread holds
     __shared__ float red[2][kThreads / 64];
     __shared__ int bad[kMaxPage];
     __shared__ __align__(16) uint32_t turned[8 * kValues * kThreads + D];    // value codes [D][words + 1], four slots to a word
     const KvView &c = p.c;
+    constexpr int kTokens = 8 * kThreads / D;          // of a workgroup of queries
     const int tid = threadIdx.x;
-    const int h = blockIdx.y, b = blockIdx.z;
+    const int h = blockIdx.y;
+    // positions in [from, to) have a place in the page table and a row in the rotation's table
+    // (first, that of row 0, may be below 0: rows without a place)
+    const auto from_of = [](const Seq &s) { return max(s.first(), 0); };
+    const auto to_of = [&](const Seq &s) { return p.rot ? min(s.len, p.rope_positions) : s.len; };
+    int b = blockIdx.z, piece = blockIdx.x, blocks = gridDim.x - pages;
+    if (pages == 0) {
+        const auto pages_of = [&](const Seq &s) {
+            return from_of(s) < to_of(s) ? ((to_of(s) - 1) >> c.log2_page) - (from_of(s) >> c.log2_page) + 1 : 0;
+        };
+        const int2 at = seq_of_piece(c, blockIdx.x, [&](const Seq &s) {
+            return pages_of(s) + (p.q && from_of(s) < to_of(s) ? (to_of(s) - from_of(s) + kTokens - 1) / kTokens : 0);
+        });
+        if (at.x >= c.seqs) return;
+        b = at.x;
+        piece = at.y;
+        pages = pages_of(load_seq(c, b));
+        blocks = 1 << 20;
+    }
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int group = p.q_heads / c.kv_heads;
-    const int first = s.first();                       // position of row 0 (below 0: rows without a place)
-    // positions in [from, to) have a place in the page table and a row in the rotation's table
-    const int from = max(first, 0);
-    const int to = p.rot ? min(s.len, p.rope_positions) : s.len;
+    const int first = s.first(), from = from_of(s), to = to_of(s);
     if (from >= to) return;
-    if ((int)blockIdx.x >= pages) {
+    if (piece >= pages) {
         if (p.q == nullptr) return;
         // queries: kTokens tokens at a time, with their rows of the table in LDS; a wave's units lie
         // side by side, and each thread has kAhead of them on the way
-        constexpr int kTokens = 8 * kThreads / D, kAhead = 4;
+        constexpr int kAhead = 4;
         constexpr bool kOnce = kThreads == 256;
         float *rows = reinterpret_cast<float *>(turned);
         const int width = group * U;
-        for (int pos = from + ((int)blockIdx.x - pages) * kTokens; pos < to; pos += ((int)gridDim.x - pages) * kTokens) {
+        for (int pos = from + (piece - pages) * kTokens; pos < to; pos += blocks * kTokens) {
             const int items = min(kTokens, to - pos) * width;
             const long long row = s.row0 + (pos - first);
             uint4 r[kAhead][2];
@@ -217,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
         return;
     }
     const int j0 = from >> c.log2_page, j1 = (to - 1) >> c.log2_page;
-    for (int j = j0 + blockIdx.x; j <= j1; j += pages) {
+    for (int j = j0 + piece; j <= j1; j += pages) {
         const int base = j << c.log2_page;
         const int lo = max(from, base), hi = min(to, base + P);
         const int count = hi - lo, held = lo - base;   // new tokens; slots that hold tokens from before
@@ -444,7 +462,14 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
 template <typename T, int D>
 hipError_t launch(const AppendArgs &p, bool adjacent, bool few, int most, int touched, hipStream_t s) {
     const int threads = few ? 128 : 256, tokens = 8 * threads / D;       // of a workgroup of queries
-    const dim3 grid(touched + (p.q ? (most + tokens - 1) / tokens : 0), p.c.kv_heads, p.c.seqs);
+    dim3 grid(touched + (p.q ? (most + tokens - 1) / tokens : 0), p.c.kv_heads, p.c.seqs);
+    // Prompts among single tokens: as many workgroups as there can be work for, which look for
+    // theirs (one of 2048 rows and 255 of one: 163 -> 68 us)
+    if ((long long)grid.x * grid.y * grid.z >= 4096 && rows_differ(p.c.seqs, p.c.rows, most)) {
+        const int some = std::min(p.c.seqs, p.c.rows);
+        grid = dim3((p.c.rows >> p.c.log2_page) + 2 * some + (p.q ? p.c.rows / tokens + some : 0), p.c.kv_heads);
+        touched = 0;
+    }
     const int elements = D << p.c.log2_page;
     if (few && adjacent)
         append_kernel<T, D, true, 128, 2><<<grid, threads, 0, s>>>(p, touched);
