@@ -349,7 +349,9 @@ awq_status awq_scale_search(const uint16_t *x, int32_t M, const uint16_t *w, int
  *   k_scales  fp32 [pages][kv_heads];  v_scales  fp32 [pages][kv_heads]
  * e4m3: one byte, sign, 4 exponent bits (bias 7), 3 mantissa bits, largest 448,
  * 0x7F and 0xFF NaN.  A key or value element is its code times its page's and
- * head's scale.  Codes of slots that hold no token may be anything.
+ * head's scale.  Codes of slots that hold no token may be anything, and so may
+ * the scales of pages that hold none; others are positive normal numbers
+ * (awq_kv_append writes powers of two from 2^-64).
  * page_size: a power of two, 16 to 256; head_dim 64, 128 or 256
  * (AWQ_ERROR_UNSUPPORTED otherwise).  k and v may be of any size (offsets are
  * 64-bit); pages * kv_heads < 2^31, kv_heads <= 65535.
