@@ -147,11 +147,16 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
         // with pages of 128 and more two tiles share each 128-byte line of the values, which two
         // waves should read at the same time (131k tokens: 112 -> 97 us).
         const int shift = tiles.b - tiles.a;
-        const auto border = [&](int k) {
-            const int at = (int)((long long)count * k / chunks);
-            return k == 0 ? 0 : k == chunks ? count : max(0, at - ((at + shift) & (kWaves - 1)));
-        };
-        const int t0 = border(split), t1 = border(split + 1);
+        int t0 = 0, t1 = count;
+        if (chunks > 1) {
+            const uint32_t each = (uint32_t)count / (uint32_t)chunks, over = count - each * chunks;
+            const auto border = [&](uint32_t k) {      // count * k / chunks, in 32 bits
+                const int at = (int)(each * k + over * k / (uint32_t)chunks);
+                return max(0, at - ((at + shift) & (kWaves - 1)));
+            };
+            t0 = split == 0 ? 0 : border(split);
+            t1 = split + 1 == chunks ? count : border(split + 1);
+        }
         const int first = t0 + ((wave - t0 - shift) & (kWaves - 1));
         // this lane's row
         const int r = min(r0 + m, r1);
