@@ -44,10 +44,10 @@ constexpr float kLeastUnit = 0x1p-6f;
 // tile) groups and, on the device, from the sequences' lengths.  Measured at 32 heads
 // over 8 of 128 elements, pages of 64 (us):
 //   not cut / dealt to 256 / 512 / 1024 workgroups
-//   1 sequence of 300: 8.6 / 11.4 / 11.4 / 11.4;  of 1000: 14.7 / 11.9 / 12.0 / 11.9
-//   1 of 32k: 216 / 23.0 / 22.8 / 28.2;  8 of 4k to 8k: 63 / 33.6 / 34.8 / 41.6
-//   16 of 4k to 8k: 65 / 52.3 / 48.4 / 51.1;  24 of 3k to 6k: 57.5 / 61.0 / 60.3 / 60.9
-//   64 of 1k to 2k: 43.9 / 50.2 / 50.0 / 54.1
+//   1 sequence of 300: 7.3 / 10.0 / 10.0 / 10.0;  of 1000: 12.1 / 10.6 / 10.6 / 10.6
+//   1 of 32k: 213 / 20.2 / 20.5 / 26.3;  8 of 4k to 8k: 59 / 29.7 / 31.1 / 37.4
+//   16 of 4k to 8k: 64 / 49.9 / 45.0 / 49.0;  24 of 3k to 6k: 54.0 / 56.8 / 55.9 / 57.9
+//   64 of 1k to 2k: 40.9 / 45.9 / 45.7 / 49.4
 // So: few tiles take no longer than the launch that joins chunks (and the call itself,
 // which is some 4 us shorter for one launch); one workgroup for
 // each CU streams as fast as the memory, while sequences of different lengths need a
@@ -458,9 +458,9 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
 // tiles of keys of all sequences and kv heads.  The split kernel reads keys and values
 // again for every sixteen rows, the prompt kernel is slower to start.  Measured (us,
 // split / prompt, 4 query heads to each of 8 kv heads of 128 elements, 20, 32, 64, 96, 128
-// rows): 1 sequence of 500 keys 9 / 15, 9 / 15, 11 / 18, 14 / 19, 14 / 20; of 4000 14 / 19,
-// 14 / 20, 16 / 21, 23 / 22, 27 / 24; of 16k 20 / 22, 21 / 23, 27 / 25, 53 / 27, 63 / 31;
-// 16 of 4000: 34 / 37, 35 / 38, 53 / 48, 82 / 53, 96 / 59; of 16k 122 / 101, 118 / 102, 180 / 111.
+// rows): 1 sequence of 500 keys 8 / 16, 9 / 16, 10 / 19, 13 / 20, 13 / 21; of 4000 14 / 19,
+// 14 / 20, 16 / 21, 23 / 23, 27 / 23; of 16k 20 / 22, 20 / 22, 26 / 25, 53 / 27, 63 / 29;
+// 16 of 4000: 34 / 37, 34 / 38, 53 / 48, 81 / 56, 95 / 62; of 16k 121 / 101, 117 / 102, 180 / 111.
 int prompt_rows(long long all_tiles) {
     return all_tiles >= 16384 ? kRows + 1 : all_tiles >= 2048 ? 64 : all_tiles >= 512 ? 96 : 128;
 }
