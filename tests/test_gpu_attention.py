@@ -258,3 +258,13 @@ def test_prompts_among_single_tokens(dtype, dim, page, heads, window):
     lens = [3001, 1500, 2, 7, 60, 1, 900, 400, 31, 700, 33, 64]
     check(kc.Batch(26, dtype, new, lens, *heads, dim, page, extra_rows=2).fill(), window=window, sinks=5)
     check(kc.Batch(27, dtype, [700] + [1, 0, 2] * 30, [900] + [80, 5, 2] * 30, *heads, dim, page).fill(), window=window)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("new", [1, 5])
+def test_heads_of_64_over_some_tiles(dtype, page, new):
+    """Eight waves to a workgroup: tiles fewer and more than they are."""
+    lens = [1400, 1000, 700, new, 65 * 8, 64 * 8 + 1, 64 * 13]
+    check(kc.Batch(28, dtype, [new] * 7, lens, 6, 2, 64, page).fill())
+    check(kc.Batch(29, dtype, [new] * 7, lens, 6, 2, 64, page).fill(), window=900, sinks=70)

@@ -8,7 +8,8 @@
 // fp32 products, that of its values the weights.  One pass over the keys, with
 // the running maximum m and sum of each row in fp32.
 //
-// split_kernel.  A workgroup of four waves takes sixteen rows (row r of a kv
+// split_kernel.  A workgroup of four waves (eight with heads of 64 where that
+// takes the place of a cut, see plan()) takes sixteen rows (row r of a kv
 // head: token r / group, head r % group) of one kv head and one sequence, over
 // a chunk of the keys; the waves take its 64-key tiles in turn.  The products
 // run transposed, on v_mfma_f32_16x16x32_f16: S^T = K Q^T, so a lane holds
@@ -98,14 +99,14 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
 // PAGE: pages of 64 keys (a tile), of more (kLarge), or of fewer (kSmall).  With
 // those of a tile or more, a tile's page and scales are the same for all lanes.
 enum { kSmall, kOne, kLarge };
-template <typename T, int D, int PAGE>
-__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) split_kernel(AttnArgs p, int row_tiles) {
+template <typename T, int D, int PAGE, int W>
+__global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_kernel(AttnArgs p, int row_tiles) {
     constexpr bool BIG = PAGE != kSmall;
     constexpr bool kRest = __is_same(T, half_t);   // weights keep their remainder
     constexpr int kC = D / 64;             // 64-element pieces of a key
     constexpr int kT = D / 16;             // 16-element pieces of a value
-    __shared__ float red_m[kWaves][kRows], red_l[kWaves][kRows];
-    __shared__ __align__(16) float red_o[kWaves][kRows][D + 4];
+    __shared__ float red_m[W][kRows], red_l[W][kRows];
+    __shared__ __align__(16) float red_o[W][kRows][D + 4];
     const KvView &c = p.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
@@ -152,12 +153,12 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
             const uint32_t each = (uint32_t)count / (uint32_t)chunks, over = count - each * chunks;
             const auto border = [&](uint32_t k) {      // count * k / chunks, in 32 bits
                 const int at = (int)(each * k + over * k / (uint32_t)chunks);
-                return max(0, at - ((at + shift) & (kWaves - 1)));
+                return max(0, at - ((at + shift) & (W - 1)));
             };
             t0 = split == 0 ? 0 : border(split);
             t1 = split + 1 == chunks ? count : border(split + 1);
         }
-        const int first = t0 + ((wave - t0 - shift) & (kWaves - 1));
+        const int first = t0 + ((wave - t0 - shift) & (W - 1));
         // this lane's row
         const int r = min(r0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
         if (first < t1) {
             ask(first);
             fetch(first);
-            ask(min(first + kWaves, t1 - 1));
+            ask(min(first + W, t1 - 1));
         }
         // One tile, with the next one's loads or without: a condition around the loads would make
         // the products wait for all of them.
@@ -260,8 +261,8 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
                 for (int e = 0; e < 4; ++e) x[4 * t + e] = acc[e] * ks;
             }
             if constexpr (decltype(more)::value) {
-                fetch(i + kWaves);
-                ask(min(i + 2 * kWaves, t1 - 1));
+                fetch(i + W);
+                ask(min(i + 2 * W, t1 - 1));
                 __builtin_amdgcn_sched_barrier(0);
             }
             const bool whole = live == 16 && j0 + kTile <= lo + 1 &&
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
             }
         };
         int i = first;
-        for (; i + kWaves < t1; i += kWaves) tile(i, std::true_type{});
+        for (; i + W < t1; i += W) tile(i, std::true_type{});
         if (i < t1) tile(i, std::false_type{});
 
         // join the four waves
@@ -346,10 +347,10 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
         __syncthreads();
         float all = red_m[0][m];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) all = fmaxf(all, red_m[w][m]);
+        for (int w = 1; w < W; ++w) all = fmaxf(all, red_m[w][m]);
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += red_l[w][m] * __builtin_amdgcn_exp2f(red_m[w][m] - all);
+        for (int w = 0; w < W; ++w) sum += red_l[w][m] * __builtin_amdgcn_exp2f(red_m[w][m] - all);
         const float f = unit * __builtin_amdgcn_exp2f(mx - all);
 #pragma unroll
         for (int e = 0; e < kT; ++e) *reinterpret_cast<float4_t *>(&red_o[wave][m][16 * e + 4 * g]) = o[e] * f;
@@ -358,13 +359,13 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
         const auto joined = [&](int row, int e) {
             float4_t y = *reinterpret_cast<const float4_t *>(&red_o[0][row][e]);
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) y += *reinterpret_cast<const float4_t *>(&red_o[w][row][e]);
+            for (int w = 1; w < W; ++w) y += *reinterpret_cast<const float4_t *>(&red_o[w][row][e]);
             return y;
         };
         if (chunks == 1) {
             // a row of D outputs by 16 lanes
             const int rr = threadIdx.x >> 4;
-            if (r0 + rr <= r1) {
+            if (rr < kRows && r0 + rr <= r1) {
                 const float total_l = __shfl(sum, rr & 15);       // lane m == rr of any group holds row rr's sum
                 const float inv = total_l > 0.0f || !(total_l == total_l) ? 1.0f / total_l : 0.0f;
                 const int tok = (r0 + rr) / p.group, hd = h * p.group + (r0 + rr) % p.group;
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : D > 64 ? 2 : 4) spl
             }
         } else {
             const int rr = threadIdx.x >> 4;
-            if (r0 + rr <= r1) {
+            if (rr < kRows && r0 + rr <= r1) {
                 const int tok = (r0 + rr) / p.group, hd = h * p.group + (r0 + rr) % p.group;
                 float *dst = p.part + (((long long)(s.row0 + tok) * p.q_heads + hd) * p.splits + split) * kPart<D>;
                 for (int e = (threadIdx.x & 15) * 4; e < D; e += 64)
@@ -472,6 +473,7 @@ int prompt_rows(long long all_tiles) {
 // kernel alone, 235 with both; 255 of one: 1854 and 476).
 struct Plan {
     bool prompt, mixed;      // whether the prompt kernel is needed, and both are
+    bool wide;               // eight waves to a workgroup
     int few, prompt_tiles;
     int row_tiles, splits, target;
 };
@@ -484,6 +486,7 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
+    pl.wide = false;
     if (pl.prompt) {
         pl.prompt_tiles = prefill_row_tiles(seqs, rows, kv_heads, group, head_dim, max_q, pl.few, pl.mixed);
         pl.splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
@@ -501,13 +504,30 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
         // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
         // 1126 at eight, 692 at two)
         long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
-        if (tiles <= kUncutTiles || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
+        // Heads of 64 (8 kv heads; us, four waves and joined or not / eight waves and not cut):
+        // 1, 16, 32, 48 sequences of 500 to 1000: 9.2 / 7.9, 12.6 / 8.5, 9.3 / 9.2, 12.0 / 12.6; of 1k to
+        // 2k 9.4 / 10.9, 14.1 / 11.6, 13.9 / 13.2, 18.9 / 19.6; of 3k to 6k 10.8 / 22.4, 24.2 / 24.8,
+        // 31.5 / 30.6, 44.4 / 46.0; of 250 to 500 6.3 / 6.5 at four.  With heads of 128 a CU has room for
+        // eight waves, whose workgroup is no faster (1 of 1000: 12.1 / 12.3).
+        pl.wide = head_dim == 64 && groups <= 256 && tiles > kUncutTiles && tiles <= std::max(24ll, groups / 2);
+        if (tiles <= kUncutTiles || pl.wide || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
         pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
     }
     // (a launch has less than 2^32 threads)
     const long long once = (long long)(units + kXcds) * pl.splits * kv_heads;
     pl.row_tiles = (int)std::max<long long>(1, std::min<long long>(pl.row_tiles, ((1 << 24) - 1) / once));
     return pl;
+}
+
+template <typename T, int D, int W>
+void launch_split(const AttnArgs &p, int row_tiles, int grid, hipStream_t s) {
+    const int page = 1 << p.c.log2_page;
+    if (page == kTile)
+        split_kernel<T, D, kOne, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
+    else if (page > kTile)
+        split_kernel<T, D, kLarge, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
+    else
+        split_kernel<T, D, kSmall, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
 }
 
 template <typename T, int D>
@@ -522,13 +542,14 @@ hipError_t launch(AttnArgs p, const Plan &pl, bool bf16, hipStream_t s) {
         p.few = pl.mixed ? pl.few : 0x7FFFFFFF;
         const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
         const int grid = units * p.c.kv_heads * pl.row_tiles;
-        const int page = 1 << p.c.log2_page;
-        if (page == kTile)
-            split_kernel<T, D, kOne><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-        else if (page > kTile)
-            split_kernel<T, D, kLarge><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
-        else
-            split_kernel<T, D, kSmall><<<grid, 64 * kWaves, 0, s>>>(p, pl.row_tiles);
+        if constexpr (D == 64) {
+            if (pl.wide)
+                launch_split<T, D, 2 * kWaves>(p, pl.row_tiles, grid, s);
+            else
+                launch_split<T, D, kWaves>(p, pl.row_tiles, grid, s);
+        } else {
+            launch_split<T, D, kWaves>(p, pl.row_tiles, grid, s);
+        }
         e = hipGetLastError();
     }
     if (e != hipSuccess || p.part == nullptr) return e;
