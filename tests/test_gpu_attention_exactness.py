@@ -1,0 +1,97 @@
+"""awq_attention on the GPU, as exact as fp32 weights make it, and at magnitudes where a
+kernel's own numbers could leave their types."""
+import math
+
+import pytest
+import torch
+
+import kv_cases as kc
+from w4a16_group_quantized_amd import binding
+
+LOG2E = math.log2(math.e)
+
+
+def run(t, **kw):
+    cache, batch, q, _, _ = t.device(kw.pop("max_q", None), kw.pop("max_kv", None))
+    out = binding.attention(q, cache, batch, **kw)
+    torch.cuda.synchronize()
+    return out.cpu()[: t.starts[-1]].double()
+
+
+def code(x):
+    return torch.tensor(float(x)).to(kc.F8).view(torch.uint8)
+
+
+def within(have, want, tol):
+    assert torch.equal(have.isnan(), want.isnan())
+    off = ((have - want).abs() - tol).nan_to_num(0.0)
+    at = int(off.argmax())
+    assert float(off.max()) <= 0, (at, float(have.flatten()[at]), float(want.flatten()[at]), float(tol.flatten()[at]))
+
+
+def one_hot(t):
+    """Queries of one element each, 0.5 to 8 of either sign, so that a score is one product
+    and nothing of a sum's roundings comes into it."""
+    q = t.split()[0]
+    at = torch.randint(0, t.dim, (*q.shape[:2], 1), generator=t.g)
+    size = torch.exp2(torch.randint(-1, 4, at.shape, generator=t.g)) * (torch.randint(0, 2, at.shape, generator=t.g) * 2 - 1)
+    q.zero_()
+    q.scatter_(-1, at, size.to(q.dtype))
+    return t
+
+
+def fine_tolerance(t, out, size, reach, vmax, weight=2.0 ** -21):
+    """Scores of one product each: with log2(e), the scale, the page's scale, the maximum and the
+    exponential at most eight roundings of 2^-24 of numbers up to 2 * reach * log2(e) + 16.
+    A weight as two halves: 2^-22 of it (twice that, for the output's two sums), and where it
+    is so small that its remainder is a subnormal, 2^-25 where the row's largest is 2^5 or more:
+    2^-30 of the largest for each key.  Sums over the keys as in kv_cases.attention_tolerance.
+    Then the output's own rounding."""
+    keys = max([1, *t.lens])
+    each = 8 * 2.0 ** -24 * (2 * reach * LOG2E + 16) + weight + (keys / 8 + 64) * 2.0 ** -24
+    near = 2 * each[..., None] * size + keys * 2.0 ** -30 * vmax
+    return near + kc.half_step(t.dtype) * (out.abs() + near) + torch.finfo(t.dtype).smallest_normal * kc.half_step(t.dtype)
+
+
+SHAPES = [(64, 16, (4, 2)), (128, 64, (8, 2)), (256, 64, (4, 2)), (256, 16, (2, 2)), (128, 128, (5, 1)), (64, 256, (3, 3))]
+ROWS = [([1] * 9, [700, 90, 64, 33, 1000, 1, 500, 65, 300]), ([5, 3, 9], [1000, 64, 400]), ([150, 70], [300, 900])]
+
+
+def signed_sums(dtype, dim, page, heads, new, lens):
+    """Sums of values of either sign come out far below their terms, so weights rounded to one
+    half (2^-12 of each term) show in them.  (inputs, the definition's outputs, tolerance)"""
+    t = one_hot(kc.Batch(90, dtype, new, lens, *heads, dim, page)).fill()
+    t.ks.fill_(2.0 ** -6)
+    want, size, reach = kc.attention(t)
+    return t, want, fine_tolerance(t, want, size, reach, 448 * float(t.vs.max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,page,heads", SHAPES)
+@pytest.mark.parametrize("new,lens", ROWS)
+def test_weights_of_more_than_one_half(dtype, dim, page, heads, new, lens):
+    t, want, tol = signed_sums(dtype, dim, page, heads, new, lens)
+    within(run(t), want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("new,lens", ROWS)
+def test_the_tolerance_tells_one_half_from_two(dtype, new, lens):
+    """The same sums on the CPU with weights as halves: within the tolerance as two, not as one."""
+    t, want, tol = signed_sums(dtype, 64, 16, (4, 2), new, lens)
+    one, two = torch.zeros_like(want), torch.zeros_like(want)
+    q = t.split()[0].double()
+    for b, n in enumerate(new):
+        rows = slice(t.starts[b], t.starts[b + 1])
+        k, v, _ = t.held(b, lens[b])
+        hidden = torch.arange(lens[b]) > (lens[b] - n + torch.arange(n))[:, None]
+        for h in range(4):
+            x = (q[rows, h] @ k[h // 2].t()).masked_fill(hidden, -math.inf) * t.dim ** -0.5
+            w = torch.exp(x - x.amax(1, keepdim=True)) * 2.0 ** 11
+            lead = w.half().double()
+            one[rows, h] = lead @ v[h // 2] / w.sum(1, keepdim=True)
+            two[rows, h] = (lead + (w - lead).half().double()) @ v[h // 2] / w.sum(1, keepdim=True)
+    within(two.to(t.dtype).double(), want, tol)
+    with pytest.raises(AssertionError):
+        within(one.to(t.dtype).double(), want, tol)

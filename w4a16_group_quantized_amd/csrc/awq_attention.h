@@ -107,6 +107,20 @@ __device__ __forceinline__ float group_sum(float x) {
     return half_sum(v.x + v.y);
 }
 
+// Two weights as halves, and what their roundings leave, as halves again: together they are
+// off by 2^-22 of a weight (or 2^-25, where the weight is below 2^-3 and the remainder a
+// subnormal), so that a product with both is one with fp32 weights.  One conversion and two
+// multiply-adds, which take a half as it lies.
+__device__ __forceinline__ void lead_and_rest(float a, float b, uint32_t &lead, uint32_t &rest) {
+    const half2_t h = {(half_t)a, (half_t)b};
+    lead = __builtin_bit_cast(uint32_t, h);
+    asm("v_fma_mixlo_f16 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(rest) : "v"(lead), "v"(a));
+    asm("v_fma_mixhi_f16 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(rest) : "v"(lead), "v"(b));
+}
+__device__ __forceinline__ half8_t halves8(const uint32_t w[4]) {
+    return __builtin_bit_cast(half8_t, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
 // Four masks of four bytes each: the first `live` of sixteen bytes.
 __device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
 #pragma unroll

@@ -27,7 +27,12 @@
 //
 // Few row tiles over many keys are cut into chunks of keys, joined by combine_kernel.
 //
-// Weights are rounded to fp16 once; the sum takes them before the rounding.
+// Weights go into the products as two halves, the leading part and its remainder
+// (lead_and_rest), as in the split kernel: a query's outputs are as exact in a prompt as alone.
+// Half more matrix instructions for it: 4096 rows 166 -> 208 us, chunks of 512 rows on 16k
+// contexts 700 -> 890 us, 8192 rows of 256 elements under a window 194 -> 232 us; with one
+// half the error against 64 bits was 2.4e-4 where fp16's own rounding makes 1.8e-4.
+// The sum takes them before the roundings.
 // They are scaled by 2^11 so that small ones stay normal numbers, and the
 // maximum that they refer to is moved only when a row exceeds it by 2^4, so the
 // largest is 2^15, and rescaling the outputs is rare after the first tiles.
@@ -69,6 +74,16 @@ __device__ __forceinline__ int piece(int row, int at) {
     return row * C + (C >= 8 ? at ^ (row & 7) : at ^ ((row >> 1) & 3));
 }
 
+// The outputs of 32 elements, and sixteen codes of each times weights w (their leading
+// parts in w[0] and w[1], their remainders in w[2] and w[3]).
+__device__ __forceinline__ void add_products(float16_t &o, uint4 codes, const half8_t w[4]) {
+    const half8_t a = e4m3x8_to_half(codes.x, codes.y), b = e4m3x8_to_half(codes.z, codes.w);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[0], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[2], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[1], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[3], o, 0, 0, 0);
+}
+
 // BIG: pages of at least a tile, so that a tile's page and scales are the same for
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
@@ -80,8 +95,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     constexpr int kRows = rows_of(D);          // rows of a workgroup
     constexpr int kO = kPairs ? kP / 2 : kP;   // 32-element blocks of a value that a wave sums up
     constexpr int kLoads = D / 64;             // loads of a wave for the keys of a tile, and for the values
-    __shared__ uint4 weights[kWaves][2][64];   // (with pairs)
-    __shared__ float tops[kWaves][64];
+    // (with pairs) A wave's weights, written by it and read by its partner; and, between that
+    // reading and the next writing, what the partner has to tell it: a maximum or a sum.
+    __shared__ uint4 weights[kWaves][4][64];
     __shared__ uint4 kbuf0[kTile * kC], vbuf0[kTile * kC], kbuf1[kTile * kC], vbuf1[kTile * kC];
     const KvView &c = p.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -213,6 +229,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         auto live_keys = [&](int j0, int grp, uint64_t ok) {
             return (ok >> grp) & 1 ? min(max(s.len - j0 - 16 * grp, 0), 16) : 0;
         };
+        const auto tell = [&](float x) { reinterpret_cast<uint32_t *>(weights[wave ^ 1])[lane] = __builtin_bit_cast(uint32_t, x); };
+        const auto told = [&]() { return __builtin_bit_cast(float, reinterpret_cast<const uint32_t *>(weights[wave])[lane]); };
         auto clear_dead = [&](int j0, uint4 *vb, uint64_t ok) {
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
@@ -266,12 +284,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
 #pragma unroll
                 for (int e = 3; e < 15; e += 2) a = max3(a, acc[e], acc[e + 1]);
                 top = half_max(max3(a, a, acc[15]) * ks);
-                tops[wave][lane] = top;
+                tell(top);
             };
             // the weights, of the maximum of both waves
-            half8_t w[2];
+            half8_t w[4];                      // leading parts, remainders
             auto weigh = [&]() {
-                const float now = fmaxf(top, tops[wave ^ 1][lane]);
+                const float now = fmaxf(top, told());
                 // The outputs count in units of a values' scale, at least that of every page so far and
                 // at most 2^6 times this tile's: moved with the maximum, which is rare.
                 if (__any(now > mx + kSlack) || vmost > unit || (vmost > 0.0f && vmost < unit * kLeastUnit)) {
@@ -295,31 +313,39 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 }
                 const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - shift;
                 float sum = 0.0f;
+                uint32_t lead[8], rest[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 16; e += 2) {
                     const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e], ks, base));
+                    const float g = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e + 1], ks, base));
                     sum += f;
-                    w[e >> 3][e & 7] = (half_t)f;
+                    sum += g;
+                    lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                 }
                 l += sum * (1.0f / ratio);
-                weights[wave][0][lane] = __builtin_bit_cast(uint4, w[0]);
-                weights[wave][1][lane] = __builtin_bit_cast(uint4, w[1]);
-            };
-            auto add_values = [&](const uint4 *vb) {
-                const half8_t x0 = __builtin_bit_cast(half8_t, weights[wave ^ 1][0][lane]), x1 = __builtin_bit_cast(half8_t, weights[wave ^ 1][1][lane]);
-                const int row = 32 * kO * side + m;
-                uint4 v0 = vb[piece<4>(row, 2 * side + hf)], v1 = vb[piece<4>(row, 2 * (side ^ 1) + hf)];
 #pragma unroll
-                for (int e = 0; e < kO; ++e) {
-                    const uint4 a0 = v0, a1 = v1;
-                    if (e + 1 < kO) {
-                        v0 = vb[piece<4>(row + 32 * e + 32, 2 * side + hf)];
-                        v1 = vb[piece<4>(row + 32 * e + 32, 2 * (side ^ 1) + hf)];
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
+                    weights[wave][e][lane] = __builtin_bit_cast(uint4, w[e]);
+                }
+            };
+            // the wave's own 32 keys first, then its partner's, for which its own weights' registers are free
+            auto add_values = [&](const uint4 *vb) {
+                const int row = 32 * kO * side + m;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int at = 2 * (u ? side ^ 1 : side) + hf;
+                    uint4 v = vb[piece<4>(row, at)];
+                    if (u) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(half8_t, weights[wave ^ 1][e][lane]);
                     }
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[1], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), x0, o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), x1, o[e], 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < kO; ++e) {
+                        const uint4 codes = v;
+                        if (e + 1 < kO) v = vb[piece<4>(row + 32 * e + 32, at)];
+                        add_products(o[e], codes, w);
+                    }
                 }
             };
 
@@ -375,7 +401,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         } else {
             auto multiply = [&](int j0, const uint4 *kb, const uint4 *vb, float ksl, float vsl, uint64_t ok) {
                 // the pieces of the next products are read while these run; the barriers keep the
-                // compiler from reading all of them at once, for which there are no registers
+                // compiler from reading all of them at once, for which there are no registers (beside the
+                // values' products, where there are, barriers took 2%)
                 float16_t acc[2] = {};
                 uint4 k0 = kb[piece<kC>(m, hf)], k1 = kb[piece<kC>(32 + m, hf)];
 #pragma unroll
@@ -462,18 +489,23 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     }
                     shift = 0.0f;
                 }
-                half8_t w[2][2];
+                half8_t w[2][4];               // leading parts, remainders
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float base = kWeightBits + bits[u] - shift;
                     float sum = 0.0f;
+                    uint32_t lead[8], rest[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 16; e += 2) {
                         const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                        const float g = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e + 1], ks[u], base));
                         sum += f;
-                        w[u][e >> 3][e & 7] = (half_t)f;
+                        sum += g;
+                        lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                     }
                     l += sum * back[u];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[u][e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
                 }
 #pragma unroll
                 for (int e = 0; e < kP; ++e) {
@@ -482,11 +514,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                         v0 = vb[piece<4>(32 * e + 32 + m, hf)];
                         v1 = vb[piece<4>(32 * e + 32 + m, 2 + hf)];
                     }
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0][0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[0][1], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), w[1][0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), w[1][1], o[e], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
+                    add_products(o[e], a0, w[0]);
+                    add_products(o[e], a1, w[1]);
                 }
             };
 
@@ -519,9 +548,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         }
         l = half_sum(l);
         if constexpr (kPairs) {
-            tops[wave][lane] = l;
+            tell(l);
             __syncthreads();
-            l += tops[wave ^ 1][lane];
+            l += told();
         }
         if (!idle && w0 + m <= r1) {
             const long long at = (long long)(s.row0 + token) * p.q_heads + head;
