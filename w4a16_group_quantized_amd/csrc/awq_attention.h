@@ -84,8 +84,18 @@ __device__ __forceinline__ float half_sum(float x) {
     const float2 v = halves(x);
     return v.x + v.y;
 }
+// Matrix results before inline assembly reads them, and what it wrote before products read
+// it.  The compiler puts the wait states that a vector instruction needs behind a matrix one
+// (12 behind a 32x32x16), and a matrix one behind a vector one (2), around its own
+// instructions only.
+__device__ __forceinline__ void settle(float16_t &acc) { asm volatile("s_nop 15" : "+v"(acc)); }
+__device__ __forceinline__ void settle(float16_t &a, float16_t &b) { asm volatile("s_nop 15" : "+v"(a), "+v"(b)); }
+__device__ __forceinline__ void settle(uint32_t (&w)[8]) {
+    asm volatile("s_nop 1" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4]), "+v"(w[5]), "+v"(w[6]), "+v"(w[7]));
+}
+
 // The largest of three (NaN only if all are), without the instructions that the
-// compiler puts before fmaxf to quiet NaNs.
+// compiler puts before fmaxf to quiet NaNs.  Not of matrix results as they come: settle() first.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -110,7 +120,7 @@ __device__ __forceinline__ float group_sum(float x) {
 // Two weights as halves, and what their roundings leave, as halves again: together they are
 // off by 2^-22 of a weight (or 2^-25, where the weight is below 2^-3 and the remainder a
 // subnormal), so that a product with both is one with fp32 weights.  One conversion and two
-// multiply-adds, which take a half as it lies.
+// multiply-adds, which take a half as it lies.  (Remainders before products: settle().)
 __device__ __forceinline__ void lead_and_rest(float a, float b, uint32_t &lead, uint32_t &rest) {
     const half2_t h = {(half_t)a, (half_t)b};
     lead = __builtin_bit_cast(uint32_t, h);

@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
                 sum += b;
                 lead_and_rest(a, b, lead[e / 2], rest[e / 2]);
             }
+            settle(rest);
             const half8_t ph[2] = {halves8(lead), halves8(lead + 4)}, pl[2] = {halves8(rest), halves8(rest + 4)};
             l += sum / ratio;
 #pragma unroll

@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), qf[e][0], acc, 0, 0, 0);
                     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), qf[e][1], acc, 0, 0, 0);
                 }
+                settle(acc);
                 // (every row of the wave sees every key of most tiles)
                 if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
                     (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     sum += g;
                     lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                 }
+                settle(rest);
                 l += sum * (1.0f / ratio);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), qf[e][1], acc[1], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                settle(acc[0], acc[1]);
                 // (every row of the wave sees every key of most tiles)
                 if ((ok & 15) != 15 || j0 + kTile > lo + 1 ||
                     (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
@@ -503,6 +506,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                         sum += g;
                         lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                     }
+                    settle(rest);
                     l += sum * back[u];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[u][e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
