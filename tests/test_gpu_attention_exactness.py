@@ -95,3 +95,39 @@ def test_the_tolerance_tells_one_half_from_two(dtype, new, lens):
     within(two.to(t.dtype).double(), want, tol)
     with pytest.raises(AssertionError):
         within(one.to(t.dtype).double(), want, tol)
+
+
+def scale_of_one():
+    """A scale whose product with log2(e) is 1 in fp32, so that scores are in the exponent's units."""
+    e = torch.tensor(LOG2E, dtype=torch.float32)
+    at = torch.tensor(1 / LOG2E, dtype=torch.float32)
+    near = [at, torch.nextafter(at, at * 2), torch.nextafter(at, at * 0)]
+    return float(next(s for s in near if float(s * e) == 1.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,page", [(64, 64), (128, 16), (128, 64), (256, 64), (256, 32)])
+@pytest.mark.parametrize("new", [1, 6, 150])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_maxima_one_step_of_fp32_apart(dtype, dim, page, new, sign):
+    """Scores around 2^26, where fp32 has steps of 8: a maximum of 2^23 + 1 such steps (or
+    -(2^23 + 3)) and, tiles later, one a step above it.  The weight of the first is 2^-8 of
+    the second's; the other keys are far below both."""
+    t = kc.Batch(91, dtype, [new], [400], 2, 1, dim, page).fill()
+    t.ks.fill_(8.0)
+    t.vs.fill_(1.0)
+    q = t.split()[0]
+    q.zero_()
+    q[..., 0], q[..., 1] = 2.0 ** 15, 1.0
+    t.k.zero_()
+    if sign < 0:
+        t.k[..., 0] = code(-288)
+    first, later = (1, 2) if sign > 0 else (-3, -2)
+    for pos, low, value in ((3, first, 1), (133, later, 2)):
+        id, slot = int(t.table[0, pos // page]), pos % page
+        t.k[id, 0, slot, 0], t.k[id, 0, slot, 1] = code(256 * sign), code(low)
+        t.v[id, 0, :, slot] = code(value)
+    want = torch.full((new, 2, dim), (2 + 2.0 ** -8) / (1 + 2.0 ** -8), dtype=torch.float64)
+    # the exponential, a quotient and sums of two: a few of 2^-24; the output's rounding
+    within(run(t, scale=scale_of_one()), want, want * (kc.half_step(t.dtype) + 2.0 ** -20))

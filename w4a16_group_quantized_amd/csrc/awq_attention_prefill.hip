@@ -35,7 +35,8 @@
 // The sum takes them before the roundings.
 // They are scaled by 2^11 so that small ones stay normal numbers, and the
 // maximum that they refer to is moved only when a row exceeds it by 2^4, so the
-// largest is 2^15, and rescaling the outputs is rare after the first tiles.
+// largest is 2^15, and rescaling the outputs is rare after the first tiles.  (The difference
+// is compared: mx + 2^4 rounds up by half a step of 2^26 and more.)
 #include <algorithm>
 
 #include "awq_attention.h"
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 const float now = fmaxf(top, told());
                 // The outputs count in units of a values' scale, at least that of every page so far and
                 // at most 2^6 times this tile's: moved with the maximum, which is rare.
-                if (__any(now > mx + kSlack) || vmost > unit || (vmost > 0.0f && vmost < unit * kLeastUnit)) {
+                if (__any(now - mx > kSlack) || vmost > unit || (vmost > 0.0f && vmost < unit * kLeastUnit)) {
                     const float to = fmaxf(mx, now), to_unit = vmost > 0.0f ? vmost : unit;
                     const float alpha = __builtin_amdgcn_exp2f(mx - to);
                     const float turn = alpha * (unit / to_unit);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 // The outputs count in units of a values' scale, at least that of every page so far and
                 // at most 2^6 times this tile's: moved with the maximum, which is rare.
                 const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-                if (__any(now > mx + kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
+                if (__any(now - mx > kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
                     const float to = fmaxf(mx, now), to_unit = most > 0.0f ? most : unit;
                     const float alpha = __builtin_amdgcn_exp2f(mx - to);
                     const float turn = alpha * (unit / to_unit);
