@@ -131,3 +131,41 @@ def test_maxima_one_step_of_fp32_apart(dtype, dim, page, new, sign):
     want = torch.full((new, 2, dim), (2 + 2.0 ** -8) / (1 + 2.0 ** -8), dtype=torch.float64)
     # the exponential, a quotient and sums of two: a few of 2^-24; the output's rounding
     within(run(t, scale=scale_of_one()), want, want * (kc.half_step(t.dtype) + 2.0 ** -20))
+
+
+def page_scales(t, level):
+    """Values of one sequence: pages' scales 2^level(first token of the page, its number), and
+    codes of zero where that is None (the append gives such pages 2^-64)."""
+    for j in range(-(-t.lens[0] // t.page)):
+        id, e = int(t.table[0, j]), level(j * t.page, j)
+        t.vs[id] = 2.0 ** (-64 if e is None else e)
+        if e is None:
+            t.v[id] = 0
+    return t
+
+
+PATTERNS = {
+    "zeros between large values": lambda pos, j: 50 if pos < 700 or pos > 1200 else None,
+    "zeros before large values": lambda pos, j: None if pos < 700 else 50,
+    "zeros beside large values": lambda pos, j: 60 if j % 3 else None,
+    "one and the least normal number": lambda pos, j: 0 if pos < 700 else -126,
+    "both in a tile": lambda pos, j: -126 if j % 2 else 0,
+    "from end to end": lambda pos, j: 100 if j % 2 else -100,
+    "large alone": lambda pos, j: 112,
+    "small alone": lambda pos, j: -112,
+    "the least normal number alone": lambda pos, j: -126,
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 64), (128, 32), (128, 128), (256, 16), (256, 64)])
+@pytest.mark.parametrize("new", [1, 6, 150])
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_value_scales_from_end_to_end(dim, page, new, pattern):
+    """Whatever a cache's scales are, from 2^-126 to values of 2^120 that bf16 holds, nothing on
+    the way to an output leaves fp32, and the outputs are as exact as with scales alike."""
+    t = one_hot(kc.Batch(92, "bf16", [new], [1500], 4, 2, dim, page)).fill()
+    t.ks.fill_(2.0 ** -7)
+    page_scales(t, PATTERNS[pattern])
+    want, size, reach = kc.attention(t)
+    within(run(t), want, fine_tolerance(t, want, size, reach, 448 * float(t.vs[t.table.long()].max())))

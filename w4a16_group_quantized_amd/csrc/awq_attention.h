@@ -11,6 +11,7 @@ constexpr float kEmpty = -0x1.fffffep127f; // running maximum of a row that has 
 // From here on a maximum is taken off the scores before anything is added: its steps are
 // half an exponent's and more, and a sum with it would lose the rest.
 constexpr float kFar = 0x1p23f;
+constexpr float kNone = -0x1p14f;           // logarithm of a scale where there is none: below that of any
 constexpr int kWidest = 1 << 30;           // a window of this many tokens sees all: no position is past it
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -56,6 +57,29 @@ __device__ __forceinline__ int seq_of_rank(const KvView &c, int rank) {
     }
     return (int)__builtin_ctzll(__ballot(lane < c.seqs && above == rank));
 }
+
+// The scale that a row's outputs count in, and the largest so far in terms of the running
+// maximum, as logarithms: quotients of scales may leave fp32.  It follows the pages' scales,
+// so that weights are normal halves whatever these are, but not further down than 2^60 from the
+// largest: outputs, below 2^45 of their unit, stay far from fp32's end.  (A page of zeros has
+// 2^-64, and values of bf16 reach 2^127.)
+struct OutUnit {
+    static constexpr float kDrop = 6.0f, kMostFall = 60.0f;
+    float at = kNone, peak = kNone;
+    // whether a tile whose largest scale is 2^most calls for another
+    __device__ __forceinline__ bool moves(float most) const { return most > at || (most < at - kDrop && most > kNone); }
+    // goes along where the maximum rises by -down; returns what the outputs are to be multiplied by
+    __device__ __forceinline__ float move(float most, float down) {
+        peak = fmaxf(peak, at) + down;
+        const float next = fmaxf(moves(most) ? most : at, peak - kMostFall);
+        const float turn = __builtin_amdgcn_exp2f(down + (at - next));
+        at = next;
+        return turn;
+    }
+};
+// From here on a tile's weights, times a page's scale to the unit, are too small to sum up the
+// weights from.
+constexpr float kLeastToUnit = -60.0f;
 
 template <typename T>
 __device__ __forceinline__ half8_t as_row_half(const uint16_t *p, float f) {
@@ -140,8 +164,8 @@ __device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
     }
 }
 
-// A partial result of a chunk of keys, in the workspace: D outputs, the maximum, the
-// sum and (of chunk 0) the number of chunks.
+// A partial result of a chunk of keys, in the workspace: D outputs (over the sum), the
+// maximum, the sum and (of chunk 0) the number of chunks.
 template <int D>
 constexpr int kPart = D + 4;
 

@@ -40,7 +40,6 @@ constexpr int kRows = 16;                  // rows of a workgroup
 constexpr int kWaves = 4;
 constexpr int kXcds = 8;
 constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of the formula
-constexpr float kLeastUnit = 0x1p-6f;
 
 // How a call is cut into chunks of keys, from the number of (sequence, kv head, row
 // tile) groups and, on the device, from the sequences' lengths.  Measured at 32 heads
@@ -191,7 +190,8 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
 #pragma unroll
             for (int half = 0; half < 2; ++half) qf[i][half] = as_row_half<T>(qrow + 64 * i + 16 * g + 8 * half, up);
 
-        float mx = kEmpty, l = 0.0f, unit = 1.0f;       // unit: the scale of the values that o counts in
+        float mx = kEmpty, l = 0.0f;
+        OutUnit unit;                                   // the scale of the values that o counts in
         float4_t o[kT];
 #pragma unroll
         for (int i = 0; i < kT; ++i) o[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -290,28 +290,30 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
 #pragma unroll
             for (int e = 3; e < 15; e += 2) top = max3(top, x[e], x[e + 1]);
             top = group_max(max3(top, top, x[15]));
-            // The outputs count in units of a values' scale, at least that of every page so far and
-            // at most 2^6 times this tile's; what a page's is to it goes into the exponent.
-            const float most = BIG ? vs : group_max(vs);
-            const float now = fmaxf(mx, top), to_unit = most > unit || most < unit * kLeastUnit ? most : unit;
-            const float next_unit = most > 0.0f ? to_unit : unit;
-            if (__any(now != mx) || next_unit != unit) {
-                const float alpha = __builtin_amdgcn_exp2f(mx - now);
-                const float turn = alpha * (unit / next_unit);
-                l *= alpha;
+            // What a page's scale is to the outputs' unit goes into the exponent.
+            const float lv = __builtin_amdgcn_logf(vs);               // (no page: -inf)
+            const float most = BIG ? lv : group_max(lv);
+            const float now = fmaxf(mx, top);
+            if (__any(now != mx || unit.moves(most))) {
+                l *= __builtin_amdgcn_exp2f(mx - now);
+                const float turn = unit.move(most, mx - now);
 #pragma unroll
                 for (int t = 0; t < kT; ++t) o[t] *= turn;
-                unit = next_unit;
                 mx = now;
             }
-            const float ratio = vs > 0.0f ? vs / unit : 1.0f;         // (no weight where there is no page)
+            const float to_unit = lv > kNone ? lv - unit.at : 0.0f;   // (no weight where there is no page)
             float shift = mx;
             if (__any(fabsf(mx) >= kFar)) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] -= mx;
                 shift = 0.0f;
             }
-            const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - shift;
+            const float base = kWeightBits + to_unit - shift;
+            const bool far = __any(to_unit < kLeastToUnit);
+            if (far) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(x[e] + (kWeightBits - shift));
+            }
             float sum = 0.0f;
             uint32_t lead[8], rest[8];
 #pragma unroll
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
             }
             settle(rest);
             const half8_t ph[2] = {halves8(lead), halves8(lead + 4)}, pl[2] = {halves8(rest), halves8(rest + 4)};
-            l += sum / ratio;
+            if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit);
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
                 const half8_t v0 = e4m3x8_to_half(vc[t].x, vc[t].y), v1 = e4m3x8_to_half(vc[t].z, vc[t].w);
@@ -350,9 +352,12 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) sum += red_l[w][m] * __builtin_amdgcn_exp2f(red_m[w][m] - all);
-        const float f = unit * __builtin_amdgcn_exp2f(mx - all);
+        // over the sum first: outputs that are no larger than the values are; the unit last, which
+        // may be the least number
+        const float inv = sum > 0.0f || !(sum == sum) ? 1.0f / sum : 0.0f;
+        const float f = __builtin_amdgcn_exp2f(mx - all), scale = __builtin_amdgcn_exp2f(unit.at);
 #pragma unroll
-        for (int e = 0; e < kT; ++e) *reinterpret_cast<float4_t *>(&red_o[wave][m][16 * e + 4 * g]) = o[e] * f;
+        for (int e = 0; e < kT; ++e) *reinterpret_cast<float4_t *>(&red_o[wave][m][16 * e + 4 * g]) = o[e] * inv * f * scale;
         __syncthreads();
         // (each wave its own: one after the other into the same took 0.8 us longer, 4 with 256 elements)
         const auto joined = [&](int row, int e) {
@@ -365,12 +370,10 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
             // a row of D outputs by 16 lanes
             const int rr = threadIdx.x >> 4;
             if (rr < kRows && r0 + rr <= r1) {
-                const float total_l = __shfl(sum, rr & 15);       // lane m == rr of any group holds row rr's sum
-                const float inv = total_l > 0.0f || !(total_l == total_l) ? 1.0f / total_l : 0.0f;
                 const int tok = (r0 + rr) / p.group, hd = h * p.group + (r0 + rr) % p.group;
                 uint16_t *dst = p.out + ((long long)(s.row0 + tok) * p.q_heads + hd) * D;
                 for (int e = (threadIdx.x & 15) * 8; e < D; e += 128) {
-                    const float4_t a = joined(rr, e) * inv, b = joined(rr, e + 4) * inv;
+                    const float4_t a = joined(rr, e), b = joined(rr, e + 4);
                     const float y[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
                     *reinterpret_cast<uint4 *>(dst + e) = pack8<T>(y);
                 }
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
                 float *dst = p.part + (((long long)(s.row0 + tok) * p.q_heads + hd) * p.splits + split) * kPart<D>;
                 for (int e = (threadIdx.x & 15) * 4; e < D; e += 64)
                     *reinterpret_cast<float4_t *>(dst + e) = joined(rr, e);
-                const float total_l = __shfl(sum, rr & 15), total_m = __shfl(all, rr & 15);
+                const float total_l = __shfl(sum, rr & 15), total_m = __shfl(all, rr & 15);  // lane m == rr of any group holds row rr's
                 if ((threadIdx.x & 15) == 0) {
                     dst[D] = total_m;
                     dst[D + 1] = total_l;
@@ -427,27 +430,26 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
         if ((tid & 63) == 0) red[0][tid >> 6] = mx;
         __syncthreads();
         mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-        const float f = __builtin_amdgcn_exp2f(own - mx);
-        if (tid < n) weight[tid] = f;
-        l = tid < n ? l * f : 0.0f;
+        l = tid < n ? l * __builtin_amdgcn_exp2f(own - mx) : 0.0f;
+        if (tid < n) weight[tid] = l;
         for (int k = 32; k > 0; k >>= 1) l += __shfl_xor(l, k);
         if ((tid & 63) == 0) red[1][tid >> 6] = l;
         __syncthreads();
         l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+        const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
         const int lane = tid % kLanes, at = tid / kLanes;
         float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int k = at; k < n; k += kAtOnce)
-            o += weight[k] * *reinterpret_cast<const float4_t *>(src + k * kPart<D> + 4 * lane);
+            o += weight[k] * inv * *reinterpret_cast<const float4_t *>(src + k * kPart<D> + 4 * lane);
         part[at][lane] = o;
         __syncthreads();
         if (at == 0) {
 #pragma unroll
             for (int k = 1; k < kAtOnce; ++k) o += part[k][lane];
-            const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
             uint2 y;
-            y.x = (uint32_t)from_float<T>(o[0] * inv) | ((uint32_t)from_float<T>(o[1] * inv) << 16);
-            y.y = (uint32_t)from_float<T>(o[2] * inv) | ((uint32_t)from_float<T>(o[3] * inv) << 16);
+            y.x = (uint32_t)from_float<T>(o[0]) | ((uint32_t)from_float<T>(o[1]) << 16);
+            y.y = (uint32_t)from_float<T>(o[2]) | ((uint32_t)from_float<T>(o[3]) << 16);
             *reinterpret_cast<uint2 *>(p.out + (long long)i * D + 4 * lane) = y;
         }
         __syncthreads();                       // the LDS arrays are free again

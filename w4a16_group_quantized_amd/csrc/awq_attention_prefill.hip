@@ -50,7 +50,7 @@ constexpr int kWaveRows = 32, kWaves = 4;
 // 500 keys, one sequence: 33 / 38 / 16 us at 16 tiles, 23 / 22 / 16 at 8, 21 / 17 / 14 at 4;
 // 16 sequences of 500: 17 / 17 / 21.
 constexpr int kLeastChunk = 6, kMostSplits = 32;
-constexpr float kWeightBits = 11.0f, kSlack = 4.0f, kLeastUnit = 0x1p-6f;
+constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
 
 // Heads of 256 elements: two waves share 32 rows.  Elsewhere a wave has 32 rows to itself.
 constexpr bool in_pairs(int head_dim) { return head_dim > 128; }
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
 #pragma unroll
             for (int e = 0; e < 2; ++e) qf[i][e] = as_row_half<T>(qrow + 32 * i + 8 * e, up);
 
-        float mx = kEmpty, l = 0.0f, unit = 1.0f;
+        float mx = kEmpty, l = 0.0f;
+        OutUnit unit;                          // the scale of the values that o counts in
         float16_t o[kO];
 #pragma unroll
         for (int i = 0; i < kO; ++i) o[i] = float16_t{};
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         if constexpr (kPairs) {
             // the scores of a tile: the wave's 32 keys
             float16_t acc;
-            float ks = 1.0f, vmost = 0.0f, vown = 0.0f, top = 0.0f;
+            float ks = 1.0f, vmost = kNone, vown = kNone, top = 0.0f;
             auto scores = [&](int j0, const uint4 *kb, float ksl, float vsl, uint64_t ok) {
                 acc = float16_t{};
                 uint4 k0 = kb[piece<kC>(32 * side + m, hf)];
@@ -273,9 +274,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                         acc[e] = see ? acc[e] : -__builtin_inff();
                     }
                 }
+                const float vlog = __builtin_amdgcn_logf(vsl);
                 float vs[4];
 #pragma unroll
-                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
+                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vlog, g) : kNone;
                 const float k_lo = lane_value(ksl, BIG ? 0 : 2 * side), k_hi = BIG ? k_lo : lane_value(ksl, 2 * side + 1);
                 // never 0, which would turn a hidden key's -inf into NaN; and where there is no page
                 // the scale may be anything, but no key is seen
@@ -292,19 +294,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
             half8_t w[4];                      // leading parts, remainders
             auto weigh = [&]() {
                 const float now = fmaxf(top, told());
-                // The outputs count in units of a values' scale, at least that of every page so far and
-                // at most 2^6 times this tile's: moved with the maximum, which is rare.
-                if (__any(now - mx > kSlack) || vmost > unit || (vmost > 0.0f && vmost < unit * kLeastUnit)) {
-                    const float to = fmaxf(mx, now), to_unit = vmost > 0.0f ? vmost : unit;
-                    const float alpha = __builtin_amdgcn_exp2f(mx - to);
-                    const float turn = alpha * (unit / to_unit);
+                if (__any(now - mx > kSlack || unit.moves(vmost))) {           // rare
+                    const float to = fmaxf(mx, now), turn = unit.move(vmost, mx - to);
+                    l *= __builtin_amdgcn_exp2f(mx - to);
                     mx = to;
-                    l *= alpha;
-                    unit = to_unit;
 #pragma unroll
                     for (int e = 0; e < kO; ++e) o[e] *= turn;
                 }
-                const float ratio = vown > 0.0f ? vown / unit : 1.0f;          // (no weight where there is no page)
+                const float to_unit = vown > kNone ? vown - unit.at : 0.0f;    // (no weight where there is no page)
                 float shift = mx;
                 if (__any(fabsf(mx) >= kFar)) {
 #pragma clang fp contract(off)   // the products as the maximum was taken of them
@@ -313,7 +310,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     ks = 1.0f;
                     shift = 0.0f;
                 }
-                const float base = kWeightBits + __builtin_amdgcn_logf(ratio) - shift;
+                const float base = kWeightBits + to_unit - shift;
+                const bool far = __any(to_unit < kLeastToUnit);
+                if (far) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e], ks, kWeightBits - shift));
+                }
                 float sum = 0.0f;
                 uint32_t lead[8], rest[8];
 #pragma unroll
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                 }
                 settle(rest);
-                l += sum * (1.0f / ratio);
+                if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     w[e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
@@ -440,11 +442,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 }
                 // (read here, they are there when the weights are: 1 to 2%)
                 uint4 v0 = vb[piece<4>(m, hf)], v1 = vb[piece<4>(m, 2 + hf)];
-                // The scales of the tile's four groups of sixteen keys (with BIG all the same) and, of the
-                // lane's two groups, the keys' scale and what the values' is to the outputs' unit.
-                float ks[2], top[2], vs[4], bits[2], back[2];
+                // The scales (of the values their logarithms) of the tile's four groups of sixteen keys, with
+                // BIG all the same, and, of the lane's two groups, the keys' scale and what the values' is
+                // to the outputs' unit.
+                const float vlog = __builtin_amdgcn_logf(vsl);
+                float ks[2], top[2], vs[4], to_unit[2];
 #pragma unroll
-                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vsl, g) : 0.0f;
+                for (int g = 0; g < (BIG ? 1 : 4); ++g) vs[g] = (ok >> g) & 1 ? lane_value(vlog, g) : kNone;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float a = lane_value(ksl, BIG ? 0 : 2 * u), d = BIG ? a : lane_value(ksl, 2 * u + 1);
@@ -457,30 +461,18 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     top[u] = max3(t, t, acc[u][15]) * ks[u];
                 }
                 const float now = half_max(fmaxf(top[0], top[1]));
-                // The outputs count in units of a values' scale, at least that of every page so far and
-                // at most 2^6 times this tile's: moved with the maximum, which is rare.
                 const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-                if (__any(now - mx > kSlack) || most > unit || (most > 0.0f && most < unit * kLeastUnit)) {
-                    const float to = fmaxf(mx, now), to_unit = most > 0.0f ? most : unit;
-                    const float alpha = __builtin_amdgcn_exp2f(mx - to);
-                    const float turn = alpha * (unit / to_unit);
+                if (__any(now - mx > kSlack || unit.moves(most))) {            // rare
+                    const float to = fmaxf(mx, now), turn = unit.move(most, mx - to);
+                    l *= __builtin_amdgcn_exp2f(mx - to);
                     mx = to;
-                    l *= alpha;
-                    unit = to_unit;
 #pragma unroll
                     for (int e = 0; e < kO; ++e) o[e] *= turn;
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (BIG && u == 1) {
-                        bits[1] = bits[0];
-                        back[1] = back[0];
-                        continue;
-                    }
                     const float v = BIG ? vs[0] : hf ? vs[2 * u + 1] : vs[2 * u];
-                    const float ratio = v > 0.0f ? v / unit : 1.0f;        // (no weight where there is no page)
-                    bits[u] = __builtin_amdgcn_logf(ratio);
-                    back[u] = 1.0f / ratio;
+                    to_unit[u] = v > kNone ? v - unit.at : 0.0f;           // (no weight where there is no page)
                 }
                 float shift = mx;
                 if (__any(fabsf(mx) >= kFar)) {
@@ -496,7 +488,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 half8_t w[2][4];               // leading parts, remainders
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float base = kWeightBits + bits[u] - shift;
+                    const float base = kWeightBits + to_unit[u] - shift;
+                    const bool far = __any(to_unit[u] < kLeastToUnit);
+                    if (far) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], kWeightBits - shift));
+                    }
                     float sum = 0.0f;
                     uint32_t lead[8], rest[8];
 #pragma unroll
@@ -508,7 +505,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                         lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                     }
                     settle(rest);
-                    l += sum * back[u];
+                    if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit[u]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[u][e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
                 }
@@ -558,7 +555,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
             l += told();
         }
         if (!idle && w0 + m <= r1) {
+            // over the sum first: outputs that are no larger than the values are
             const long long at = (long long)(s.row0 + token) * p.q_heads + head;
+            const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f, scale = __builtin_amdgcn_exp2f(unit.at);
+#pragma unroll
+            for (int e = 0; e < kO; ++e) o[e] = o[e] * inv * scale;
             if (chunks > 1) {
                 float *dst = p.part + (at * p.splits + split) * kPart<D> + 32 * kO * side + 4 * hf;
 #pragma unroll
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         *reinterpret_cast<float4_t *>(dst + 32 * e + 8 * u) =
-                            float4_t{o[e][4 * u], o[e][4 * u + 1], o[e][4 * u + 2], o[e][4 * u + 3]} * unit;
+                            float4_t{o[e][4 * u], o[e][4 * u + 1], o[e][4 * u + 2], o[e][4 * u + 3]};
                 if (hf == 0 && side == 0) {
                     dst[D] = mx;
                     dst[D + 1] = l;
@@ -574,15 +575,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 }
             } else {
                 if (p.part != nullptr && hf == 0 && side == 0) p.part[at * p.splits * kPart<D> + D + 2] = 1.0f;
-                const float inv = l > 0.0f || !(l == l) ? unit / l : 0.0f;
                 uint16_t *dst = p.out + at * D + 32 * kO * side + 4 * hf;
 #pragma unroll
                 for (int e = 0; e < kO; ++e)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         uint2 y;
-                        y.x = (uint32_t)from_float<T>(o[e][4 * u] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 1] * inv) << 16);
-                        y.y = (uint32_t)from_float<T>(o[e][4 * u + 2] * inv) | ((uint32_t)from_float<T>(o[e][4 * u + 3] * inv) << 16);
+                        y.x = (uint32_t)from_float<T>(o[e][4 * u]) | ((uint32_t)from_float<T>(o[e][4 * u + 1]) << 16);
+                        y.y = (uint32_t)from_float<T>(o[e][4 * u + 2]) | ((uint32_t)from_float<T>(o[e][4 * u + 3]) << 16);
                         *reinterpret_cast<uint2 *>(dst + 32 * e + 8 * u) = y;
                     }
             }
