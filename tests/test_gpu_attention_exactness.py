@@ -169,3 +169,30 @@ def test_value_scales_from_end_to_end(dim, page, new, pattern):
     page_scales(t, PATTERNS[pattern])
     want, size, reach = kc.attention(t)
     within(run(t), want, fine_tolerance(t, want, size, reach, 448 * float(t.vs[t.table.long()].max())))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 64), (128, 32), (128, 64), (256, 16), (256, 128)])
+@pytest.mark.parametrize("new", [1, 6, 150])
+@pytest.mark.parametrize("far,small,large", [(64, -30, 5), (40, -20, 20), (64, -22, 8), (24, -16, 8)])
+@pytest.mark.parametrize("place", ["in turn", "large first", "large last"])
+def test_weights_and_scales_against_each_other(dtype, dim, page, new, far, small, large, place):
+    """Keys with all the weight to speak of in pages of small values, and keys 2^-far of theirs in
+    pages of large ones, which add less, as much or nothing to the outputs."""
+    t = kc.Batch(93, dtype, [new], [1300], 2, 1, dim, page).fill()
+    q = t.split()[0]
+    q.zero_()
+    q[..., 0] = 8.0
+    t.k.zero_()
+    t.ks.fill_(1.0)
+    for j in range(-(-1300 // page)):
+        id = int(t.table[0, j])
+        big = {"in turn": j % 2, "large first": j * page < 600, "large last": j * page >= 600}[place]
+        t.vs[id] = 2.0 ** (large if big else small)
+        near = torch.randint(0, 8, t.k.shape[1:3], generator=t.g) / 64                # weights of 2^0 to 2^-0.875
+        t.k[id, :, :, 0] = code(-far / 8) if big else (-near).to(kc.F8).view(torch.uint8)
+    want, size, reach = kc.attention(t, scale_of_one())
+    # the largest of weight times scale, as the sums count it
+    most = 448 * max(2.0 ** small, 2.0 ** (large - far))
+    within(run(t, scale=scale_of_one()), want, fine_tolerance(t, want, size, reach, most))

@@ -59,19 +59,23 @@ __device__ __forceinline__ int seq_of_rank(const KvView &c, int rank) {
 }
 
 // The scale that a row's outputs count in, and the largest so far in terms of the running
-// maximum, as logarithms: quotients of scales may leave fp32.  It follows the pages' scales,
-// so that weights are normal halves whatever these are, but not further down than 2^60 from the
-// largest: outputs, below 2^45 of their unit, stay far from fp32's end.  (A page of zeros has
-// 2^-64, and values of bf16 reach 2^127.)
+// maximum, as logarithms: quotients of scales may leave fp32.  A weight times its page's scale
+// is what it adds to an output, so the largest such product (need) says how high the unit has
+// to be, which a page of large values and no weight to speak of does not.  Down it goes where
+// the maximum rises to a key of smaller values, whose product is then what counts, and with the
+// pages' scales (most), so that weights are normal halves whatever these are; but not further
+// than 2^60 from the largest: outputs, below 2^45 of their unit, stay far from fp32's end.  (A
+// page of zeros has 2^-64, and values of bf16 reach 2^127.)
 struct OutUnit {
     static constexpr float kDrop = 6.0f, kMostFall = 60.0f;
     float at = kNone, peak = kNone;
-    // whether a tile whose largest scale is 2^most calls for another
-    __device__ __forceinline__ bool moves(float most) const { return most > at || (most < at - kDrop && most > kNone); }
+    // whether a tile of the largest product 2^need and the largest scale 2^most calls for another
+    __device__ __forceinline__ bool moves(float need, float most) const { return need > at || (most < at - kDrop && most > kNone); }
     // goes along where the maximum rises by -down; returns what the outputs are to be multiplied by
-    __device__ __forceinline__ float move(float most, float down) {
+    __device__ __forceinline__ float move(float need, float most, float down) {
         peak = fmaxf(peak, at) + down;
-        const float next = fmaxf(moves(most) ? most : at, peak - kMostFall);
+        const bool by_need = need > at || (down < 0.0f && need < at - kDrop);
+        const float next = fmaxf(by_need ? fminf(most, need + kDrop) : moves(need, most) ? most : at, peak - kMostFall);
         const float turn = __builtin_amdgcn_exp2f(down + (at - next));
         at = next;
         return turn;

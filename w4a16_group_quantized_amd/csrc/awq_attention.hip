@@ -289,14 +289,16 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
             float top = max3(x[0], x[1], x[2]);
 #pragma unroll
             for (int e = 3; e < 15; e += 2) top = max3(top, x[e], x[e + 1]);
-            top = group_max(max3(top, top, x[15]));
+            const float own = max3(top, top, x[15]);
+            top = group_max(own);
             // What a page's scale is to the outputs' unit goes into the exponent.
             const float lv = __builtin_amdgcn_logf(vs);               // (no page: -inf)
             const float most = BIG ? lv : group_max(lv);
             const float now = fmaxf(mx, top);
-            if (__any(now != mx || unit.moves(most))) {
+            const float need = BIG ? lv + (top - now) : group_max(lv + (own - now));
+            if (__any(now != mx || unit.moves(need, most))) {
                 l *= __builtin_amdgcn_exp2f(mx - now);
-                const float turn = unit.move(most, mx - now);
+                const float turn = unit.move(need, most, mx - now);
 #pragma unroll
                 for (int t = 0; t < kT; ++t) o[t] *= turn;
                 mx = now;

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         if constexpr (kPairs) {
             // the scores of a tile: the wave's 32 keys
             float16_t acc;
-            float ks = 1.0f, vmost = kNone, vown = kNone, top = 0.0f;
+            float ks = 1.0f, vmost = kNone, vown = kNone, vother = kNone, top = 0.0f;   // (of the values' scales, logarithms)
             auto scores = [&](int j0, const uint4 *kb, float ksl, float vsl, uint64_t ok) {
                 acc = float16_t{};
                 uint4 k0 = kb[piece<kC>(32 * side + m, hf)];
@@ -284,18 +284,20 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                 ks = fminf(fmaxf((hf ? k_hi : k_lo) * down, 0x1p-126f), 0x1p126f);
                 vmost = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
                 vown = BIG ? vs[0] : side ? (hf ? vs[3] : vs[2]) : (hf ? vs[1] : vs[0]);
+                vother = BIG ? vs[0] : side ? (hf ? vs[1] : vs[0]) : (hf ? vs[3] : vs[2]);
                 float a = max3(acc[0], acc[1], acc[2]);
 #pragma unroll
                 for (int e = 3; e < 15; e += 2) a = max3(a, acc[e], acc[e + 1]);
-                top = half_max(max3(a, a, acc[15]) * ks);
-                tell(top);
+                top = max3(a, a, acc[15]) * ks;
+                tell(top);                     // of sixteen keys
             };
             // the weights, of the maximum of both waves
             half8_t w[4];                      // leading parts, remainders
             auto weigh = [&]() {
-                const float now = fmaxf(top, told());
-                if (__any(now - mx > kSlack || unit.moves(vmost))) {           // rare
-                    const float to = fmaxf(mx, now), turn = unit.move(vmost, mx - to);
+                const float other = told(), now = half_max(fmaxf(top, other)), to = fmaxf(mx, now);
+                const float need = BIG ? vmost + (now - to) : half_max(fmaxf(vown + (top - to), vother + (other - to)));
+                if (__any(now - mx > kSlack || unit.moves(need, vmost))) {     // rare
+                    const float turn = unit.move(need, vmost, mx - to);
                     l *= __builtin_amdgcn_exp2f(mx - to);
                     mx = to;
 #pragma unroll
@@ -460,10 +462,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     for (int e = 3; e < 15; e += 2) t = max3(t, acc[u][e], acc[u][e + 1]);
                     top[u] = max3(t, t, acc[u][15]) * ks[u];
                 }
-                const float now = half_max(fmaxf(top[0], top[1]));
+                const float now = half_max(fmaxf(top[0], top[1])), to = fmaxf(mx, now);
                 const float most = BIG ? vs[0] : fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-                if (__any(now - mx > kSlack || unit.moves(most))) {            // rare
-                    const float to = fmaxf(mx, now), turn = unit.move(most, mx - to);
+                const float need = BIG ? most + (now - to)
+                                       : half_max(fmaxf((hf ? vs[1] : vs[0]) + (top[0] - to), (hf ? vs[3] : vs[2]) + (top[1] - to)));
+                if (__any(now - mx > kSlack || unit.moves(need, most))) {      // rare
+                    const float turn = unit.move(need, most, mx - to);
                     l *= __builtin_amdgcn_exp2f(mx - to);
                     mx = to;
 #pragma unroll
