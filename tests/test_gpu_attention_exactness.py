@@ -196,3 +196,22 @@ def test_weights_and_scales_against_each_other(dtype, dim, page, new, far, small
     # the largest of weight times scale, as the sums count it
     most = 448 * max(2.0 ** small, 2.0 ** (large - far))
     within(run(t, scale=scale_of_one()), want, fine_tolerance(t, want, size, reach, most))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,page,heads", [(64, 16, (16, 4)), (128, 64, (32, 8)), (256, 128, (8, 4))])
+def test_long_single_tokens_beside_a_prompt(dim, page, heads):
+    """A prompt that is not cut, and single tokens over keys that are."""
+    t = one_hot(kc.Batch(94, "fp16", [2100, 1, 3, 1], [2100, 9000, 5003, 70], *heads, dim, page, extra_rows=2)).fill()
+    t.ks.fill_(2.0 ** -7)
+    cache, batch, q, _, _ = t.device()
+    room = binding.attention_workspace_bytes(q.shape[0], heads[0], cache, batch)
+    assert room > 0
+    have = binding.attention(q, cache, batch, workspace=torch.full((room,), 0xFF, dtype=torch.uint8, device="cuda:0"))
+    torch.cuda.synchronize()
+    # (the definition of the prompt's last rows only: it is dear)
+    cut, t.new, t.lens, t.table = 2080, [20, 1, 3, 1], t.lens, t.table
+    t.x, t.starts = t.x[cut:], [0, 20, 21, 24, 25]
+    want, size, reach = kc.attention(t)
+    n = t.starts[-1]
+    within(have.cpu()[cut: cut + n].double(), want[:n], fine_tolerance(t, want, size, reach, 448 * float(t.vs.max()))[:n])

@@ -156,3 +156,16 @@ def test_binding_batch(kw, error, what):
              q_starts=torch.zeros(3, dtype=torch.int32), max_q=1, max_kv=1) | kw
     with pytest.raises(error, match=what):
         binding.KvBatch(**a)
+
+
+def test_long_single_tokens_beside_a_prompt_are_cut():
+    """The prompt's row tiles fill the GPU, so the prompt kernel cuts nothing; the kernel of the
+    two single tokens, which may be long, cuts by its own count, within 256 MiB of room."""
+    lib, c = binding.load(), cache(heads=8)
+    need = lambda rows, kv: lib.awq_attention_workspace_bytes(  # noqa: E731
+        32, 0, 0, c, batch(seqs=3, width=4096, rows=rows + 2, max_q=rows, max_kv=kv))
+    one = lambda rows: (rows + 2) * 32 * (128 + 4) * 4  # noqa: E731
+    assert need(2048, 131000) == 7 * one(2048) <= 1 << 28
+    assert need(4096, 131000) == 3 * one(4096)
+    assert need(16384, 131000) == 0                  # no room for two chunks
+    assert need(2048, 500) == 0                      # too short to cut

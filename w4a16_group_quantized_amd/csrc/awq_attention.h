@@ -24,7 +24,8 @@ struct AttnArgs {
     int q_heads, group;
     float scale;             // scale * log2(e)
     int window, sinks;
-    int splits, target;      // most chunks of a row tile; workgroups that all chunks are dealt to
+    int most, target;        // most chunks of a row tile in this kernel; workgroups that all chunks are dealt to
+    int splits;              // chunks that a row has room for in the workspace
     int few;                 // rows (times query heads of a kv head) of a sequence from which the prompt kernel takes it
 };
 

@@ -56,6 +56,7 @@ constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of th
 // among short ones would be the last by far.
 constexpr int kUncutTiles = 12, kManyGroups = 192, kLongTiles = 256, kLeastChunk = 4, kMaxSplits = 256;
 constexpr int kJoinGroups = 8192;          // workgroups that join chunks
+constexpr size_t kMixedRoom = 1u << 28;    // bytes of partial results for single tokens among prompts
 
 // Chunks for a tile: from the tiles that all sequences' rows see, for all kv heads.
 // The host knows no lengths, so each wave adds them up, with more than 64 sequences four
@@ -117,18 +118,18 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
     const int unit_id = slot / (row_tiles * c.kv_heads) * kXcds + blockIdx.x % kXcds;
     const int split = unit_id / c.seqs, b = unit_id % c.seqs;
     const int h = slot / row_tiles % c.kv_heads;
-    if (split >= p.splits) return;
+    if (split >= p.most) return;
     const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
     const int total = s.n * p.group;
     if (total >= p.few) return;                // the prompt kernel's
     float per_tile = 0.0f;
-    if (p.part != nullptr) {
+    if (p.most > 1) {
         // With many sequences only those who may be cut ask: 1024 of 300 tokens in a call that may
         // have 64k, 760 -> 180 us (138 uncut).  With few, asking at once saves a load's time (0.6 us).
         bool ask = c.seqs < 64;
         if (!ask) {
-            const int most = min(p.splits, visible_tiles(p, s.first(), s.len - 1, s.len).count() / kLeastChunk);
+            const int most = min(p.most, visible_tiles(p, s.first(), s.len - 1, s.len).count() / kLeastChunk);
             if (split >= max(1, most)) return;
             ask = most > 1;
         }
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
         const int count = tiles.count();
         // its share of the chunks, rounded down: one more than one for each CU would share a CU
         const int chunks = __builtin_amdgcn_readfirstlane(
-            max(1, min(min(p.splits, count / kLeastChunk), (int)((float)count * per_tile * 1.0001f))));
+            max(1, min(min(p.most, count / kLeastChunk), (int)((float)count * per_tile * 1.0001f))));
         if (split >= chunks) continue;
         // Chunks begin at, and waves take, tiles by their number in the sequence modulo the waves:
         // with pages of 128 and more two tiles share each 128-byte line of the values, which two
@@ -473,12 +474,13 @@ int prompt_rows(long long all_tiles) {
 // workgroups that they are dealt to.
 // Where most sequences have far fewer rows than the longest, each kernel takes those that
 // suit it (one sequence of 2048 rows, 63 of one, all over 4k keys: 810 us with the prompt
-// kernel alone, 235 with both; 255 of one: 1854 and 476).
+// kernel alone, 235 with both; 255 of one: 1854 and 476), and cuts them by a number of its own.
 struct Plan {
     bool prompt, mixed;      // whether the prompt kernel is needed, and both are
     bool wide;               // eight waves to a workgroup
-    int few, prompt_tiles;
+    int few, prompt_tiles, prompt_splits;
     int row_tiles, splits, target;
+    int room() const { return std::max(splits, prompt_splits); }
 };
 Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks) {
     Plan pl;
@@ -489,10 +491,11 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
+    pl.splits = pl.prompt_splits = 1;
     pl.wide = false;
     if (pl.prompt) {
         pl.prompt_tiles = prefill_row_tiles(seqs, rows, kv_heads, group, head_dim, max_q, pl.few, pl.mixed);
-        pl.splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
+        pl.prompt_splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
         if (!pl.mixed) return pl;
     }
     // (the kernel steps on where the grid is cut)
@@ -502,19 +505,22 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
                                             std::max(1, ((1 << 24) - 1) / (units * kv_heads)));
     const long long groups = (long long)seqs * kv_heads * pl.row_tiles;
     pl.target = groups <= 64 ? 256 : 512;
-    if (!pl.mixed) {
-        // lengths may differ by much; but a workgroup that has no chunk takes its launch
-        // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
-        // 1126 at eight, 692 at two)
-        long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
-        // Heads of 64 (8 kv heads; us, four waves and joined or not / eight waves and not cut):
-        // 1, 16, 32, 48 sequences of 500 to 1000: 9.2 / 7.9, 12.6 / 8.5, 9.3 / 9.2, 12.0 / 12.6; of 1k to
-        // 2k 9.4 / 10.9, 14.1 / 11.6, 13.9 / 13.2, 18.9 / 19.6; of 3k to 6k 10.8 / 22.4, 24.2 / 24.8,
-        // 31.5 / 30.6, 44.4 / 46.0; of 250 to 500 6.3 / 6.5 at four.  With heads of 128 a CU has room for
-        // eight waves, whose workgroup is no faster (1 of 1000: 12.1 / 12.3).
-        pl.wide = head_dim == 64 && groups <= 256 && tiles > kUncutTiles && tiles <= std::max(24ll, groups / 2);
-        if (tiles <= kUncutTiles || pl.wide || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
-        pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
+    // lengths may differ by much; but a workgroup that has no chunk takes its launch
+    // (8 kv heads of 1024 sequences of 300 tokens: 274 us at eight chunks, 209 at four; of 4096,
+    // 1126 at eight, 692 at two)
+    long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
+    // Heads of 64 (8 kv heads; us, four waves and joined or not / eight waves and not cut):
+    // 1, 16, 32, 48 sequences of 500 to 1000: 9.2 / 7.9, 12.6 / 8.5, 9.3 / 9.2, 12.0 / 12.6; of 1k to
+    // 2k 9.4 / 10.9, 14.1 / 11.6, 13.9 / 13.2, 18.9 / 19.6; of 3k to 6k 10.8 / 22.4, 24.2 / 24.8,
+    // 31.5 / 30.6, 44.4 / 46.0; of 250 to 500 6.3 / 6.5 at four.  With heads of 128 a CU has room for
+    // eight waves, whose workgroup is no faster (1 of 1000: 12.1 / 12.3).
+    pl.wide = !pl.mixed && head_dim == 64 && groups <= 256 && tiles > kUncutTiles && tiles <= std::max(24ll, groups / 2);
+    if (tiles <= kUncutTiles || pl.wide || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;
+    pl.splits = (int)std::max<long long>(1, std::min<long long>({want, (tiles + kLeastChunk - 1) / kLeastChunk, kMaxSplits}));
+    // Partial results have room by rows, the prompts' among them.
+    if (pl.mixed) {
+        const size_t each = (size_t)rows * kv_heads * group * (head_dim + 4) * sizeof(float);
+        pl.splits = (int)std::max<long long>(1, std::min<long long>(pl.splits, (long long)(kMixedRoom / each)));
     }
     // (a launch has less than 2^32 threads)
     const long long once = (long long)(units + kXcds) * pl.splits * kv_heads;
@@ -538,11 +544,13 @@ hipError_t launch(AttnArgs p, const Plan &pl, bool bf16, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (pl.prompt) {
         p.few = pl.mixed ? pl.few : 0;
+        p.most = pl.prompt_splits;
         e = launch_attention_prefill(p, D, bf16, pl.prompt_tiles, pl.mixed, s);
         if (e != hipSuccess) return e;
     }
     if (!pl.prompt || pl.mixed) {
         p.few = pl.mixed ? pl.few : 0x7FFFFFFF;
+        p.most = pl.splits;
         const int units = (p.c.seqs * pl.splits + kXcds - 1) / kXcds * kXcds;
         const int grid = units * p.c.kv_heads * pl.row_tiles;
         if constexpr (D == 64) {
@@ -575,16 +583,16 @@ hipError_t launch_dim(const AttnArgs &p, int D, const Plan &pl, bool bf16, hipSt
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
                            int max_kv, int window, int sinks) {
     const Plan pl = plan(seqs, rows, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks);
-    if (pl.splits == 1) return 0;
-    return (size_t)rows * q_heads * pl.splits * (head_dim + 4) * sizeof(float);
+    if (pl.room() == 1) return 0;
+    return (size_t)rows * q_heads * pl.room() * (head_dim + 4) * sizeof(float);
 }
 
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
                             int max_q, int max_kv, void *workspace, hipStream_t s) {
     const Plan pl = plan(c.seqs, c.rows, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
-    AttnArgs p{c, q, q_stride, out, pl.splits > 1 ? (float *)workspace : nullptr, q_heads,
-               q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, pl.splits, pl.target, 0};
+    AttnArgs p{c, q, q_stride, out, pl.room() > 1 ? (float *)workspace : nullptr, q_heads,
+               q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, 1, pl.target, pl.room(), 0};
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, pl, bf16, s) : launch_dim<half_t>(p, head_dim, pl, bf16, s);
 }
 

@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     const int m = lane & 31, hf = lane >> 5;
     // with pairs: which 32 keys of a tile, and which half of the outputs, are the wave's
     const int side = kPairs ? wave & 1 : 0, row_wave = kPairs ? wave >> 1 : wave;
-    const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.splits;
-    const int slot = blockIdx.x / (c.kv_heads * p.splits);
+    const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.most;
+    const int slot = blockIdx.x / (c.kv_heads * p.most);
     int b, tile, tile_step = tiles_per_seq;
     if (tiles_per_seq > 0) {
         b = seq_of_rank(c, slot / tiles_per_seq);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
         // this workgroup's chunk of them
-        const int every = tiles.count(), chunks = max(1, min(p.splits, every / kLeastChunk));
+        const int every = tiles.count(), chunks = max(1, min(p.most, every / kLeastChunk));
         if (split >= chunks) continue;
         const int start = (int)((long long)every * split / chunks);
         const int count = (int)((long long)every * (split + 1) / chunks) - start;
@@ -637,7 +637,7 @@ hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, 
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
     // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
-    const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.splits;
+    const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.most;
     if (grid == 0) return hipSuccess;
     return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, flat ? 0 : row_tiles, s)
                 : launch_dim<half_t>(p, head_dim, grid, flat ? 0 : row_tiles, s);
