@@ -459,15 +459,38 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
     }
 }
 
-// Rows of a sequence and kv head from which the prompt kernel takes a call, by the
-// tiles of keys of all sequences and kv heads.  The split kernel reads keys and values
-// again for every sixteen rows, the prompt kernel is slower to start.  Measured (us,
-// split / prompt, 4 query heads to each of 8 kv heads of 128 elements, 20, 32, 64, 96, 128
-// rows): 1 sequence of 500 keys 8 / 16, 9 / 16, 10 / 19, 13 / 20, 13 / 21; of 4000 14 / 19,
-// 14 / 20, 16 / 21, 23 / 23, 27 / 23; of 16k 20 / 22, 20 / 22, 26 / 25, 53 / 27, 63 / 29;
-// 16 of 4000: 34 / 37, 34 / 38, 53 / 48, 81 / 56, 95 / 62; of 16k 121 / 101, 117 / 102, 180 / 111.
-int prompt_rows(long long all_tiles) {
-    return all_tiles >= 16384 ? kRows + 1 : all_tiles >= 2048 ? 64 : all_tiles >= 512 ? 96 : 128;
+// Rows of a sequence and kv head from which the prompt kernel takes a call, by the pairs of
+// sequence and kv head, the tiles of keys of each, and the width of heads.  The split kernel
+// reads keys and values again for every sixteen rows; the prompt kernel is slower to start, and
+// cuts a row tile into 32 chunks at most, so with few pairs most of the GPU has nothing to do.
+// Measured (us, split / prompt, by rows times query heads to a kv head):
+//   heads of 128                  20        32        64        96       128       256
+//   8 pairs, 500 keys          14/21     14/22     14/23     14/24     14/24     22/25
+//   8, 4000                    20/25     20/25     19/27     26/28     29/29     51/32
+//   8, 16k                     22/27     23/27     29/30     55/33     66/34    114/48
+//   8, 131k                   79/123    78/125   130/133   366/136   453/141  1124/224
+//   128, 500                   13/23     13/23     14/25     19/26     23/26     37/28
+//   128, 4000                  37/46     37/49     62/65     88/74    110/83   195/141
+//   128, 16k                 130/134   129/135   238/187   349/209   436/235   817/421
+//   32, 4000                   22/27     22/28     30/36     31/39     32/41     55/54
+//   16, 131k                  93/141   154/139   308/191   407/211   599/248   912/444
+//   2, 131k                   24/122    30/123    41/129    92/130    64/130   108/133
+//   1, 131k                   21/121    23/122    28/128    52/129    39/132    61/131
+//   heads of 256: 8, 4000      21/26     22/27     28/31     47/32     58/34    108/43
+//   8, 16k                     35/30     37/30     52/36    108/43    134/49    253/71
+//   128, 500                   17/25     17/25     30/28     42/29     54/30    105/39
+//   32, 16k                    92/54     89/56    156/78   236/101   240/111   422/199
+//   2, 131k                   39/124    54/125    81/133   189/133   134/136   238/144
+//   heads of 64: 8, 16k        18/23     19/23     22/25     33/27     40/28     61/38
+//   8, 131k                    46/94     48/94    77/100   153/103   186/105   455/152
+//   128, 4000                  20/37     21/40     30/52     39/59     48/65    84/110
+//   128, 16k                  63/99    64/102    93/136   135/145   171/155   314/286
+int prompt_rows(long long pairs, long long tiles, int head_dim) {
+    const long long all = pairs * tiles;
+    const int at = all >= 16384 ? 0 : all >= 2048 ? 1 : all >= 512 ? 2 : 3;
+    static const int rows[3][4] = {{80, 112, 160, 224}, {48, 72, 112, 224}, {kRows + 1, 32, 64, 96}};
+    const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
+    return (int)std::max<long long>(rows[width][at], (width == 2 ? 256 : 640) / pairs);
 }
 
 // The grid of a call: the most chunks, whose number is found on the device, and the
@@ -487,7 +510,7 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
     const long long tiles = (keys + kTile - 1) / kTile;
-    pl.few = prompt_rows((long long)seqs * kv_heads * tiles);
+    pl.few = prompt_rows((long long)seqs * kv_heads, tiles, head_dim);
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
