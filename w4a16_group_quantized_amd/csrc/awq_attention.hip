@@ -312,10 +312,11 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
                 shift = 0.0f;
             }
             const float base = kWeightBits + to_unit - shift;
-            const bool far = __any(to_unit < kLeastToUnit);
-            if (far) {
+            float back = __builtin_amdgcn_exp2f(-to_unit);
+            if (__any(to_unit < kLeastToUnit)) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(x[e] + (kWeightBits - shift));
+                back = 0.0f;
             }
             float sum = 0.0f;
             uint32_t lead[8], rest[8];
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
             }
             settle(rest);
             const half8_t ph[2] = {halves8(lead), halves8(lead + 4)}, pl[2] = {halves8(rest), halves8(rest + 4)};
-            if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit);
+            l += sum * back;
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
                 const half8_t v0 = e4m3x8_to_half(vc[t].x, vc[t].y), v1 = e4m3x8_to_half(vc[t].z, vc[t].w);

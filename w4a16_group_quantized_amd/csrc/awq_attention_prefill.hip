@@ -313,10 +313,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     shift = 0.0f;
                 }
                 const float base = kWeightBits + to_unit - shift;
-                const bool far = __any(to_unit < kLeastToUnit);
-                if (far) {
+                float back = __builtin_amdgcn_exp2f(-to_unit);
+                if (__any(to_unit < kLeastToUnit)) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e], ks, kWeightBits - shift));
+                    back = 0.0f;
                 }
                 float sum = 0.0f;
                 uint32_t lead[8], rest[8];
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                 }
                 settle(rest);
-                if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit);
+                l += sum * back;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     w[e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
@@ -489,15 +490,19 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     }
                     shift = 0.0f;
                 }
+                float back[2] = {__builtin_amdgcn_exp2f(-to_unit[0]), __builtin_amdgcn_exp2f(-to_unit[1])};
+                if (__any(fminf(to_unit[0], to_unit[1]) < kLeastToUnit)) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], kWeightBits - shift));
+                        back[u] = 0.0f;
+                    }
+                }
                 half8_t w[2][4];               // leading parts, remainders
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float base = kWeightBits + to_unit[u] - shift;
-                    const bool far = __any(to_unit[u] < kLeastToUnit);
-                    if (far) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], kWeightBits - shift));
-                    }
                     float sum = 0.0f;
                     uint32_t lead[8], rest[8];
 #pragma unroll
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                         lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                     }
                     settle(rest);
-                    if (!far) l += sum * __builtin_amdgcn_exp2f(-to_unit[u]);
+                    l += sum * back[u];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[u][e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
                 }
