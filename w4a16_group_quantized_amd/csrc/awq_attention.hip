@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
 //   128, 16k                  63/99    64/102    93/136   135/145   171/155   314/286
 int prompt_rows(long long pairs, long long tiles, int head_dim) {
     const long long all = pairs * tiles;
-    const int at = all >= 16384 ? 0 : all >= 2048 ? 1 : all >= 512 ? 2 : 3;
-    static const int rows[3][4] = {{80, 112, 160, 224}, {48, 72, 112, 224}, {kRows + 1, 32, 64, 96}};
+    const int at = all >= 12288 ? 0 : all >= 1536 ? 1 : all >= 384 ? 2 : 3;
+    static const int rows[3][4] = {{80, 96, 160, 288}, {48, 72, 112, 288}, {kRows + 1, 32, 64, 160}};
     const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
     return (int)std::max<long long>(rows[width][at], (width == 2 ? 256 : 640) / pairs);
 }
