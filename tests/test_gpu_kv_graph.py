@@ -243,3 +243,31 @@ def test_append_then_attend(dim, page, new):
     t.x[:, : 4 * dim] = turned.flatten(1).cpu()
     want, size, reach = kc.attention(t)
     assert bool(((got - want).abs() <= kc.attention_tolerance(t, want, size, reach)).all())
+
+
+def test_tensors_that_get_other_memory():
+    """A cache's or a batch's tensor whose storage is exchanged after construction: the calls
+    follow it, and what no longer fits is refused.  (The old memory stays alive throughout.)"""
+    t = kc.Batch(72, "fp16", [1, 3], [150, 40], 4, 2, 64, 16).fill()
+    cache, batch, q, k, v = t.device()
+    old = [x.clone() for x in (cache.k, cache.k_scales, batch.kv_lens, batch.page_table)]
+    keep = [x.detach() for x in (cache.k, cache.k_scales, batch.kv_lens, batch.page_table)]
+    shorter = torch.tensor([100, 30], dtype=torch.int32, device=DEV)
+    want = binding.attention(q, cache, binding.KvBatch(batch.page_table, shorter, batch.q_starts, batch.max_q, batch.max_kv))
+    batch.kv_lens.set_(shorter.clone())
+    assert torch.equal(binding.attention(q, cache, batch), want)
+    cache.k_scales.set_(old[1] * 4)
+    again = binding.KvCache(cache.k, cache.v, old[1] * 4, cache.v_scales)
+    assert torch.equal(binding.attention(q, cache, batch), binding.attention(q, again, batch))
+    fresh = torch.zeros_like(old[0].view(torch.uint8)).view(kc.F8)
+    cache.k.set_(fresh)
+    turned = binding.kv_append(q, k, v, cache, batch)
+    assert bool(fresh.view(torch.uint8).any()) and torch.equal(turned, q)
+    assert torch.equal(keep[0].view(torch.uint8), old[0].view(torch.uint8))
+    cache.k.set_(fresh[:2].clone())
+    with pytest.raises(ValueError, match="v must be"):
+        binding.attention(q, cache, batch)
+    cache.k.set_(fresh)
+    batch.page_table.set_(old[3].t().contiguous())
+    with pytest.raises(ValueError, match="kv_lens must be"):
+        binding.attention(q, cache, batch)

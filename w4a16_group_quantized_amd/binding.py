@@ -489,7 +489,8 @@ def _kv_check(t, dtype, shape, name):
 class KvCache:
     """A paged cache of keys and values held in e4m3 codes, with one fp32 scale for
     each page and kv head (see ``awq_kv_cache`` in include/awq.h).  Shapes and
-    devices are checked here, once; the calls take the view made here."""
+    devices are checked here, once, and again where a tensor has got other memory
+    since (``set_``, ``resize_``, ``.data``); the calls take the view made here."""
 
     k: torch.Tensor          # float8_e4m3fn [pages][kv_heads][page_size][head_dim]
     v: torch.Tensor          # float8_e4m3fn [pages][kv_heads][head_dim][page_size]
@@ -509,8 +510,15 @@ class KvCache:
                 raise ValueError(f"{name} is on {getattr(self, name).device}, k on {self.k.device}")
         ptr = [_dev(getattr(self, n), getattr(self, n).dtype, n) for n in ("k", "v", "k_scales", "v_scales")]
         for name, value in (("_c", CKvCache(*ptr, pages, page, heads, dim)), ("_heads", heads), ("_dim", dim),
-                            ("_device", self.k.device)):
+                            ("_device", self.k.device), ("_at", tuple(ptr)),
+                            ("_ask", tuple(t.data_ptr for t in (self.k, self.v, self.k_scales, self.v_scales)))):
             object.__setattr__(self, name, value)
+
+    def _view(self) -> CKvCache:
+        a, b, c, d = self._ask
+        if (a(), b(), c(), d()) != self._at:
+            self.__post_init__()
+        return self._c
 
     @property
     def kv_heads(self) -> int:
@@ -538,7 +546,8 @@ class KvBatch:
     """The sequences of a call (see ``awq_kv_batch`` in include/awq.h): device int32
     arrays, whose contents may change from call to call (and from replay to replay
     of a captured graph).  ``max_q`` and ``max_kv``, the most rows and tokens of a
-    sequence, size the grids: smaller than the truth costs time, not correctness."""
+    sequence, size the grids: smaller than the truth costs time, not correctness.
+    Checked here, once, and again where a tensor has got other memory since."""
 
     page_table: torch.Tensor   # int32 [seqs][table_width]
     kv_lens: torch.Tensor      # int32 [seqs]: tokens with this call's rows
@@ -561,11 +570,16 @@ class KvBatch:
             if not 0 <= getattr(self, name) < 1 << 31:
                 raise ValueError(f"{name} must be in [0, 2^31), got {getattr(self, name)}")
         ptr = [_dev(getattr(self, n), torch.int32, n) for n in ("page_table", "kv_lens", "q_starts")]
-        object.__setattr__(self, "_args", (*ptr, seqs, width))
+        object.__setattr__(self, "_at", tuple(ptr))
+        object.__setattr__(self, "_ask", (self.page_table.data_ptr, self.kv_lens.data_ptr, self.q_starts.data_ptr))
+        object.__setattr__(self, "_size", (seqs, width))
         object.__setattr__(self, "_device", self.page_table.device)
 
     def _c(self, rows: int) -> CKvBatch:
-        return CKvBatch(*self._args, rows, self.max_q, self.max_kv)
+        a, b, c = self._ask
+        if (a(), b(), c()) != self._at:
+            self.__post_init__()
+        return CKvBatch(*self._at, *self._size, rows, self.max_q, self.max_kv)
 
 
 def _rows(t: torch.Tensor, rows: int, heads: int, dtype: torch.dtype, cache: KvCache, name: str):
@@ -633,6 +647,7 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
     values into the cache.  q [rows][q_heads][head_dim] (or None), k and v
     [rows][kv_heads][head_dim], fp16 or bf16, rows at any stride; rope fp32
     [positions][rot_dim] (cosines, then sines) or None.  Returns the rotated q."""
+    c, b = cache._view(), batch._c(k.shape[0])
     kind = _kv_type(k, batch, cache, "k")
     rows, heads = k.shape[0], cache._heads
     kp, ks = _rows(k, rows, heads, k.dtype, cache, "k")
@@ -651,13 +666,13 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
         rp = _dev(rope, torch.float32, "rope")
         positions, rot = rope.shape
     _kv_call(cache._device, stream, load().awq_kv_append, qp, qs, kp, ks, vp, vs, op, heads, kind, rp, positions,
-             rot, int(interleaved), cache._c, batch._c(rows))
+             rot, int(interleaved), c, b)
     return out
 
 
 def attention_workspace_bytes(rows: int, q_heads: int, cache: KvCache, batch: KvBatch, window: int = 0,
                               sinks: int = 0) -> int:
-    return load().awq_attention_workspace_bytes(q_heads, window, sinks, cache._c, batch._c(rows))
+    return load().awq_attention_workspace_bytes(q_heads, window, sinks, cache._view(), batch._c(rows))
 
 
 def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | None = None,
@@ -667,6 +682,7 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
     their own keys and values already: causal, and with ``window`` > 0 only over the
     last ``window`` tokens and the first ``sinks``.  scale: 1 / sqrt(head_dim) unless
     given.  The workspace is allocated here unless one is given."""
+    c, b = cache._view(), batch._c(q.shape[0])
     kind = _kv_type(q, batch, cache, "q")
     rows, heads = q.shape[0], _heads(q, cache)
     qp, qs = _rows(q, rows, heads, q.dtype, cache, "q")
@@ -674,7 +690,7 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
         raise ValueError(f"window and sinks must be in [0, 2^31), got {window}, {sinks}")
     out = _kv_out(out, q, stream)
     op = _dev(out, q.dtype, "out")
-    lib, c, b = load(), cache._c, batch._c(rows)
+    lib = load()
     if workspace is None:
         nbytes = lib.awq_attention_workspace_bytes(heads, window, sinks, c, b)
         if nbytes:
