@@ -409,7 +409,8 @@ typedef struct awq_kv_batch {
  *   q [rows][q_heads][head_dim], k and v [rows][kv_heads][head_dim] of `type`,
  *   with q_stride, k_stride, v_stride elements from row to row (slices of a
  *   fused projection's output will do): at least heads * head_dim, a multiple of
- *   8.  q_out: dense [rows][q_heads][head_dim].  q and q_out may both be NULL.
+ *   8.  q_out: dense [rows][q_heads][head_dim]; q itself if that is dense too, no
+ *   other overlap.  q and q_out may both be NULL.
  *   rope: fp32 [rope_positions][rot_dim], per position rot_dim / 2 cosines, then
  *   as many sines; rot_dim 0 rotates nothing (rope may be NULL), else a multiple
  *   of 16 up to head_dim: the first rot_dim elements of a head are rotated, in
@@ -421,7 +422,9 @@ typedef struct awq_kv_batch {
  * scale becomes 2^e if the call's first token there is in slot 0, and otherwise
  * the larger of 2^e and the scale it has; codes of tokens that are there already
  * are then moved to the new scale, code = e4m3_rne(code * old / new).  New codes
- * are e4m3_rne(x / scale), to nearest, ties to even.
+ * are e4m3_rne(x / scale), to nearest, ties to even.  (Powers of two make the
+ * quotients exact; under a scale that is none, left in the cache by others, they
+ * are rounded to fp32 first.)
  * A token whose key or value of a head holds a NaN or an infinity gets NaN key
  * codes there, and zero for the value's non-finite elements: rows that see it
  * come out NaN, others are not touched by it.
@@ -445,7 +448,7 @@ awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k,
  * no window (sinks then say nothing).  A row that sees no key gets zeros.
  * Products, maxima, sums and outputs are held in fp32, weights as two halves
  * (22 bits) in the second product; out is rounded once.
- *   q [rows][q_heads][head_dim] with q_stride as above; out dense.
+ *   q [rows][q_heads][head_dim] with q_stride as above; out dense, apart from q.
  *   scale: finite (1 / sqrt(head_dim) by custom).
  *   workspace: device scratch of at least awq_attention_workspace_bytes for the
  *   same arguments, 16-byte aligned, owned by the caller, contents unspecified

@@ -197,3 +197,19 @@ def test_prompts_among_single_tokens(dtype, dim, page, rope):
     binding.kv_append(None, k, v, alone, batch)
     assert torch.equal(cache.k.view(torch.uint8), alone.k.view(torch.uint8))
     assert torch.equal(cache.v.view(torch.uint8), alone.v.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype,dim,page", [("fp16", 128, 64), ("bf16", 64, 16), ("fp16", 256, 32)])
+@pytest.mark.parametrize("rot,interleaved", [(None, False), (48, False), (64, True)])
+def test_queries_rotated_in_place(dtype, dim, page, rot, interleaved):
+    """q_out the dense q itself: the same bits as apart from it."""
+    new, lens = [150, 1, 3], [170, 33, 3]
+    t = kc.Batch(33, dtype, new, lens, 6, 2, dim, page).fill([n - m for n, m in zip(lens, new)])
+    rope = None if rot is None else kc.rope_table(180, rot).to("cuda:0")
+    cache, batch, q, k, v = t.device()
+    want = binding.kv_append(q, k, v, cache, batch, rope=rope, interleaved=interleaved)
+    for max_q in (150, 1):
+        cache, batch, q, k, v = t.device(max_q)
+        dense = q.contiguous()
+        assert binding.kv_append(dense, k, v, cache, batch, rope=rope, interleaved=interleaved, out=dense) is dense
+        assert torch.equal(dense, want)
