@@ -86,9 +86,10 @@ __device__ __forceinline__ float chunks_per_tile(const AttnArgs &p) {
     return (float)p.target / fmaxf(sum, 1.0f);
 }
 
-// Codes are read once.  With pages of a tile, whole 128-byte lines at a time: the
-// caches need not keep them (3 to 4% on 4k to 8k tokens; with larger pages, where two
-// waves share the lines of the values, 25% slower).
+// Where sixteen rows are all that a kv head has, codes are read once, and with pages of a
+// tile whole 128-byte lines at a time: the caches need not keep them (32 sequences of 8k: 97
+// -> 87 us; with larger pages, where two waves share the lines of the values, 25% slower, and
+// with more rows, for which they are read again, 121 -> 150 us at 32, 160 -> 214 us at 44).
 template <bool ONCE>
 __device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
     typedef uint32_t words __attribute__((ext_vector_type(4)));
@@ -97,7 +98,7 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// PAGE: pages of 64 keys (a tile), of more (kLarge), or of fewer (kSmall).  With
+// PAGE: pages of 64 keys (a tile), read once (kOne), of that and more (kLarge), or of fewer (kSmall).  With
 // those of a tile or more, a tile's page and scales are the same for all lanes.
 enum { kSmall, kOne, kLarge };
 template <typename T, int D, int PAGE, int W>
@@ -460,38 +461,52 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
     }
 }
 
-// Rows of a sequence and kv head from which the prompt kernel takes a call, by the pairs of
-// sequence and kv head, the tiles of keys of each, and the width of heads.  The split kernel
+// Rows of a sequence and kv head from which the prompt kernel takes a call, by the width of
+// heads, the pairs of sequence and kv head, and the tiles of keys of all pairs.  The split kernel
 // reads keys and values again for every sixteen rows; the prompt kernel is slower to start, and
 // cuts a row tile into 32 chunks at most, so with few pairs most of the GPU has nothing to do.
-// Measured (us, split / prompt, by rows times query heads to a kv head):
-//   heads of 128                  20        32        64        96       128       256
-//   8 pairs, 500 keys          14/21     14/22     14/23     14/24     14/24     22/25
-//   8, 4000                    20/25     20/25     19/27     26/28     29/29     51/32
-//   8, 16k                     22/27     23/27     29/30     55/33     66/34    114/48
-//   8, 131k                   79/123    78/125   130/133   366/136   453/141  1124/224
-//   128, 500                   13/23     13/23     14/25     19/26     23/26     37/28
-//   128, 4000                  37/46     37/49     62/65     88/74    110/83   195/141
-//   128, 16k                 130/134   129/135   238/187   349/209   436/235   817/421
-//   32, 4000                   22/27     22/28     30/36     31/39     32/41     55/54
-//   16, 131k                  93/141   154/139   308/191   407/211   599/248   912/444
-//   2, 131k                   24/122    30/123    41/129    92/130    64/130   108/133
-//   1, 131k                   21/121    23/122    28/128    52/129    39/132    61/131
-//   heads of 256: 8, 4000      21/26     22/27     28/31     47/32     58/34    108/43
-//   8, 16k                     35/30     37/30     52/36    108/43    134/49    253/71
-//   128, 500                   17/25     17/25     30/28     42/29     54/30    105/39
-//   32, 16k                    92/54     89/56    156/78   236/101   240/111   422/199
-//   2, 131k                   39/124    54/125    81/133   189/133   134/136   238/144
-//   heads of 64: 8, 16k        18/23     19/23     22/25     33/27     40/28     61/38
-//   8, 131k                    46/94     48/94    77/100   153/103   186/105   455/152
-//   128, 4000                  20/37     21/40     30/52     39/59     48/65    84/110
-//   128, 16k                  63/99    64/102    93/136   135/145   171/155   314/286
-int prompt_rows(long long pairs, long long tiles, int head_dim) {
-    const long long all = pairs * tiles;
-    const int at = all >= 12288 ? 0 : all >= 1536 ? 1 : all >= 384 ? 2 : 3;
-    static const int rows[3][4] = {{80, 96, 160, 288}, {48, 72, 112, 288}, {kRows + 1, 32, 64, 160}};
+// With fewer sequences than XCDs the split kernel's chunks leave some of these idle.
+// Measured (us, split / prompt, by rows times query heads to a kv head, pages of 64):
+//   heads of 128                 32        64        96       128       256       512
+//   1 x 1 kv head, 16k        20/25     20/26     22/28     20/28     23/29     27/31
+//   1 x 1, 131k              22/114    27/119    48/121    38/124    60/125   115/128
+//   1 x 2, 131k              28/115    39/120    81/123    61/123   104/128   464/137
+//   1 x 8, 500                13/21     14/21     14/22     14/23     21/24     36/24
+//   1 x 8, 4000               19/24     19/25     24/27     29/28     48/32    182/45
+//   1 x 8, 16k                21/26     27/28     51/32     63/33    109/47    681/72
+//   1 x 8, 131k              66/118   107/124   293/132   359/137   801/222  4788/418
+//   16 x 1, 4000              19/26     21/27     27/30     29/32     30/42     51/53
+//   16 x 1, 16k               26/30     40/39     50/42     64/48     92/72   169/119
+//   16 x 1, 131k            126/132   244/184   298/207   462/232   704/435  1366/802
+//   16 x 2, 4000              21/27     30/34     30/38     30/40     51/51     92/80
+//   16 x 2, 16k               40/43     64/58     91/65     94/71   170/121   326/211
+//   16 x 8, 500               14/21     14/24     18/25     22/26     37/28     66/39
+//   16 x 8, 4000              31/46     50/62     71/70     92/81   173/140   336/185
+//   16 x 8, 16k             107/126   183/178   257/196   331/233   650/418  1278/713
+//   heads of 64: 1 x 8, 500   14/17     14/17     14/18     14/18     13/19     20/19
+//   1 x 8, 4000               20/20     19/22     21/23     20/23     50/25     90/35
+//   1 x 8, 16k                20/23     22/24     33/26     39/28     61/37    289/55
+//   1 x 8, 131k               46/90     76/97    153/99   188/100   409/150  1918/277
+//   16 x 2, 4000              19/23     19/27     19/30     19/33     31/41     50/66
+//   16 x 2, 16k               31/34     41/46     63/50     64/52     93/86   158/152
+//   16 x 8, 4000              20/37     30/52     39/58     48/64    85/109   153/125
+//   16 x 8, 16k               63/94    93/136   123/146   155/156   284/287   538/472
+//   heads of 256: 1 x 2, 131k 45/126   66/132   152/135   109/133   195/147   803/208
+//   1 x 8, 500                15/23     15/25     26/26     26/26     50/26     97/26
+//   1 x 8, 4000               21/27     26/30     44/32     55/34     96/42    388/51
+//   1 x 8, 16k                33/30     46/35     95/43    117/48    219/71  1384/117
+//   16 x 1, 4000              30/29     31/32     50/37     53/40     53/49     99/74
+//   16 x 2, 16k               67/55    120/78   175/105   178/113   333/201   661/376
+//   16 x 8, 500               16/25     28/28     40/29     51/30     96/39    187/70
+//   16 x 8, 4000              54/57    101/79   146/114   192/124   375/184   750/341
+int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim) {
+    static const int rows[3][2][5] = {{{80, 80, 80, 144, 512}, {96, 128, 768, 768, 768}},
+                                      {{72, 72, 72, 120, 288}, {64, 96, 256, 384, 768}},
+                                      {{24, 24, 24, 72, 96}, {24, 24, 40, 72, 288}}};
+    const long long pairs = (long long)seqs * kv_heads, all = pairs * tiles;
     const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
-    return (int)std::max<long long>(rows[width][at], (width == 2 ? 256 : 640) / pairs);
+    const int at = all >= 12288 ? 0 : all >= 3072 ? 1 : all >= 1536 ? 2 : all >= 384 ? 3 : 4;
+    return (int)std::max<long long>(rows[width][seqs >= kXcds][at], (width == 2 ? 320 : 640) / pairs);
 }
 
 // The grid of a call: the most chunks, whose number is found on the device, and the
@@ -511,7 +526,7 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
     const long long tiles = (keys + kTile - 1) / kTile;
-    pl.few = prompt_rows((long long)seqs * kv_heads, tiles, head_dim);
+    pl.few = prompt_rows(seqs, kv_heads, tiles, head_dim);
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
@@ -555,9 +570,9 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
 template <typename T, int D, int W>
 void launch_split(const AttnArgs &p, int row_tiles, int grid, hipStream_t s) {
     const int page = 1 << p.c.log2_page;
-    if (page == kTile)
+    if (page == kTile && row_tiles == 1)
         split_kernel<T, D, kOne, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
-    else if (page > kTile)
+    else if (page >= kTile)
         split_kernel<T, D, kLarge, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
     else
         split_kernel<T, D, kSmall, W><<<grid, 64 * W, 0, s>>>(p, row_tiles);
