@@ -446,8 +446,11 @@ awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k,
  * over the keys j that the row at position i sees: j <= i and, with a window
  * > 0, j > i - window or j < sinks (the first tokens stay visible).  window 0:
  * no window (sinks then say nothing).  A row that sees no key gets zeros.
- * Products, maxima, sums and outputs are held in fp32, weights as two halves
- * (22 bits) in the second product; out is rounded once.
+ * Products, maxima, sums and outputs are held in fp32; out is rounded once.  In
+ * the second product weights are two halves, 22 bits together, and what a key
+ * adds (its weight times its page's scale) is off by 2^-30 of the row's largest
+ * such product at most.  bf16 queries are halves times a power of two of their
+ * row: elements 2^-28 below the row's largest lose bits, and from 2^-38 on all.
  *   q [rows][q_heads][head_dim] with q_stride as above; out dense, apart from q.
  *   scale: finite (1 / sqrt(head_dim) by custom).
  *   workspace: device scratch of at least awq_attention_workspace_bytes for the

@@ -45,10 +45,10 @@ constexpr float kWeightBits = 14.0f;       // weights are 2^14 times those of th
 // tile) groups and, on the device, from the sequences' lengths.  Measured at 32 heads
 // over 8 of 128 elements, pages of 64 (us):
 //   not cut / dealt to 256 / 512 / 1024 workgroups
-//   1 sequence of 300: 7.3 / 10.0 / 10.0 / 10.0;  of 1000: 12.1 / 10.6 / 10.6 / 10.6
-//   1 of 32k: 213 / 20.2 / 20.5 / 26.3;  8 of 4k to 8k: 59 / 29.7 / 31.1 / 37.4
-//   16 of 4k to 8k: 64 / 49.9 / 45.0 / 49.0;  24 of 3k to 6k: 54.0 / 56.8 / 55.9 / 57.9
-//   64 of 1k to 2k: 40.9 / 45.9 / 45.7 / 49.4
+//   1 sequence of 300: 7.3 / 10.0 / 10.0 / 10.0;  of 1000: 10.8 / 10.4 / 10.4 / 10.4
+//   1 of 32k: 211 / 19.0 / 19.8 / 25.6;  8 of 4k to 8k: 57 / 34.3 / 31.3 / 37.3
+//   16 of 4k to 8k: 68 / 58.1 / 46.5 / 53.1;  24 of 3k to 6k: 53.9 / 56.5 / 55.4 / 57.8
+//   64 of 1k to 2k: 39.8 / 45.1 / 45.0 / 48.8
 // So: few tiles take no longer than the launch that joins chunks (and the call itself,
 // which is some 4 us shorter for one launch); one workgroup for
 // each CU streams as fast as the memory, while sequences of different lengths need a
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
     float per_tile = 0.0f;
     if (p.most > 1) {
         // With many sequences only those who may be cut ask: 1024 of 300 tokens in a call that may
-        // have 64k, 760 -> 180 us (138 uncut).  With few, asking at once saves a load's time (0.6 us).
+        // have 64k, 760 -> 182 us (142 uncut).  With few, asking at once saves a load's time (0.6 us).
         bool ask = c.seqs < 64;
         if (!ask) {
             const int most = min(p.most, visible_tiles(p, s.first(), s.len - 1, s.len).count() / kLeastChunk);
@@ -513,7 +513,9 @@ int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim) {
 // workgroups that they are dealt to.
 // Where most sequences have far fewer rows than the longest, each kernel takes those that
 // suit it (one sequence of 2048 rows, 63 of one, all over 4k keys: 810 us with the prompt
-// kernel alone, 235 with both; 255 of one: 1854 and 476), and cuts them by a number of its own.
+// kernel alone, 235 with both, before weights were two halves, 255 since; 255 of one: 1854,
+// 476 and 494), and cuts them by a number of its own (one of 2048 rows and one single token
+// over 131k keys: 930 -> 221 us, the prompt alone 70).
 struct Plan {
     bool prompt, mixed;      // whether the prompt kernel is needed, and both are
     bool wide;               // eight waves to a workgroup
@@ -549,9 +551,9 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     // 1126 at eight, 692 at two)
     long long want = groups >= 16384 ? 2 : groups >= 4096 ? 4 : std::max(8ll, 4 * ((pl.target + groups - 1) / groups));
     // Heads of 64 (8 kv heads; us, four waves and joined or not / eight waves and not cut):
-    // 1, 16, 32, 48 sequences of 500 to 1000: 9.2 / 7.9, 12.6 / 8.5, 9.3 / 9.2, 12.0 / 12.6; of 1k to
-    // 2k 9.4 / 10.9, 14.1 / 11.6, 13.9 / 13.2, 18.9 / 19.6; of 3k to 6k 10.8 / 22.4, 24.2 / 24.8,
-    // 31.5 / 30.6, 44.4 / 46.0; of 250 to 500 6.3 / 6.5 at four.  With heads of 128 a CU has room for
+    // 1, 16, 32, 48 sequences of 500 to 1000: 9.1 / 7.4, 11.9 / 8.2, 8.7 / 8.6, 11.6 / 12.0; of 1k to
+    // 2k 9.2 / 10.2, 13.5 / 10.7, 13.3 / 12.6, 18.3 / 18.8; of 3k to 6k 10.6 / 21.8, 23.1 / 24.2,
+    // 30.6 / 29.0, 43.0 / 44.7; of 250 to 500 5.9 / 5.9 at one.  With heads of 128 a CU has room for
     // eight waves, whose workgroup is no faster (1 of 1000: 12.1 / 12.3).
     pl.wide = !pl.mixed && head_dim == 64 && groups <= 256 && tiles > kUncutTiles && tiles <= std::max(24ll, groups / 2);
     if (tiles <= kUncutTiles || pl.wide || (groups >= kManyGroups && tiles <= kLongTiles)) want = 1;

@@ -10,7 +10,9 @@
 // O^T = V^T P^T takes them as they lie.  LDS row m of a half tile holds key
 // 16 (m / 4 % 2) + 4 (m / 8) + m % 4, so that lane half hf ends up with the
 // sixteen consecutive keys 16 hf .. 16 hf + 15 of it, one 16-byte piece of a row
-// of V^T.  Pieces are stored xor-swizzled by their row: no bank conflicts.
+// of V^T.  Pieces are stored xor-swizzled by their row, which spreads eight rows over the
+// banks; rows r and r + 8 meet (half of the LDS cycles with 128 elements are such conflicts,
+// a third with 256).
 //
 // Heads of 256 elements: queries, outputs and scores of 32 rows are 224 registers of
 // a wave, which leaves one wave to a SIMD and nothing beside its vector instructions
@@ -19,19 +21,21 @@
 // of the outputs; the rows' maxima and the weights go from one to the other through LDS, lane
 // by lane as they lie.  A tile's scores run beside the outputs of the tile before, so
 // two barriers a tile do.  Two waves to a SIMD: 8192 rows under a window of 1024, 250
-// -> 191 us (680 TFLOP/s).  With 128 elements, where two waves fit as it is, 163 against
-// 180 us on 4096 rows: not there.
+// -> 191 us.  With 128 elements, where two waves fit as it is, 163 against 180 us on 4096
+// rows: not there.  (Both before weights were two halves.)  Four registers are spilled, six
+// with pages of fewer than 64 tokens.
 //
-// Bound: vector instructions (half of the issue slots; the codes' conversion is a third
-// of them) and matrix instructions, which overlap in part, under the power limit.
+// Bound: vector and matrix instructions, one after the other: of a SIMD's cycles on 4096
+// rows the first take 54%, the second 43% (1.5 times that of the formula's products, for the
+// remainders), and the two waves of a SIMD hardly overlap them.
 //
 // Few row tiles over many keys are cut into chunks of keys, joined by combine_kernel.
 //
 // Weights go into the products as two halves, the leading part and its remainder
 // (lead_and_rest), as in the split kernel: a query's outputs are as exact in a prompt as alone.
-// Half more matrix instructions for it: 4096 rows 166 -> 208 us, chunks of 512 rows on 16k
-// contexts 700 -> 890 us, 8192 rows of 256 elements under a window 194 -> 232 us; with one
-// half the error against 64 bits was 2.4e-4 where fp16's own rounding makes 1.8e-4.
+// Half more matrix instructions for it: 4096 rows 166 -> 214 us (640 TFLOP/s), chunks of 512
+// rows on 16k contexts 700 -> 898 us, 8192 rows of 256 elements under a window 194 -> 235 us;
+// with one half the error against 64 bits was 2.4e-4 where fp16's own rounding makes 1.8e-4.
 // The sum takes them before the roundings.
 // They are scaled by 2^11 so that small ones stay normal numbers, and the
 // maximum that they refer to is moved only when a row exceeds it by 2^4, so the
@@ -46,9 +50,9 @@ namespace awq {
 namespace {
 
 constexpr int kWaveRows = 32, kWaves = 4;
-// Least tiles of a chunk, most chunks of a row tile.  5 rows of 32 heads over 16k, 4k and
-// 500 keys, one sequence: 33 / 38 / 16 us at 16 tiles, 23 / 22 / 16 at 8, 21 / 17 / 14 at 4;
-// 16 sequences of 500: 17 / 17 / 21.
+// Least tiles of a chunk, most chunks of a row tile.  32 rows of 32 heads over 4k, 16k and 131k
+// keys, one sequence: 47 / 43 / 140 us at 16 tiles, 26 / 32 / 137 at 6, 24 / 32 / 140 at 4; 16
+// sequences of 32 rows over 4k: 90 / 84 / 85.
 constexpr int kLeastChunk = 6, kMostSplits = 32;
 constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
 
@@ -640,7 +644,7 @@ hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, 
     // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
     // keys meet in one XCD's cache.  Then the row tiles of a sequence, and the sequences, the
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
-    // one of them over twice the keys of the others: 1080 -> 693 us).  The kernel steps on where
+    // one of them over twice the keys of the others: 1080 -> 693 us before weights were two halves).  The kernel steps on where
     // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
     const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.most;
     if (grid == 0) return hipSuccess;

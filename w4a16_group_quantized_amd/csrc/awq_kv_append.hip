@@ -140,8 +140,10 @@ __device__ __forceinline__ void turn_unit(float x[16], int c0, int c1, int rot, 
 
 // kThreads: 256 for prompts, 128 for a few tokens.  kKeys: units of keys that a thread
 // can hold (and half as many tiles of values): 2, or 4 where pages of 128 tokens of
-// 128 elements need it (there 146 -> 140 us against reading them twice; with 4 for
-// pages of 64 the registers cost 45.6 -> 49 us).  Workgroups 0 .. pages - 1 of a
+// 128 elements, or as much, need it.  There 16384 tokens of 64/8 heads go 146 -> 136 us with
+// adjacent pairs and 140 -> 137 with the others, whose instance spills 17 to 21 registers, 4 x
+// 2048 of 32/8 heads 56 -> 50 and 51 -> 50; 8 x 300 tokens 22.8 -> 22.3 and 20.8 -> 22.2.  (With 4
+// for pages of 64 the registers cost 45.6 -> 49 us.)  Workgroups 0 .. pages - 1 of a
 // (sequence, kv head) take its pages, the others its queries: those are two thirds
 // of a prompt's bytes at four query heads to a kv head, and with them in the pages'
 // workgroups the last round of these was long.
