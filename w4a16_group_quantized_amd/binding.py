@@ -573,13 +573,18 @@ class KvBatch:
         object.__setattr__(self, "_at", tuple(ptr))
         object.__setattr__(self, "_ask", (self.page_table.data_ptr, self.kv_lens.data_ptr, self.q_starts.data_ptr))
         object.__setattr__(self, "_size", (seqs, width))
+        object.__setattr__(self, "_last", (-1, None))
         object.__setattr__(self, "_device", self.page_table.device)
 
     def _c(self, rows: int) -> CKvBatch:
         a, b, c = self._ask
         if (a(), b(), c()) != self._at:
             self.__post_init__()
-        return CKvBatch(*self._at, *self._size, rows, self.max_q, self.max_kv)
+        last = self._last                    # (rows, the view of so many): most calls have as many as the one before
+        if last[0] != rows:
+            last = (rows, CKvBatch(*self._at, *self._size, rows, self.max_q, self.max_kv))
+            object.__setattr__(self, "_last", last)
+        return last[1]
 
 
 def _rows(t: torch.Tensor, rows: int, heads: int, dtype: torch.dtype, cache: KvCache, name: str):
