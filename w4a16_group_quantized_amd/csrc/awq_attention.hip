@@ -505,7 +505,7 @@ int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim) {
                                       {{24, 24, 24, 72, 96}, {24, 24, 40, 72, 288}}};
     const long long pairs = (long long)seqs * kv_heads, all = pairs * tiles;
     const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
-    const int at = all >= 12288 ? 0 : all >= 3072 ? 1 : all >= 1536 ? 2 : all >= 384 ? 3 : 4;
+    const int at = all >= 12000 ? 0 : all >= 3000 ? 1 : all >= 1500 ? 2 : all >= 400 ? 3 : 4;
     return (int)std::max<long long>(rows[width][seqs >= kXcds][at], (width == 2 ? 320 : 640) / pairs);
 }
 
