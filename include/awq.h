@@ -467,6 +467,134 @@ awq_status awq_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int
                          const awq_kv_cache *cache, const awq_kv_batch *batch, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/*
+ * awq_kv_append_at: awq_kv_append for rows whose rotary positions are not their
+ * places in the sequence, or are several: drafted rows (a token's position is its
+ * depth's, its place the next free one), images and video (time, height, width).
+ *   positions: device int32 [rows][axes], 1 <= axes <= AWQ_MAX_AXES;
+ *   axis_of: HOST array of rot_dim / 2 axes, that of each frequency (sections, or in
+ *   turn), each below `axes` (AWQ_ERROR_INVALID_VALUE otherwise), read before the
+ *   call returns; NULL: axis 0 for all.
+ * Frequency f of a row is turned by column f (cosine) and rot_dim / 2 + f (sine) of
+ * row positions[row][axis_of[f]] of the table; a position outside the table turns by
+ * NaN: the query comes out NaN there, the key is one that is not finite (see above).
+ * A row's place in the cache is that of awq_kv_batch, and only a row without one is
+ * dropped.  All else is as with awq_kv_append; positions may be NULL if there are
+ * no rows.
+ */
+#define AWQ_MAX_AXES 4
+
+awq_status awq_kv_append_at(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                            const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
+                            int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                            int32_t interleaved, const int32_t *positions, int32_t axes,
+                            const uint8_t *axis_of, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                            void *stream);
+
+/*
+ * Drafted trees: a sequence's rows in a call are the nodes of a tree of guesses
+ * behind its other tokens, and are checked all at once.  A row sees every token
+ * before the tree, and of the tree itself and its ancestors.
+ *
+ * awq_tree_rows: that, from the parents.  parents: device int32 [rows], a row's
+ * parent by its number among its sequence's rows; one that is negative, or not
+ * before the row itself, is none: the row hangs on the last token before the tree.
+ *   mask: device uint32 [rows][mask_words]: bit u % 32 of word u / 32 of a row says
+ *   that it sees row u of its sequence.  Rows past 32 * mask_words have no bit.
+ *   positions: device int32 [rows], or NULL: kv_lens - rows of the sequence + depth,
+ *   for awq_kv_append_at (depth 0: no parent).
+ * Of the batch, page_table, table_width and max_kv are not looked at.  Rows of no
+ * sequence are left as they were.
+ */
+awq_status awq_tree_rows(const int32_t *parents, uint32_t *mask, int32_t mask_words, int32_t *positions,
+                         const awq_kv_batch *batch, void *stream);
+
+/*
+ * awq_tree_attention: awq_attention where a row sees, of its sequence's rows in this
+ * call, those whose bits are set in its row of `mask` (laid out as above; any bits,
+ * in any order, also none), and every token before these.  With a window w > 0 a
+ * row counts as standing at position i = (tokens before the rows) + (bits set in its
+ * mask) - 1, and of the tokens j before the rows it sees those with j > i - w or
+ * j < sinks; the rows' own tokens are not subject to the window.  (Bits past the
+ * sequence's rows name no token, but count.)  A chain (row t sees rows 0 .. t)
+ * gives awq_attention's outputs.
+ * Everything else, the workspace included, is as with awq_attention.
+ */
+size_t awq_tree_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
+                                          const awq_kv_cache *cache, const awq_kv_batch *batch);
+
+awq_status awq_tree_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
+                              int32_t type, float scale, int32_t window, int32_t sinks,
+                              const uint32_t *mask, int32_t mask_words, const awq_kv_cache *cache,
+                              const awq_kv_batch *batch, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * awq_kv_keep: compaction.  Of each sequence's rows (its last tokens: a drafted
+ * tree, or with q_starts over all of its tokens the whole sequence) the kept ones
+ * move together, in place: the token at position first + i becomes the one that was
+ * at first + kept[b][i], i < counts[b], with first = kv_lens[b] - rows of b.
+ *   kept: device int32 [seqs][kept_width], row numbers that ascend; the list ends
+ *   before the first that does not, or names no row of the sequence.
+ *   counts: device int32 [seqs];
+ *   lens_out: device int32 [seqs], another array than kv_lens: the tokens that are
+ *   left, first + (kept ones).  (Call it for each layer's cache with the same batch.)
+ * The scale of a page that tokens come to becomes the largest of those that its
+ * tokens, the ones that stay among them, had; a code c moves from scale s to s' as
+ * e4m3_rne(c * (s / s')), and as it is where these are equal.  Slots behind the
+ * last kept token stay as they are, and so does a page whose tokens are all in place.
+ * A token whose page is none comes as NaN key codes and zero values, as one that is
+ * not finite; one that comes to a place without a page is not written.  A sequence
+ * whose rows do not all have a place (first < 0) is left as it is.
+ * The pages of the kept rows' places and of those behind belong to one sequence only
+ * (awq_kv_fork sees to that).  batch->rows only bounds q_starts.
+ */
+awq_status awq_kv_keep(const int32_t *kept, int32_t kept_width, const int32_t *counts, int32_t *lens_out,
+                       const awq_kv_cache *cache, const awq_kv_batch *batch, void *stream);
+
+/*
+ * awq_kv_fork: the page table of the next step.  New sequence b goes on from sequence
+ * from[b] of the batch with all of its tokens (several may go on from one: they
+ * share its pages), or begins with none if from[b] is none of 0 .. seqs - 1, and is
+ * to grow by grow[b] tokens (less than 0 counts as 0), up to table_width *
+ * page_size in all.  Sequences that nothing goes on from end.
+ *   table_out: int32 [new_seqs][table_width]: the pages of the tokens that b goes on
+ *   with, then those given to it for its growth, then -1.
+ *   lens_out: int32 [new_seqs]: the tokens that b goes on with (without the growth).
+ *   copies: int32 [new_seqs][2]: a page that b has in part, is to grow into, and
+ *   shares, is replaced in its row by a page of its own; from and to for awq_kv_copy,
+ *   or -1, -1.
+ *   missing: int32 [1]: pages that were needed and not there.
+ * Free pages are those that are in no row of the new table (up to its tokens) and not
+ * held; the lowest are given first, to sequences in their order and to their places in
+ * order.  A sequence gets all that it needs or none: none if what it and those
+ * before it need is more than there is; its places are then -1.  With missing > 0
+ * the present table still stands: the call changes none of its inputs.
+ *   held: uint8 [pages] or NULL: pages with another value than 0 are not given, and
+ *   count as shared (a prefix that is kept for later).
+ * All arrays are device memory, outputs apart from inputs (AWQ_ERROR_INVALID_VALUE
+ * where table_out or lens_out is the batch's).  0 <= new_seqs <= 65535, new_seqs *
+ * table_width < 2^31.  The pages' contents and q_starts are not looked at; a page
+ * number that names no page goes on as -1.
+ *   workspace: as with awq_attention.
+ */
+size_t awq_kv_fork_workspace_bytes(int32_t new_seqs, const awq_kv_cache *cache, const awq_kv_batch *batch);
+
+awq_status awq_kv_fork(const int32_t *from, const int32_t *grow, int32_t new_seqs, const uint8_t *held,
+                       const awq_kv_cache *cache, const awq_kv_batch *batch, int32_t *table_out,
+                       int32_t *lens_out, int32_t *copies, int32_t *missing, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * awq_kv_copy: pages (codes and scales, of all heads) from one cache to another of
+ * the same page_size, kv_heads and head_dim, or within one: pairs: device int32
+ * [n][2], from and to; a pair with a number that names no page is passed over.
+ * n <= 2^22.  No page may be copied to twice in a call, or be copied from and to:
+ * what it then holds is unspecified.  (Of awq_kv_fork neither happens.)
+ */
+awq_status awq_kv_copy(const int32_t *pairs, int32_t n, const awq_kv_cache *from, const awq_kv_cache *to,
+                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,7 +26,10 @@ ENTRY_POINTS = ("awq_status_string", "awq_pack", "awq_pack_zeros", "awq_repack",
                 "awq_gemm_splitk_workspace_bytes", "awq_gemm_splitk", "awq_gemm_splitk_static",
                 "awq_channel_stats_workspace_bytes", "awq_channel_stats",
                 "awq_scale_search_workspace_bytes", "awq_scale_search",
-                "awq_kv_append", "awq_attention_workspace_bytes", "awq_attention")
+                "awq_kv_append", "awq_attention_workspace_bytes", "awq_attention",
+                "awq_kv_append_at", "awq_tree_rows", "awq_tree_attention_workspace_bytes",
+                "awq_tree_attention", "awq_kv_keep", "awq_kv_fork_workspace_bytes", "awq_kv_fork",
+                "awq_kv_copy")
 
 # awq_status values of include/awq.h
 AWQ_SUCCESS = 0
@@ -139,6 +142,24 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.awq_attention.restype = ctypes.c_int
     lib.awq_attention.argtypes = [vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, *kv, vp,
                                   ctypes.c_size_t, vp]
+    lib.awq_kv_append_at.restype = ctypes.c_int
+    lib.awq_kv_append_at.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, i32, vp, i32, i32, i32, vp, i32,
+                                     ctypes.c_char_p, *kv, vp]
+    lib.awq_tree_rows.restype = ctypes.c_int
+    lib.awq_tree_rows.argtypes = [vp, vp, i32, vp, ctypes.POINTER(CKvBatch), vp]
+    lib.awq_tree_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.awq_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, *kv]
+    lib.awq_tree_attention.restype = ctypes.c_int
+    lib.awq_tree_attention.argtypes = [vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, vp, i32, *kv, vp,
+                                       ctypes.c_size_t, vp]
+    lib.awq_kv_keep.restype = ctypes.c_int
+    lib.awq_kv_keep.argtypes = [vp, i32, vp, vp, *kv, vp]
+    lib.awq_kv_fork_workspace_bytes.restype = ctypes.c_size_t
+    lib.awq_kv_fork_workspace_bytes.argtypes = [i32, *kv]
+    lib.awq_kv_fork.restype = ctypes.c_int
+    lib.awq_kv_fork.argtypes = [vp, vp, i32, vp, *kv, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.awq_kv_copy.restype = ctypes.c_int
+    lib.awq_kv_copy.argtypes = [vp, i32, kv[0], kv[0], vp]
     if path == LIBRARY:
         _LIB = lib
     return lib
@@ -652,6 +673,14 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
     values into the cache.  q [rows][q_heads][head_dim] (or None), k and v
     [rows][kv_heads][head_dim], fp16 or bf16, rows at any stride; rope fp32
     [positions][rot_dim] (cosines, then sines) or None.  Returns the rotated q."""
+    out, rows, turns, views = _append_args(q, k, v, cache, batch, rope, interleaved, out, stream)
+    _kv_call(cache._device, stream, load().awq_kv_append, *rows, *turns, *views)
+    return out
+
+
+def _append_args(q, k, v, cache, batch, rope, interleaved, out, stream):
+    """The checks of an append's arguments: its output, and what the C call takes (rows,
+    rotation, views)."""
     c, b = cache._view(), batch._c(k.shape[0])
     kind = _kv_type(k, batch, cache, "k")
     rows, heads = k.shape[0], cache._heads
@@ -670,8 +699,43 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
             raise ValueError(f"rope must be [positions][rot_dim] on {k.device}, got {list(rope.shape)} on {rope.device}")
         rp = _dev(rope, torch.float32, "rope")
         positions, rot = rope.shape
-    _kv_call(cache._device, stream, load().awq_kv_append, qp, qs, kp, ks, vp, vs, op, heads, kind, rp, positions,
-             rot, int(interleaved), c, b)
+    return out, (qp, qs, kp, ks, vp, vs, op, heads, kind), (rp, positions, rot, int(interleaved)), (c, b)
+
+
+def axis_map(sections, in_turn: bool = False) -> bytes:
+    """``axis_of`` of kv_append_at for axes that take ``sections[a]`` frequencies each: one axis
+    after the other, or with ``in_turn`` one frequency each as long as each has some left."""
+    if any(n < 0 for n in sections):
+        raise ValueError(f"sections must not be negative, got {list(sections)}")
+    if not in_turn:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    left, out = list(sections), []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return bytes(out)
+
+
+def kv_append_at(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatch,
+                 positions: torch.Tensor, rope: torch.Tensor, axis_of: bytes | None = None,
+                 interleaved: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """kv_append with the rows' rotary positions given: int32 [rows] or [rows][axes], up to
+    four axes.  ``axis_of``: the axis of each of the rot_dim / 2 frequencies (see axis_map),
+    all 0 unless given."""
+    out, rows, turns, views = _append_args(q, k, v, cache, batch, rope, interleaved, out, stream)
+    shape = positions.shape
+    if not 1 <= len(shape) <= 2 or shape[0] != k.shape[0]:
+        raise ValueError(f"positions must be [{k.shape[0]}] or [{k.shape[0]}][axes], got {list(shape)}")
+    at = _kv_ints(positions, cache._device, "positions")
+    if axis_of is not None:
+        if not isinstance(axis_of, bytes):
+            axis_of = bytes(axis_of)
+        if len(axis_of) != turns[2] // 2:
+            raise ValueError(f"axis_of must name an axis for each of {turns[2] // 2} frequencies, got {len(axis_of)}")
+    _kv_call(cache._device, stream, load().awq_kv_append_at, *rows, *turns, at, shape[1] if len(shape) == 2 else 1,
+             axis_of, *views)
     return out
 
 
@@ -687,6 +751,11 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
     their own keys and values already: causal, and with ``window`` > 0 only over the
     last ``window`` tokens and the first ``sinks``.  scale: 1 / sqrt(head_dim) unless
     given.  The workspace is allocated here unless one is given."""
+    return _attention("awq_attention", (), q, cache, batch, scale, window, sinks, out, stream, workspace)
+
+
+def _attention(fn, extra, q, cache, batch, scale, window, sinks, out, stream, workspace):
+    """Either attention: ``extra`` are the arguments that one has beside the other's."""
     c, b = cache._view(), batch._c(q.shape[0])
     kind = _kv_type(q, batch, cache, "q")
     rows, heads = q.shape[0], _heads(q, cache)
@@ -705,6 +774,119 @@ def attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | No
         wp, wn = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
         if workspace.device != cache._device:
             raise ValueError(f"workspace is on {workspace.device}, the cache on {cache._device}")
-    _kv_call(cache._device, stream, lib.awq_attention, qp, qs, op, heads, kind,
-             cache._dim ** -0.5 if scale is None else scale, window, sinks, c, b, wp, wn)
+    _kv_call(cache._device, stream, getattr(lib, fn), qp, qs, op, heads, kind,
+             cache._dim ** -0.5 if scale is None else scale, window, sinks, *extra, c, b, wp, wn)
     return out
+
+
+# ---- drafted trees, compaction, forks ----
+
+def _kv_ints(t: torch.Tensor, device: torch.device, name: str) -> int:
+    """The address of an int32 array on ``device``."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return _dev(t, torch.int32, name)
+
+
+def tree_rows(parents: torch.Tensor, batch: KvBatch, words: int | None = None, out=None, stream=None):
+    """(mask int32 [rows][words], positions int32 [rows]) of drafted rows, from the parents
+    int32 [rows] (by their numbers among the sequence's rows; -1: none): the rows of its
+    sequence that each sees, as bits, and its position.  ``words``: enough for max_q rows
+    unless given.  ``out``: the two to be written, if they are there already."""
+    if parents.dim() != 1:
+        raise ValueError(f"parents must be [rows], got {list(parents.shape)}")
+    at = _kv_ints(parents, batch._device, "parents")
+    rows = parents.shape[0]
+    words = max(1, -(-batch.max_q // 32)) if words is None else words
+    if out is None:
+        out = (_new((rows, words), torch.int32, parents.device, stream), _new(rows, torch.int32, parents.device, stream))
+    mask, positions = out
+    _kv_check(mask, torch.int32, (rows, words), "mask")
+    _kv_check(positions, torch.int32, (rows,), "positions")
+    _kv_call(batch._device, stream, load().awq_tree_rows, at, _kv_ints(mask, batch._device, "mask"), words,
+             _kv_ints(positions, batch._device, "positions"), batch._c(rows))
+    return out
+
+
+def tree_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask: torch.Tensor, scale: float | None = None,
+                   window: int = 0, sinks: int = 0, out: torch.Tensor | None = None, stream=None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """attention where each row sees the tokens before its sequence's rows (with ``window`` > 0
+    the last ones of them, and the first ``sinks``), and of these rows those whose bits are set
+    in ``mask`` int32 [rows][words] (see tree_rows)."""
+    if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
+        raise ValueError(f"mask must be [{q.shape[0]}][words], got {list(mask.shape)}")
+    extra = (_kv_ints(mask, cache._device, "mask"), mask.shape[1])
+    return _attention("awq_tree_attention", extra, q, cache, batch, scale, window, sinks, out, stream, workspace)
+
+
+def kv_keep(kept: torch.Tensor, counts: torch.Tensor, cache: KvCache, batch: KvBatch,
+            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Of each sequence's rows the kept ones move together in the cache, in place: row numbers
+    int32 [seqs][width] that ascend, ``counts`` int32 [seqs] of them.  Returns the sequences'
+    new lengths int32 [seqs] (the batch's stay)."""
+    seqs = batch._size[0]
+    if batch._device != cache._device:
+        raise ValueError(f"the batch is on {batch._device}, the cache on {cache._device}")
+    if kept.dim() != 2 or kept.shape[0] != seqs:
+        raise ValueError(f"kept must be [{seqs}][width], got {list(kept.shape)}")
+    _kv_check(counts, torch.int32, (seqs,), "counts")
+    if out is None:
+        out = _new(seqs, torch.int32, kept.device, stream)
+    _kv_check(out, torch.int32, (seqs,), "out")
+    _kv_call(cache._device, stream, load().awq_kv_keep, _kv_ints(kept, cache._device, "kept"), kept.shape[1],
+             _kv_ints(counts, cache._device, "counts"), _kv_ints(out, cache._device, "out"), cache._view(),
+             batch._c(0x7FFFFFFF))
+    return out
+
+
+def kv_fork(from_: torch.Tensor, grow: torch.Tensor, cache: KvCache, batch: KvBatch, held: torch.Tensor | None = None,
+            out=None, stream=None, workspace: torch.Tensor | None = None):
+    """The next step's page table: new sequence b goes on from sequence ``from_[b]`` (int32
+    [new_seqs]; -1: from none) and is to grow by ``grow[b]`` tokens.  Returns (table
+    [new_seqs][table_width], lens [new_seqs], copies [new_seqs][2], missing [1]), all int32, or
+    writes them to ``out``; ``copies`` go to kv_copy, and with ``missing`` > 0 some sequences
+    have got no pages.  ``held`` uint8 [pages]: pages that are not to be given or written."""
+    if batch._device != cache._device:
+        raise ValueError(f"the batch is on {batch._device}, the cache on {cache._device}")
+    if from_.dim() != 1 or grow.shape != from_.shape:
+        raise ValueError(f"from_ and grow must be [new_seqs], got {list(from_.shape)}, {list(grow.shape)}")
+    n, width, device = from_.shape[0], batch._size[1], cache._device
+    c, b, lib = cache._view(), batch._c(0), load()
+    shapes = ((n, width), (n,), (n, 2), (1,))
+    if out is None:
+        out = tuple(_new(x, torch.int32, device, stream) for x in shapes)
+        if n == 0:
+            out[3].zero_()
+    for t, x, name in zip(out, shapes, ("table", "lens", "copies", "missing")):
+        _kv_check(t, torch.int32, x, name)
+    hp = None
+    if held is not None:
+        _kv_check(held, torch.uint8, (cache.k.shape[0],), "held")
+        if held.device != device:
+            raise ValueError(f"held is on {held.device}, the cache on {device}")
+        hp = _dev(held, torch.uint8, "held")
+    if workspace is None:
+        workspace = _new(max(16, lib.awq_kv_fork_workspace_bytes(n, c, b)), torch.uint8, device, stream)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the cache on {device}")
+    _kv_call(device, stream, lib.awq_kv_fork, _kv_ints(from_, device, "from_"), _kv_ints(grow, device, "grow"), n, hp, c, b,
+             *(_kv_ints(t, device, name) for t, name in zip(out, ("table", "lens", "copies", "missing"))),
+             _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    return out
+
+
+def kv_fork_workspace_bytes(new_seqs: int, cache: KvCache, batch: KvBatch) -> int:
+    return load().awq_kv_fork_workspace_bytes(new_seqs, cache._view(), batch._c(0))
+
+
+def kv_copy(pairs: torch.Tensor, cache: KvCache, to: KvCache | None = None, stream=None) -> None:
+    """Copies pages within a cache, or to another of the same geometry: int32 [n][2], from and to;
+    pairs with a number that names no page (-1) are passed over."""
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError(f"pairs must be [n][2], got {list(pairs.shape)}")
+    to = cache if to is None else to
+    if to._device != cache._device:
+        raise ValueError(f"to is on {to._device}, the cache on {cache._device}")
+    _kv_call(cache._device, stream, load().awq_kv_copy, _kv_ints(pairs, cache._device, "pairs"), pairs.shape[0],
+             cache._view(), to._view())

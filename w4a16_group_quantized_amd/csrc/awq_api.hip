@@ -361,11 +361,12 @@ awq_status awq_scale_search(const uint16_t *x, int32_t M, const uint16_t *w, int
                                              as_stream(stream)));
 }
 
-awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
-                         const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
-                         int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
-                         int32_t interleaved, const awq_kv_cache *cache, const awq_kv_batch *batch,
-                         void *stream) {
+// What both forms of awq_kv_append check; `work`: whether there is any.
+static awq_status check_append(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                               const uint16_t *v, int32_t v_stride, const uint16_t *q_out, int32_t q_heads,
+                               int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                               const awq_kv_cache *cache, const awq_kv_batch *batch, bool *work) {
+    *work = false;
     awq_status st = check_kv(cache, batch);
     if (st != AWQ_SUCCESS) return st;
     if (!known_type(type) || rot_dim < 0 || q_heads <= 0) return AWQ_ERROR_INVALID_VALUE;
@@ -381,11 +382,50 @@ awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k,
     if (st == AWQ_SUCCESS && q != nullptr)
         st = check_rows(q, batch->rows, q_stride, q_heads, cache->head_dim);
     if (st == AWQ_SUCCESS && q_out != nullptr && !aligned16(q_out)) st = AWQ_ERROR_ALIGNMENT;
-    if (st != AWQ_SUCCESS) return st;
+    *work = st == AWQ_SUCCESS;
+    return st;
+}
+
+awq_status awq_kv_append(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                         const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
+                         int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                         int32_t interleaved, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                         void *stream) {
+    bool work;
+    const awq_status st = check_append(q, q_stride, k, k_stride, v, v_stride, q_out, q_heads, type, rope,
+                                       rope_positions, rot_dim, cache, batch, &work);
+    if (!work) return st;
     return done(stream, awq::launch_kv_append(kv_view(cache, batch), cache->head_dim, q, q_stride, k,
                                               k_stride, v, v_stride, q_out, q_heads, rope,
                                               rope_positions, rot_dim, interleaved != 0,
                                               type == AWQ_TYPE_BF16, grid_rows(batch), as_stream(stream)));
+}
+
+awq_status awq_kv_append_at(const uint16_t *q, int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                            const uint16_t *v, int32_t v_stride, uint16_t *q_out, int32_t q_heads,
+                            int32_t type, const float *rope, int32_t rope_positions, int32_t rot_dim,
+                            int32_t interleaved, const int32_t *positions, int32_t axes,
+                            const uint8_t *axis_of, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                            void *stream) {
+    bool work;
+    const awq_status st = check_append(q, q_stride, k, k_stride, v, v_stride, q_out, q_heads, type, rope,
+                                       rope_positions, rot_dim, cache, batch, &work);
+    if (st != AWQ_SUCCESS) return st;
+    if (axes < 1 || axes > AWQ_MAX_AXES) return AWQ_ERROR_INVALID_VALUE;
+    awq::AxisMap map{};
+    for (int f = 0; f < rot_dim / 2; ++f) {
+        const int axis = axis_of == nullptr ? 0 : axis_of[f];
+        if (axis >= axes) return AWQ_ERROR_INVALID_VALUE;
+        map.set(f, axis);
+    }
+    if (!work) return st;
+    if (positions == nullptr) return AWQ_ERROR_INVALID_VALUE;
+    if ((long long)batch->rows * axes > kMaxElems) return AWQ_ERROR_SHAPE;
+    if (!aligned16(positions)) return AWQ_ERROR_ALIGNMENT;
+    return done(stream, awq::launch_kv_append_at(kv_view(cache, batch), cache->head_dim, q, q_stride, k,
+                                                 k_stride, v, v_stride, q_out, q_heads, rope,
+                                                 rope_positions, rot_dim, interleaved != 0, positions, axes, map,
+                                                 type == AWQ_TYPE_BF16, grid_rows(batch), as_stream(stream)));
 }
 
 size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
@@ -397,27 +437,128 @@ size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t si
                                     grid_rows(batch), grid_keys(cache, batch), window, sinks);
 }
 
-awq_status awq_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
-                         int32_t type, float scale, int32_t window, int32_t sinks,
-                         const awq_kv_cache *cache, const awq_kv_batch *batch, void *workspace,
-                         size_t workspace_bytes, void *stream) {
+// Both attentions; tree: whether the rows' bits are asked for.
+static awq_status attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads, int32_t type,
+                            float scale, int32_t window, int32_t sinks, bool tree, const uint32_t *mask,
+                            int32_t mask_words, const awq_kv_cache *cache, const awq_kv_batch *batch,
+                            void *workspace, size_t workspace_bytes, void *stream) {
     awq_status st = check_kv(cache, batch);
     if (st != AWQ_SUCCESS) return st;
     if (!known_type(type) || !isfinite(scale) || window < 0 || sinks < 0 || q_heads <= 0)
         return AWQ_ERROR_INVALID_VALUE;
+    if (tree && mask_words <= 0) return AWQ_ERROR_INVALID_VALUE;
     if (q_heads % cache->kv_heads) return AWQ_ERROR_SHAPE;
     if (batch->seqs == 0 || batch->rows == 0) return AWQ_SUCCESS;
     st = check_rows(q, batch->rows, q_stride, q_heads, cache->head_dim);
-    if (st == AWQ_SUCCESS && out == nullptr) st = AWQ_ERROR_INVALID_VALUE;
-    if (st == AWQ_SUCCESS && !aligned16(out)) st = AWQ_ERROR_ALIGNMENT;
+    if (st == AWQ_SUCCESS && (out == nullptr || (tree && mask == nullptr))) st = AWQ_ERROR_INVALID_VALUE;
+    if (st == AWQ_SUCCESS && tree && (long long)batch->rows * mask_words > kMaxElems) st = AWQ_ERROR_SHAPE;
+    if (st == AWQ_SUCCESS && (!aligned16(out) || (tree && !aligned16(mask)))) st = AWQ_ERROR_ALIGNMENT;
     if (st != AWQ_SUCCESS) return st;
     const size_t need = awq_attention_workspace_bytes(q_heads, window, sinks, cache, batch);
     if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return AWQ_ERROR_WORKSPACE;
     return done(stream, awq::launch_attention(kv_view(cache, batch), cache->head_dim, q, q_stride, out,
                                               q_heads, type == AWQ_TYPE_BF16, scale, window, sinks,
-                                              grid_rows(batch), grid_keys(cache, batch), workspace,
-                                              as_stream(stream)));
+                                              grid_rows(batch), grid_keys(cache, batch), mask, mask_words,
+                                              workspace, as_stream(stream)));
+}
+
+awq_status awq_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
+                         int32_t type, float scale, int32_t window, int32_t sinks,
+                         const awq_kv_cache *cache, const awq_kv_batch *batch, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    return attention(q, q_stride, out, q_heads, type, scale, window, sinks, false, nullptr, 0, cache, batch,
+                     workspace, workspace_bytes, stream);
+}
+
+awq_status awq_tree_rows(const int32_t *parents, uint32_t *mask, int32_t mask_words, int32_t *positions,
+                         const awq_kv_batch *batch, void *stream) {
+    if (batch == nullptr || batch->seqs < 0 || batch->rows < 0 || batch->max_q < 0 || mask_words <= 0 ||
+        (batch->seqs > 0 && (batch->kv_lens == nullptr || batch->q_starts == nullptr)))
+        return AWQ_ERROR_INVALID_VALUE;
+    if (batch->seqs > 65535 || (long long)batch->rows * mask_words > kMaxElems) return AWQ_ERROR_SHAPE;
+    if (!aligned16(batch->kv_lens) || !aligned16(batch->q_starts)) return AWQ_ERROR_ALIGNMENT;
+    if (batch->seqs == 0 || batch->rows == 0) return AWQ_SUCCESS;
+    if (parents == nullptr || mask == nullptr) return AWQ_ERROR_INVALID_VALUE;
+    if (!aligned16(parents) || !aligned16(mask) || !aligned16(positions)) return AWQ_ERROR_ALIGNMENT;
+    awq::KvView c{};
+    c.kv_lens = batch->kv_lens;
+    c.q_starts = batch->q_starts;
+    c.seqs = batch->seqs;
+    c.rows = batch->rows;
+    return done(stream, awq::launch_tree_rows(parents, c, grid_rows(batch), mask, mask_words, positions, as_stream(stream)));
+}
+
+size_t awq_tree_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
+                                          const awq_kv_cache *cache, const awq_kv_batch *batch) {
+    return awq_attention_workspace_bytes(q_heads, window, sinks, cache, batch);
+}
+
+awq_status awq_tree_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,
+                              int32_t type, float scale, int32_t window, int32_t sinks,
+                              const uint32_t *mask, int32_t mask_words, const awq_kv_cache *cache,
+                              const awq_kv_batch *batch, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    return attention(q, q_stride, out, q_heads, type, scale, window, sinks, true, mask, mask_words, cache,
+                     batch, workspace, workspace_bytes, stream);
+}
+
+awq_status awq_kv_keep(const int32_t *kept, int32_t kept_width, const int32_t *counts, int32_t *lens_out,
+                       const awq_kv_cache *cache, const awq_kv_batch *batch, void *stream) {
+    const awq_status st = check_kv(cache, batch);
+    if (st != AWQ_SUCCESS) return st;
+    if (kept_width <= 0) return AWQ_ERROR_INVALID_VALUE;
+    if ((long long)batch->seqs * kept_width > kMaxElems) return AWQ_ERROR_SHAPE;
+    if (batch->seqs == 0) return AWQ_SUCCESS;
+    if (kept == nullptr || counts == nullptr || lens_out == nullptr || lens_out == batch->kv_lens)
+        return AWQ_ERROR_INVALID_VALUE;
+    if (!aligned16(kept) || !aligned16(counts) || !aligned16(lens_out)) return AWQ_ERROR_ALIGNMENT;
+    return done(stream, awq::launch_kv_keep(kv_view(cache, batch), cache->head_dim, kept, kept_width, counts,
+                                            lens_out, as_stream(stream)));
+}
+
+size_t awq_kv_fork_workspace_bytes(int32_t new_seqs, const awq_kv_cache *cache, const awq_kv_batch *batch) {
+    if (check_kv(cache, batch) != AWQ_SUCCESS || new_seqs <= 0 || new_seqs > 65535 ||
+        (long long)new_seqs * batch->table_width > kMaxElems)
+        return 0;
+    return awq::kv_fork_workspace(new_seqs, batch->table_width, cache->pages);
+}
+
+awq_status awq_kv_fork(const int32_t *from, const int32_t *grow, int32_t new_seqs, const uint8_t *held,
+                       const awq_kv_cache *cache, const awq_kv_batch *batch, int32_t *table_out,
+                       int32_t *lens_out, int32_t *copies, int32_t *missing, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    const awq_status st = check_kv(cache, batch);
+    if (st != AWQ_SUCCESS) return st;
+    if (new_seqs < 0) return AWQ_ERROR_INVALID_VALUE;
+    if (new_seqs > 65535 || (long long)new_seqs * batch->table_width > kMaxElems) return AWQ_ERROR_SHAPE;
+    if (new_seqs == 0) return AWQ_SUCCESS;
+    if (from == nullptr || grow == nullptr || table_out == nullptr || lens_out == nullptr || copies == nullptr ||
+        missing == nullptr || table_out == batch->page_table || lens_out == batch->kv_lens)
+        return AWQ_ERROR_INVALID_VALUE;
+    if (!aligned16(from) || !aligned16(grow) || !aligned16(held) || !aligned16(table_out) || !aligned16(lens_out) ||
+        !aligned16(copies) || !aligned16(missing))
+        return AWQ_ERROR_ALIGNMENT;
+    if (workspace == nullptr || !aligned16(workspace) ||
+        workspace_bytes < awq::kv_fork_workspace(new_seqs, batch->table_width, cache->pages))
+        return AWQ_ERROR_WORKSPACE;
+    return done(stream, awq::launch_kv_fork(from, grow, new_seqs, held, kv_view(cache, batch), table_out, lens_out,
+                                            copies, missing, workspace, as_stream(stream)));
+}
+
+awq_status awq_kv_copy(const int32_t *pairs, int32_t n, const awq_kv_cache *from, const awq_kv_cache *to, void *stream) {
+    awq_kv_batch none{};
+    none.table_width = 1;
+    awq_status st = check_kv(from, &none);
+    if (st == AWQ_SUCCESS) st = check_kv(to, &none);
+    if (st != AWQ_SUCCESS) return st;
+    if (n < 0) return AWQ_ERROR_INVALID_VALUE;
+    if (from->page_size != to->page_size || from->kv_heads != to->kv_heads || from->head_dim != to->head_dim || n > 1 << 22)
+        return AWQ_ERROR_SHAPE;
+    if (n == 0) return AWQ_SUCCESS;
+    if (pairs == nullptr) return AWQ_ERROR_INVALID_VALUE;
+    if (!aligned16(pairs)) return AWQ_ERROR_ALIGNMENT;
+    return done(stream, awq::launch_kv_copy(pairs, n, kv_view(from, &none), kv_view(to, &none), from->head_dim, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -7,6 +7,9 @@
 namespace awq {
 
 constexpr int kTile = 64;                  // keys of a tile
+constexpr int kSplitRows = 16;             // rows of a workgroup of the kernel of few rows
+constexpr int kSplitLeastChunk = 4;        // tiles of its chunks
+constexpr int kXcds = 8;
 constexpr float kEmpty = -0x1.fffffep127f; // running maximum of a row that has seen no key
 // From here on a maximum is taken off the scores before anything is added: its steps are
 // half an exponent's and more, and a sum with it would lose the rest.
@@ -27,6 +30,8 @@ struct AttnArgs {
     int most, target;        // most chunks of a row tile in this kernel; workgroups that all chunks are dealt to
     int splits;              // chunks that a row has room for in the workspace
     int few;                 // rows (times query heads of a kv head) of a sequence from which the prompt kernel takes it
+    const uint32_t *tree;    // awq_tree_attention: [rows][tree_words], the rows of its sequence that a row sees
+    int tree_words;
 };
 
 // The 64-key tiles that rows at positions lo .. hi see: tiles [0, a) that hold
@@ -44,6 +49,61 @@ __device__ __forceinline__ Tiles visible_tiles(const AttnArgs &p, int lo, int hi
     t.a = p.window > 0 ? min((min(p.sinks, end > 0 ? end : 0) + kTile - 1) / kTile, t.b) : 0;
     return t;
 }
+
+// A drafted tree's rows see all tokens before the tree (under a window those that are near
+// enough, or first), and of the tree the rows that their bits name, in any order.  So tiles
+// go from those that a row right behind these tokens' last sees to the last token.  The last
+// token's number, which bounds every row's place, stands for the place where only time
+// depends on it.
+template <bool TREE>
+__device__ __forceinline__ int first_place(const Seq &s, int row) { return TREE ? s.first() - 1 : s.first() + row; }
+template <bool TREE>
+__device__ __forceinline__ int last_place(const Seq &s, int row) { return TREE ? s.len - 1 : s.first() + row; }
+
+// A row's bits.
+struct TreeRow {
+    const uint32_t *bits;
+    int words;
+    __device__ __forceinline__ uint32_t word(int i) const { return (uint32_t)i < (uint32_t)words ? bits[i] : 0u; }
+    // of the sixteen rows from u on (u may be below 0)
+    __device__ __forceinline__ uint32_t sixteen(int u) const {
+        return __builtin_amdgcn_alignbit(word((u >> 5) + 1), word(u >> 5), u & 31) & 0xFFFFu;
+    }
+    __device__ __forceinline__ int count() const {
+        int n = 0;
+        for (int i = 0; i < words; ++i) n += __builtin_popcount(bits[i]);
+        return n;
+    }
+};
+__device__ __forceinline__ TreeRow tree_row(const AttnArgs &p, const Seq &s, int token) {
+    return {p.tree + (long long)(s.row0 + token) * p.tree_words, p.tree_words};
+}
+
+// What a row sees.
+template <bool TREE>
+struct Sight {
+    int pos, far, sinks;     // keys up to `far` are out of sight, but for the first `sinks`
+    __device__ __forceinline__ Sight(const AttnArgs &p, const Seq &s, int token, int at)
+        : pos(at), far(p.window > 0 ? at - p.window : -0x7FFFFFFF), sinks(p.sinks) {}
+    // key j, the e-th of a group
+    __device__ __forceinline__ bool operator()(int j, int) const { return (j <= pos) & ((j > far) | (j < sinks)); }
+    __device__ __forceinline__ void group(int) {}
+};
+template <>
+struct Sight<true> {
+    TreeRow row;
+    int first, far, sinks;
+    uint32_t bits = 0;
+    __device__ __forceinline__ Sight(const AttnArgs &p, const Seq &s, int token, int)
+        : row(tree_row(p, s, token)), first(s.first()), far(-0x7FFFFFFF), sinks(p.sinks) {
+        if (p.window > 0) far = first + row.count() - 1 - p.window;
+    }
+    __device__ __forceinline__ bool operator()(int j, int e) const {
+        return j < first ? (j > far) | (j < sinks) : (bits >> e & 1) != 0;
+    }
+    // before the keys of a group of sixteen: its first key
+    __device__ __forceinline__ void group(int j) { bits = row.sixteen(j - first); }
+};
 
 // The sequence with the rank-th most tokens, among up to 64 of them (equal ones in
 // their order); with more the order is as it comes.  All 64 lanes have to ask.
@@ -174,10 +234,15 @@ __device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
 template <int D>
 constexpr int kPart = D + 4;
 
-// Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
+// Few rows (awq_attention_split.h).  wide: eight waves to a workgroup (heads of 64).
+hipError_t launch_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
+hipError_t launch_tree_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
+
+// Rows by rows of 32 to a wave, for prompts (awq_attention_prompt.h).
 // row_tiles: of each sequence, or with `flat` of all of them, one after the other.
 int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat);
 int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
+hipError_t launch_tree_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
 
 }  // namespace awq

@@ -1,5 +1,5 @@
-// awq_attention for many rows (prompts, chunks of prompts): see
-// awq_attention.hip for the formula and the transposed products.
+// awq_attention, awq_tree_attention for many rows (prompts, chunks of prompts, large trees): see
+// awq_attention_split.h for the formula and the transposed products.
 //
 // A workgroup of four waves takes 128 rows (64 with heads of 256; row r of a kv head: token r / group,
 // head r % group) of one kv head and one sequence, 32 to a wave, and goes once
@@ -41,7 +41,9 @@
 // maximum that they refer to is moved only when a row exceeds it by 2^4, so the
 // largest is 2^15, and rescaling the outputs is rare after the first tiles.  (The difference
 // is compared: mx + 2^4 rounds up by half a step of 2^26 and more.)
-#include <algorithm>
+//
+// TREE (awq_tree_attention): the last tokens are a drafted tree's rows; see Sight.
+#pragma once
 
 #include "awq_attention.h"
 #include "awq_internal.h"
@@ -92,7 +94,7 @@ __device__ __forceinline__ void add_products(float16_t &o, uint4 codes, const ha
 // BIG: pages of at least a tile, so that a tile's page and scales are the same for
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
-template <typename T, int D, bool BIG>
+template <typename T, int D, bool BIG, bool TREE>
 __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {      // 0: flat
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     // the longest rows first
     for (int rt = row_tiles - 1 - tile; rt >= 0; rt -= tile_step) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
-        const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
+        const Tiles tiles = visible_tiles(p, first_place<TREE>(s, r0 / p.group), last_place<TREE>(s, r1 / p.group), s.len);
         // this workgroup's chunk of them
         const int every = tiles.count(), chunks = max(1, min(p.most, every / kLeastChunk));
         if (split >= chunks) continue;
@@ -158,10 +160,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         // the wave's rows, and the lane's
         const int w0 = min(r0 + row_wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
         const bool idle = r0 + row_wave * kWaveRows > r1;
-        const int lo = s.first() + w0 / p.group, hi = s.first() + w1 / p.group;
+        const int lo = first_place<TREE>(s, w0 / p.group), hi = last_place<TREE>(s, w1 / p.group);
         const int r = min(w0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
-        const int pos = s.first() + token;
+        Sight<TREE> sight(p, s, token, s.first() + token);
         const uint16_t *qrow = p.q + (long long)(s.row0 + token) * p.q_stride + head * D + 16 * hf;
         float up = p.scale < 0.0f ? -1.0f : 1.0f, down = fabsf(p.scale);
         if constexpr (!__is_same(T, half_t)) {
@@ -270,11 +272,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
                     const int jg = j0 + 32 * side + 16 * hf;
                     const int live = live_keys(j0, 2 * side + hf, ok);
-                    const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
+                    sight.group(jg);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int j = jg + e;
-                        const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
+                        const bool see = (e < live) & sight(jg + e, e);
                         acc[e] = see ? acc[e] : -__builtin_inff();
                     }
                 }
@@ -438,11 +439,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     for (int u = 0; u < 2; ++u) {
                         const int jg = j0 + 32 * u + 16 * hf;
                         const int live = live_keys(j0, 2 * u + hf, ok);
-                        const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
+                        sight.group(jg);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int j = jg + e;
-                            const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
+                            const bool see = (e < live) & sight(jg + e, e);
                             acc[u][e] = see ? acc[u][e] : -__builtin_inff();
                         }
                     }
@@ -604,43 +604,27 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool TREE>
 void launch_page(const AttnArgs &p, int grid, int tiles_per_seq, hipStream_t s) {
     if ((1 << p.c.log2_page) >= kTile)
-        prefill_kernel<T, D, true><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
+        prefill_kernel<T, D, true, TREE><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
     else
-        prefill_kernel<T, D, false><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
+        prefill_kernel<T, D, false, TREE><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
 }
 
-template <typename T>
+template <typename T, bool TREE>
 hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hipStream_t s) {
     switch (D) {
-    case 64: launch_page<T, 64>(p, grid, tiles_per_seq, s); break;
-    case 128: launch_page<T, 128>(p, grid, tiles_per_seq, s); break;
-    case 256: launch_page<T, 256>(p, grid, tiles_per_seq, s); break;
+    case 64: launch_page<T, 64, TREE>(p, grid, tiles_per_seq, s); break;
+    case 128: launch_page<T, 128, TREE>(p, grid, tiles_per_seq, s); break;
+    case 256: launch_page<T, 256, TREE>(p, grid, tiles_per_seq, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
-}  // namespace
-
-int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat) {
-    const int each = rows_of(head_dim);
-    if (flat)                                  // all that there can be
-        return (int)((long long)rows * group / each + std::min<long long>(seqs, (long long)rows * group / few));
-    const long long tiles = ((long long)max_q * group + each - 1) / each;
-    const long long pairs = (long long)kv_heads * seqs;                          // below 2^20
-    return (int)std::max<long long>(1, std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * pairs)));
-}
-
-// Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a CU).
-int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles) {
-    const long long groups = std::max<long long>(1, (long long)(flat ? 1 : seqs) * kv_heads * row_tiles);
-    return (int)std::max<long long>(1, std::min<long long>({512 / groups, key_tiles / kLeastChunk, kMostSplits}));
-}
-
-hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
+template <bool TREE>
+hipError_t launch_prompt_rows(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
     // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
     // keys meet in one XCD's cache.  Then the row tiles of a sequence, and the sequences, the
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
@@ -648,8 +632,9 @@ hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, 
     // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
     const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.most;
     if (grid == 0) return hipSuccess;
-    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, flat ? 0 : row_tiles, s)
-                : launch_dim<half_t>(p, head_dim, grid, flat ? 0 : row_tiles, s);
+    return bf16 ? launch_dim<bhalf_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s)
+                : launch_dim<half_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s);
 }
 
+}  // namespace
 }  // namespace awq

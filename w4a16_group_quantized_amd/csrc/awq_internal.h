@@ -68,16 +68,34 @@ hipError_t launch_scale_search(const uint16_t *x, int M, const uint16_t *w, int 
 // 8-bit paged key/value cache (KvView: awq_kv.h).  max_q, max_kv: the largest
 // row and token counts of a sequence, which size the grids.
 struct KvView;
+struct AxisMap;
 bool kv_head_dim_supported(int head_dim);
 hipError_t launch_kv_append(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             const uint16_t *k, long long k_stride, const uint16_t *v,
                             long long v_stride, uint16_t *q_out, int q_heads, const float *rope,
                             int rope_positions, int rot, bool adjacent, bool bf16, int max_q,
                             hipStream_t s);
+// The same with given rotary positions: [rows][axes], and the axis of each frequency.
+hipError_t launch_kv_append_at(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
+                               const uint16_t *k, long long k_stride, const uint16_t *v,
+                               long long v_stride, uint16_t *q_out, int q_heads, const float *rope,
+                               int rope_positions, int rot, bool adjacent, const int32_t *positions,
+                               int axes, const AxisMap &map, bool bf16, int max_q, hipStream_t s);
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
                            int max_kv, int window, int sinks);
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
-                            int max_q, int max_kv, void *workspace, hipStream_t s);
+                            int max_q, int max_kv, const uint32_t *tree, int tree_words, void *workspace, hipStream_t s);
+// Drafted trees: bits and positions of their rows (tree: the bits, [rows][tree_words], null for causal rows).
+hipError_t launch_tree_rows(const int32_t *parents, const KvView &c, int max_q, uint32_t *mask, int words,
+                            int32_t *positions, hipStream_t s);
+// Compaction, the next step's page table, and copies of pages.
+hipError_t launch_kv_keep(const KvView &c, int head_dim, const int32_t *kept, int width, const int32_t *counts,
+                          int32_t *lens_out, hipStream_t s);
+size_t kv_fork_workspace(int new_seqs, int width, int pages);
+hipError_t launch_kv_fork(const int32_t *from, const int32_t *grow, int new_seqs, const uint8_t *held, const KvView &c,
+                          int32_t *table_out, int32_t *lens_out, int32_t *copies, int32_t *missing, void *workspace,
+                          hipStream_t s);
+hipError_t launch_kv_copy(const int32_t *pairs, int n, const KvView &from, const KvView &to, int head_dim, hipStream_t s);
 
 }  // namespace awq

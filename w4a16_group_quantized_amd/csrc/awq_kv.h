@@ -20,6 +20,16 @@ struct KvView {
     int seqs, table_width, rows;
 };
 
+// The axis of each of up to 128 frequencies, two bits each.
+struct AxisMap {
+    uint64_t bits[4];
+    void set(int f, int axis) { bits[f / 32] |= (uint64_t)axis << (2 * (f % 32)); }
+    __device__ __forceinline__ uint8_t at(int f) const {
+        const uint64_t w = f < 64 ? (f < 32 ? bits[0] : bits[1]) : (f < 96 ? bits[2] : bits[3]);
+        return (uint8_t)(w >> (2 * (f % 32)) & 3);
+    }
+};
+
 // What a sequence has in a call: rows [row0, row0 + n) at positions
 // len - n + t.  Everything is clamped to the arrays that the host checked, so
 // no content of the device arrays leads out of them.
