@@ -6,18 +6,36 @@
 //   codes   c as it is where the scales are alike, else e4m3_rne(c * (old / new)): scales that are
 //           powers of two only shift the exponent, exact but for codes that become subnormal
 //
-// kept ascends, so a token never moves up: what is read for a place lies there or behind it.
-// One workgroup owns a (sequence, kv head) and takes the pages from the first, each in pieces
-// that are read, then (after a barrier) written: a piece's places are behind all that was written
-// before, and in front of all that is read later.  Nobody else writes these slabs or scales: no
-// atomics, and the same bits each time.  Bound: latency; a page after the other.
+// kept ascends, so a token never moves up: what a place takes lies there or behind it.  So if
+// places are taken from the first, what is read for some of them may be read before or after
+// earlier ones are written, and must be read before they are.
+//
+// few_kernel (few kept rows, a matter of latency): one workgroup owns a (sequence, kv head) and
+// takes the pages one after the other, each in pieces that are read, then (after a barrier)
+// written.
+//
+// many_kernel: keys, and each element's row of the values, do not meet, so waves share a sequence
+// and kv head by pieces of the elements, each through all of its tokens, with no wait for
+// another: 16 elements of the keys, or 4 rows of the values, byte by byte, 64 tokens to an
+// instruction, and all of a block of 512 tokens on the way before the first is written.  The scales
+// are what they share: only the codes move, and a second launch goes over the scales alone.
+//
+// Nobody else writes a sequence's slabs or scales: the same bits each time.
+// Bound: latency of a block (kept, page, scales, codes: four loads in a row), blocks one after the other.
+#include <algorithm>
+
 #include "awq_internal.h"
 #include "awq_kv.h"
 
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256, kMaxPage = 256, kAtOnce = 4;
+constexpr int kFewThreads = 256, kMaxPage = 256, kAtOnce = 4;
+constexpr int kThreads = 256;
+constexpr int kBlock = 512;                // tokens on the way: whole pages
+constexpr int kLeastPage = 16;
+constexpr int kKeyWidth = 16, kRows = 4;   // elements of a piece of the keys; rows of a piece of the values
+constexpr int kStays = -2;
 
 struct KeepArgs {
     KvView c;
@@ -35,10 +53,10 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
+__global__ void __launch_bounds__(kFewThreads) few_kernel(KeepArgs p) {
     constexpr int U = D / 16;                  // 16-byte pieces of a key
     __shared__ int m_s, id_s[kMaxPage], slot_s[kMaxPage];
-    __shared__ float fk_s[kMaxPage], fv_s[kMaxPage], red[2][kThreads / 64];
+    __shared__ float fk_s[kMaxPage], fv_s[kMaxPage], red[2][kFewThreads / 64];
     const KvView &c = p.c;
     const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
     const Seq s = load_seq(c, b);
@@ -49,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
     const int most = first < 0 ? 0 : min(max(p.counts[b], 0), min(s.n, p.width));
     if (tid == 0) m_s = most;
     __syncthreads();
-    for (int i = tid; i < most; i += kThreads) {
+    for (int i = tid; i < most; i += kFewThreads) {
         const int k = kept[i];
         if (k <= (i > 0 ? kept[i - 1] : -1) || k >= s.n) atomicMin(&m_s, i);
     }
@@ -105,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
         // tokens that stay
         if (held > 0 && ka != ks0) {
             const float f = ks0 / ka;
-            for (int i = tid; i < held * (D / 4); i += kThreads) {
+            for (int i = tid; i < held * (D / 4); i += kFewThreads) {
                 uint32_t *w = reinterpret_cast<uint32_t *>(kslab) + i;
                 *w = rescaled(*w, f);
             }
@@ -113,17 +131,17 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
         const int w0 = held >> 2, w1 = (held + count + 3) >> 2, words = w1 - w0;
         if (w0 > 0 && va != vs0) {
             const float f = vs0 / va;
-            for (int i = tid; i < w0 * D; i += kThreads) {
+            for (int i = tid; i < w0 * D; i += kFewThreads) {
                 uint32_t *w = reinterpret_cast<uint32_t *>(vslab + (i / w0) * P) + i % w0;
                 *w = rescaled(*w, f);
             }
         }
         // keys that come, token after token
-        for (int x0 = 0; x0 < count * U; x0 += kAtOnce * kThreads) {
+        for (int x0 = 0; x0 < count * U; x0 += kAtOnce * kFewThreads) {
             uint4 r[kAtOnce];
 #pragma unroll
             for (int n = 0; n < kAtOnce; ++n) {
-                const int x = x0 + n * kThreads + tid, t = held + x / U;
+                const int x = x0 + n * kFewThreads + tid, t = held + x / U;
                 if (x >= count * U) continue;
                 const int from = id_s[t];
                 r[n] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -136,16 +154,16 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
             __syncthreads();
 #pragma unroll
             for (int n = 0; n < kAtOnce; ++n) {
-                const int x = x0 + n * kThreads + tid;
+                const int x = x0 + n * kFewThreads + tid;
                 if (x < count * U) *reinterpret_cast<uint4 *>(kslab + (held + x / U) * D + 16 * (x % U)) = r[n];
             }
         }
         // values, element after element: four slots to a word
-        for (int x0 = 0; x0 < words * D; x0 += kAtOnce * kThreads) {
+        for (int x0 = 0; x0 < words * D; x0 += kAtOnce * kFewThreads) {
             uint32_t r[kAtOnce];
 #pragma unroll
             for (int n = 0; n < kAtOnce; ++n) {
-                const int x = x0 + n * kThreads + tid, d = x / words, w = w0 + x % words;
+                const int x = x0 + n * kFewThreads + tid, d = x / words, w = w0 + x % words;
                 if (x >= words * D) continue;
                 uint32_t now = held + count < 4 * w + 4 ? reinterpret_cast<const uint32_t *>(vslab + d * P)[w] : 0u;     // (slots behind stay)
 #pragma unroll
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
             __syncthreads();
 #pragma unroll
             for (int n = 0; n < kAtOnce; ++n) {
-                const int x = x0 + n * kThreads + tid;
+                const int x = x0 + n * kFewThreads + tid;
                 if (x < words * D) reinterpret_cast<uint32_t *>(vslab + (x / words) * P)[w0 + x % words] = r[n];
             }
         }
@@ -169,15 +187,243 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(KeepArgs p) {
     }
 }
 
+// Four rows' codes, one byte of each in a lane, as words of four lanes' bytes: lane 4 i + e gets
+// row e's word of the lanes 4 i .. 4 i + 3.
+__device__ __forceinline__ uint32_t words_of(const uint32_t (&r)[4]) {
+    const int at = threadIdx.x & 3;
+    uint32_t out = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        int x = (int)(r[e] << (8 * at));
+        x |= __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);       // lanes 1, 0, 3, 2
+        x |= __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);       // lanes 2, 3, 0, 1
+        out = at == e ? (uint32_t)x : out;
+    }
+    return out;
+}
+
+// SCALES: only these, and the lengths; otherwise only the codes, a piece to a wave: gridDim.y
+// workgroups share a sequence and kv head.
+template <int D, bool SCALES>
+__global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
+    constexpr int kWaves = kThreads / 64;
+    constexpr int kGroups = kBlock / 64, kEach = kBlock / kThreads, kPages = kBlock / kLeastPage;
+    // by place in the block: the page that its token comes from (-1: none, kStays: nothing is written),
+    // the slot there, what its codes are multiplied by
+    __shared__ int from[kBlock], slot[kBlock], to[kPages], limits[2];
+    __shared__ float fk[kBlock], fv[kBlock];
+    __shared__ uint32_t most[2][2][kPages];    // scales as bits (they are positive), of this block and the next
+    const KvView &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
+    const Seq s = load_seq(c, b);
+    const int lp = c.log2_page, P = 1 << lp, first = s.first();
+    const int32_t *kept = p.kept + (long long)b * p.width;
+    const int32_t *table = c.page_table + (long long)b * c.table_width;
+    // the kept rows: up to the first that is not behind the one before it, or is none; and from
+    // where on they are not in place
+    const int listed = first < 0 ? 0 : min(max(p.counts[b], 0), min(s.n, p.width));
+    if (tid < 2) limits[tid] = listed;
+    if (tid < 2 * kPages) most[0][tid / kPages][tid % kPages] = 0u;
+    __syncthreads();
+    int bad = listed, moved = listed;
+    for (int i0 = tid; i0 < listed; i0 += 8 * kThreads) {
+        int k[8], last[8];                     // (all on the way at once)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int i = min(i0 + n * kThreads, listed - 1);
+            k[n] = kept[i];
+            last[n] = kept[max(i - 1, 0)];
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int i = min(i0 + n * kThreads, listed - 1);
+            if (k[n] <= (i > 0 ? last[n] : -1) || k[n] >= s.n) bad = min(bad, i);
+            if (k[n] != i) moved = min(moved, i);
+        }
+    }
+    for (int k = 32; k > 0; k >>= 1) {
+        bad = min(bad, __shfl_xor(bad, k));
+        moved = min(moved, __shfl_xor(moved, k));
+    }
+    if (lane == 0) {
+        atomicMin(&limits[0], bad);
+        atomicMin(&limits[1], moved);
+    }
+    __syncthreads();
+    const int m = limits[0], end = first + m, begin = first + limits[1];
+    if (SCALES && h == 0 && tid == 0) p.lens_out[b] = first < 0 ? s.len : end;
+    if (begin >= end) return;
+    const long long slab = (long long)P * D;
+    const int start = begin >> lp << lp;
+
+    // A block's tokens, their pages and these pages' scales are asked for three, two and one block
+    // ahead: each is found by the one before.  (What is loaded is looked at when it is used, and
+    // loads have no conditions around them: either would be a wait.)
+    int tok1[kEach], tok2[kEach], tok3[kEach], id1[kEach], id2[kEach], own1, own2;
+    float ks1[kEach], vs1[kEach];
+    const auto ask_tokens = [&](int base, int (&row)[kEach]) {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) row[n] = kept[min(max(base + n * kThreads + tid - first, 0), m - 1)];
+    };
+    const auto token = [&](int base, int n, int row) {     // of a place; -1: it has none
+        const int place = base + n * kThreads + tid;
+        return place >= end ? -1 : place < first ? place : first + row;
+    };
+    const auto ask_pages = [&](int base, const int (&row)[kEach], int (&id)[kEach], int &own) {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) id[n] = table[max(token(base, n, row[n]), 0) >> lp];
+        own = table[min(base + (tid << lp), end - 1) >> lp];
+    };
+    const auto page = [&](int base, int n, int row, int id) { return token(base, n, row) >= 0 && id >= 0 && id < c.pages ? id : -1; };
+    const auto ask_scales = [&](int base, const int (&row)[kEach], const int (&id)[kEach], float (&ks)[kEach], float (&vs)[kEach]) {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) {
+            const long long at = (long long)max(page(base, n, row[n], id[n]), 0) * c.kv_heads + h;
+            ks[n] = c.k_scales[at];
+            vs[n] = c.v_scales[at];
+        }
+    };
+    ask_tokens(start, tok1);
+    ask_tokens(start + kBlock, tok2);
+    ask_tokens(start + 2 * kBlock, tok3);
+    ask_pages(start, tok1, id1, own1);
+    ask_pages(start + kBlock, tok2, id2, own2);
+    ask_scales(start, tok1, id1, ks1, vs1);
+    for (int base = start, odd = 0; base < end; base += kBlock, odd ^= 1) {
+        // the largest scales of each page's tokens
+        const int width = min(P, 64);
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) {
+            const int id = page(base, n, tok1[n], id1[n]);
+            float ka = id < 0 ? 0.0f : ks1[n], va = id < 0 ? 0.0f : vs1[n];
+            ks1[n] = ka;
+            vs1[n] = va;
+            id1[n] = id;
+#pragma unroll
+            for (int k = 32; k > 0; k >>= 1) {
+                const float a = __shfl_xor(ka, k), v = __shfl_xor(va, k);
+                ka = k < width ? fmaxf(ka, a) : ka;
+                va = k < width ? fmaxf(va, v) : va;
+            }
+            const int x = n * kThreads + tid;
+            if ((lane & (width - 1)) == 0) {
+                atomicMax(&most[odd][0][x >> lp], __builtin_bit_cast(uint32_t, ka));
+                atomicMax(&most[odd][1][x >> lp], __builtin_bit_cast(uint32_t, va));
+            }
+        }
+        if (tid < kBlock >> lp) to[tid] = base + (tid << lp) >= end || own1 < 0 || own1 >= c.pages ? -1 : own1;
+        __syncthreads();                       // (and every wave is done with the block before)
+        if (tid < 2 * kPages) most[odd ^ 1][tid / kPages][tid % kPages] = 0u;
+        if constexpr (!SCALES) {
+#pragma unroll
+            for (int n = 0; n < kEach; ++n) {
+                const int x = n * kThreads + tid, place = base + x, tok = token(base, n, tok1[n]);
+                const float ka = __builtin_bit_cast(float, most[odd][0][x >> lp]), va = __builtin_bit_cast(float, most[odd][1][x >> lp]);
+                const float a = ks1[n] == ka ? 1.0f : ks1[n] / ka, v = vs1[n] == va ? 1.0f : vs1[n] / va;
+                const bool stays = tok < 0 || to[x >> lp] < 0 || (tok == place && a == 1.0f && v == 1.0f);
+                from[x] = stays ? kStays : id1[n];
+                slot[x] = tok & (P - 1);
+                fk[x] = a;
+                fv[x] = v;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) {
+            tok1[n] = tok2[n];
+            tok2[n] = tok3[n];
+            id1[n] = id2[n];
+        }
+        own1 = own2;
+        ask_scales(base + kBlock, tok1, id1, ks1, vs1);
+        ask_pages(base + 2 * kBlock, tok2, id2, own2);
+        ask_tokens(base + 3 * kBlock, tok3);
+        if constexpr (SCALES) {
+            // (later blocks' are of later pages)
+            if (tid < kBlock >> lp && to[tid] >= 0 && most[odd][0][tid] != 0u) {
+                c.k_scales[(long long)to[tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][0][tid]);
+                c.v_scales[(long long)to[tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][1][tid]);
+            }
+            __syncthreads();
+            continue;
+        }
+        const int piece = blockIdx.y * kWaves + wave;
+        if (piece < D / kKeyWidth) {
+            const int at = piece * kKeyWidth;
+            uint4 r[kGroups];
+#pragma unroll
+            for (int n = 0; n < kGroups; ++n) {
+                const int x = 64 * n + lane;
+                r[n] = *reinterpret_cast<const uint4 *>(c.k + ((long long)max(from[x], 0) * c.kv_heads + h) * slab + slot[x] * D + at);
+            }
+#pragma unroll
+            for (int n = 0; n < kGroups; ++n) {
+                const int x = 64 * n + lane, id = from[x];
+                if (id != kStays) {
+                    const float f = fk[x];
+                    const uint32_t none = 0x7F7F7F7Fu;
+                    *reinterpret_cast<uint4 *>(c.k + ((long long)to[x >> lp] * c.kv_heads + h) * slab + (x & (P - 1)) * D + at) =
+                        id < 0 ? make_uint4(none, none, none, none)
+                               : make_uint4(rescaled(r[n].x, f), rescaled(r[n].y, f), rescaled(r[n].z, f), rescaled(r[n].w, f));
+                }
+            }
+        } else {
+            const int d = (piece - D / kKeyWidth) * kRows;
+            uint32_t r[kGroups][kRows];
+#pragma unroll
+            for (int n = 0; n < kGroups; ++n) {
+                const int x = 64 * n + lane;
+                const uint8_t *v = c.v + ((long long)max(from[x], 0) * c.kv_heads + h) * slab + d * P + slot[x];
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) r[n][e] = v[e * P];
+            }
+#pragma unroll
+            for (int n = 0; n < kGroups; ++n) {
+                const int x = 64 * n + lane, id = from[x];
+                const bool put = id != kStays;
+                const float f = fv[x];
+                uint8_t *v = c.v + ((long long)to[x >> lp] * c.kv_heads + h) * slab + d * P + (x & (P - 1));
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) r[n][e] = id < 0 ? 0u : rescaled(r[n][e], f) & 0xFFu;
+                // four places to a word, where all four are written (pages are of whole words)
+                const uint32_t four = (uint32_t)(__ballot(put) >> (lane & ~3)) & 15u;
+                const uint32_t w = words_of(r[n]);
+                if (four == 15u) {
+                    *reinterpret_cast<uint32_t *>(v - (lane & 3) + (lane & 3) * P) = w;
+                } else if (put) {
+#pragma unroll
+                    for (int e = 0; e < kRows; ++e) v[e * P] = (uint8_t)r[n][e];
+                }
+            }
+        }
+    }
+}
+
+// Kept rows of a sequence from which many waves share it.
+constexpr int kMany = 64;
+
+template <int D>
+void launch(const KeepArgs &p, hipStream_t s) {
+    if (p.width <= kMany) {
+        few_kernel<D><<<dim3(p.c.kv_heads, p.c.seqs), kFewThreads, 0, s>>>(p);
+        return;
+    }
+    constexpr int pieces = D / kKeyWidth + D / kRows;
+    const int pairs = p.c.kv_heads * p.c.seqs;
+    static_assert(pieces % (kThreads / 64) == 0, "a piece to a wave");
+    many_kernel<D, false><<<dim3(pairs, pieces / (kThreads / 64)), kThreads, 0, s>>>(p);
+    many_kernel<D, true><<<pairs, kThreads, 0, s>>>(p);
+}
+
 }  // namespace
 
 hipError_t launch_kv_keep(const KvView &c, int head_dim, const int32_t *kept, int width, const int32_t *counts, int32_t *lens_out, hipStream_t s) {
     const KeepArgs p{c, kept, counts, lens_out, width};
-    const dim3 grid(c.kv_heads, c.seqs);
     switch (head_dim) {
-    case 64: keep_kernel<64><<<grid, kThreads, 0, s>>>(p); break;
-    case 128: keep_kernel<128><<<grid, kThreads, 0, s>>>(p); break;
-    case 256: keep_kernel<256><<<grid, kThreads, 0, s>>>(p); break;
+    case 64: launch<64>(p, s); break;
+    case 128: launch<128>(p, s); break;
+    case 256: launch<256>(p, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
