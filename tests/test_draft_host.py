@@ -128,17 +128,20 @@ def test_keep_refusals(kw, want):
     (dict(from_=None), INVALID), (dict(grow=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
     (dict(copies=None), INVALID), (dict(missing=None), INVALID), (dict(table=FAKE), INVALID), (dict(lens=FAKE), INVALID),
     (dict(n=-1), INVALID), (dict(n=65536), SHAPE), (dict(n=65535, b=dict(width=1 << 16)), SHAPE), (dict(from_=MISALIGNED), ALIGN),
-    (dict(held=MISALIGNED), ALIGN), (dict(copies=MISALIGNED), ALIGN), (dict(ws=None), WS), (dict(ws=MISALIGNED), WS),
-    (dict(nbytes=0), WS),
+    (dict(held=MISALIGNED), ALIGN), (dict(copies=MISALIGNED), ALIGN),
 ])
 def test_fork_refusals(kw, want):
     assert fork(**{k: batch(**v) if k == "b" else v for k, v in kw.items()}) == want
 
 
 def test_fork_workspace():
-    lib, c, b = binding.load(), cache(), batch()
+    """A small table takes none, a large one a few words for each entry and bits for each page."""
+    lib, c, b = binding.load(), cache(), batch(width=1 << 15)
     need = lib.awq_kv_fork_workspace_bytes(3, c, b)
-    assert need > 0 and fork(nbytes=need - 1) == WS
+    assert need > 0 and fork(b=b, nbytes=need - 1) == WS
+    assert fork(b=b, ws=None) == WS and fork(b=b, ws=MISALIGNED) == WS
+    assert lib.awq_kv_fork_workspace_bytes(3, c, batch()) == 0
+    assert lib.awq_kv_fork_workspace_bytes(3, cache(pages=1 << 20), batch()) > 0 < lib.awq_kv_fork_workspace_bytes(2000, c, batch())
     assert lib.awq_kv_fork_workspace_bytes(0, c, b) == 0 and lib.awq_kv_fork_workspace_bytes(3, None, b) == 0
 
 

@@ -278,8 +278,9 @@ def test_binding_refusals():
         binding.kv_fork(two, two, cache, batch, held=torch.zeros(3, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="table must be"):
         binding.kv_fork(two, two, cache, batch, out=(two, two, kept, two))
+    many = torch.zeros(2000, dtype=torch.int32, device=DEV)
     with pytest.raises(binding.AwqError) as e:
-        binding.kv_fork(two, two, cache, batch, workspace=torch.empty(4, dtype=torch.uint8, device=DEV))
+        binding.kv_fork(many, many, cache, batch, workspace=torch.empty(4, dtype=torch.uint8, device=DEV))
     assert e.value.status == binding.AWQ_ERROR_WORKSPACE
     with pytest.raises(ValueError, match="pairs must be"):
         binding.kv_copy(two, cache)

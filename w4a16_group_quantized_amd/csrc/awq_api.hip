@@ -539,8 +539,8 @@ awq_status awq_kv_fork(const int32_t *from, const int32_t *grow, int32_t new_seq
     if (!aligned16(from) || !aligned16(grow) || !aligned16(held) || !aligned16(table_out) || !aligned16(lens_out) ||
         !aligned16(copies) || !aligned16(missing))
         return AWQ_ERROR_ALIGNMENT;
-    if (workspace == nullptr || !aligned16(workspace) ||
-        workspace_bytes < awq::kv_fork_workspace(new_seqs, batch->table_width, cache->pages))
+    const size_t need = awq::kv_fork_workspace(new_seqs, batch->table_width, cache->pages);
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return AWQ_ERROR_WORKSPACE;
     return done(stream, awq::launch_kv_fork(from, grow, new_seqs, held, kv_view(cache, batch), table_out, lens_out,
                                             copies, missing, workspace, as_stream(stream)));
