@@ -31,7 +31,7 @@ def check(t, bits, words=None, scale=None, window=0, sinks=0, max_q=None, max_kv
     words = max(1, -(-max([0, *t.new]) // 32)) if words is None else words
     mask = dc.mask_of(bits + [0] * (q.shape[0] - len(bits)), words).to(DEV)
     out = torch.full(q.shape, 7.0, dtype=t.dtype, device=DEV)
-    need = binding.attention_workspace_bytes(q.shape[0], t.q_heads, cache, batch, window, sinks)
+    need = binding.tree_attention_workspace_bytes(q.shape[0], t.q_heads, cache, batch, window, sinks)
     work = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device=DEV)           # NaN throughout
     got = binding.tree_attention(q, cache, batch, mask, scale=scale, window=window, sinks=sinks, out=out, workspace=work)
     torch.cuda.synchronize()

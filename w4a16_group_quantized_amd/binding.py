@@ -766,7 +766,7 @@ def _attention(fn, extra, q, cache, batch, scale, window, sinks, out, stream, wo
     op = _dev(out, q.dtype, "out")
     lib = load()
     if workspace is None:
-        nbytes = lib.awq_attention_workspace_bytes(heads, window, sinks, c, b)
+        nbytes = getattr(lib, fn + "_workspace_bytes")(heads, window, sinks, c, b)
         if nbytes:
             workspace = _new(nbytes, torch.uint8, q.device, stream)
     wp, wn = None, 0
@@ -819,6 +819,11 @@ def tree_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask: torch.
         raise ValueError(f"mask must be [{q.shape[0]}][words], got {list(mask.shape)}")
     extra = (_kv_ints(mask, cache._device, "mask"), mask.shape[1])
     return _attention("awq_tree_attention", extra, q, cache, batch, scale, window, sinks, out, stream, workspace)
+
+
+def tree_attention_workspace_bytes(rows: int, q_heads: int, cache: KvCache, batch: KvBatch, window: int = 0,
+                                   sinks: int = 0) -> int:
+    return load().awq_tree_attention_workspace_bytes(q_heads, window, sinks, cache._view(), batch._c(rows))
 
 
 def kv_keep(kept: torch.Tensor, counts: torch.Tensor, cache: KvCache, batch: KvBatch,

@@ -428,13 +428,18 @@ awq_status awq_kv_append_at(const uint16_t *q, int32_t q_stride, const uint16_t 
                                                  type == AWQ_TYPE_BF16, grid_rows(batch), as_stream(stream)));
 }
 
-size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
-                                     const awq_kv_cache *cache, const awq_kv_batch *batch) {
+static size_t attention_workspace(int32_t q_heads, int32_t window, int32_t sinks, const awq_kv_cache *cache,
+                                  const awq_kv_batch *batch, bool tree) {
     if (check_kv(cache, batch) != AWQ_SUCCESS || q_heads <= 0 || q_heads % cache->kv_heads || window < 0 ||
         sinks < 0 || batch->seqs == 0 || batch->rows == 0)
         return 0;
     return awq::attention_workspace(batch->seqs, batch->rows, q_heads, cache->kv_heads, cache->head_dim,
-                                    grid_rows(batch), grid_keys(cache, batch), window, sinks);
+                                    grid_rows(batch), grid_keys(cache, batch), window, sinks, tree);
+}
+
+size_t awq_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
+                                     const awq_kv_cache *cache, const awq_kv_batch *batch) {
+    return attention_workspace(q_heads, window, sinks, cache, batch, false);
 }
 
 // Both attentions; tree: whether the rows' bits are asked for.
@@ -454,7 +459,7 @@ static awq_status attention(const uint16_t *q, int32_t q_stride, uint16_t *out, 
     if (st == AWQ_SUCCESS && tree && (long long)batch->rows * mask_words > kMaxElems) st = AWQ_ERROR_SHAPE;
     if (st == AWQ_SUCCESS && (!aligned16(out) || (tree && !aligned16(mask)))) st = AWQ_ERROR_ALIGNMENT;
     if (st != AWQ_SUCCESS) return st;
-    const size_t need = awq_attention_workspace_bytes(q_heads, window, sinks, cache, batch);
+    const size_t need = attention_workspace(q_heads, window, sinks, cache, batch, tree);
     if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return AWQ_ERROR_WORKSPACE;
     return done(stream, awq::launch_attention(kv_view(cache, batch), cache->head_dim, q, q_stride, out,
@@ -491,7 +496,7 @@ awq_status awq_tree_rows(const int32_t *parents, uint32_t *mask, int32_t mask_wo
 
 size_t awq_tree_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
                                           const awq_kv_cache *cache, const awq_kv_batch *batch) {
-    return awq_attention_workspace_bytes(q_heads, window, sinks, cache, batch);
+    return attention_workspace(q_heads, window, sinks, cache, batch, true);
 }
 
 awq_status awq_tree_attention(const uint16_t *q, int32_t q_stride, uint16_t *out, int32_t q_heads,

@@ -60,25 +60,6 @@ __device__ __forceinline__ int first_place(const Seq &s, int row) { return TREE 
 template <bool TREE>
 __device__ __forceinline__ int last_place(const Seq &s, int row) { return TREE ? s.len - 1 : s.first() + row; }
 
-// A row's bits.
-struct TreeRow {
-    const uint32_t *bits;
-    int words;
-    __device__ __forceinline__ uint32_t word(int i) const { return (uint32_t)i < (uint32_t)words ? bits[i] : 0u; }
-    // of the sixteen rows from u on (u may be below 0)
-    __device__ __forceinline__ uint32_t sixteen(int u) const {
-        return __builtin_amdgcn_alignbit(word((u >> 5) + 1), word(u >> 5), u & 31) & 0xFFFFu;
-    }
-    __device__ __forceinline__ int count() const {
-        int n = 0;
-        for (int i = 0; i < words; ++i) n += __builtin_popcount(bits[i]);
-        return n;
-    }
-};
-__device__ __forceinline__ TreeRow tree_row(const AttnArgs &p, const Seq &s, int token) {
-    return {p.tree + (long long)(s.row0 + token) * p.tree_words, p.tree_words};
-}
-
 // What a row sees.
 template <bool TREE>
 struct Sight {
@@ -91,18 +72,28 @@ struct Sight {
 };
 template <>
 struct Sight<true> {
-    TreeRow row;
-    int first, far, sinks;
+    const AttnArgs &p;
+    int row, first, far;
     uint32_t bits = 0;
-    __device__ __forceinline__ Sight(const AttnArgs &p, const Seq &s, int token, int)
-        : row(tree_row(p, s, token)), first(s.first()), far(-0x7FFFFFFF), sinks(p.sinks) {
-        if (p.window > 0) far = first + row.count() - 1 - p.window;
+    __device__ __forceinline__ Sight(const AttnArgs &args, const Seq &s, int token, int)
+        : p(args), row(s.row0 + token), first(s.first()), far(-0x7FFFFFFF) {
+        if (p.window > 0) {
+            far = first - 1 - p.window;
+            for (int i = 0; i < p.tree_words; ++i) far += __builtin_popcount(word(i));
+        }
+    }
+    __device__ __forceinline__ uint32_t word(int i) const {
+        return (uint32_t)i < (uint32_t)p.tree_words ? p.tree[(long long)row * p.tree_words + i] : 0u;
     }
     __device__ __forceinline__ bool operator()(int j, int e) const {
-        return j < first ? (j > far) | (j < sinks) : (bits >> e & 1) != 0;
+        return j < first ? (j > far) | (j < p.sinks) : (bits >> e & 1) != 0;
     }
-    // before the keys of a group of sixteen: its first key
-    __device__ __forceinline__ void group(int j) { bits = row.sixteen(j - first); }
+    // before the keys of a group of sixteen, from its first key on: their rows' bits (those of
+    // tokens before the tree have none)
+    __device__ __forceinline__ void group(int j) {
+        const int u = j - first;
+        bits = __builtin_amdgcn_alignbit(word((u >> 5) + 1), word(u >> 5), u & 31) & 0xFFFFu;
+    }
 };
 
 // The sequence with the rank-th most tokens, among up to 64 of them (equal ones in
@@ -242,6 +233,11 @@ hipError_t launch_tree_attention_split(const AttnArgs &p, int head_dim, bool bf1
 // row_tiles: of each sequence, or with `flat` of all of them, one after the other.
 int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat);
 int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
+// Drafted trees there: workgroups that share a kv head, and chunks that a row tile has room for.
+struct TreePlan {
+    int shares, room;
+};
+TreePlan tree_plan(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
 hipError_t launch_tree_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
 

@@ -78,6 +78,58 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs p) {
     }
 }
 
+// The same where a row has few chunks: D / 4 lanes to a row and head, all of its chunks on the way
+// at once, no LDS, and the same bits (the sums in combine_kernel's order).  1024 rows of 32 heads
+// of 128 in up to three chunks: 34 -> 12 us.
+constexpr int kFewChunks = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(256) combine_few_kernel(AttnArgs p) {
+#pragma clang fp contract(off)   // (weights are rounded before they are summed up)
+    constexpr int kLanes = D / 4, kParts = 256 / kLanes < kFewChunks ? 256 / kLanes : kFewChunks;
+    const KvView &c = p.c;
+    const int row0 = min(max(c.q_starts[0], 0), c.rows), row1 = min(max(c.q_starts[c.seqs], 0), c.rows);
+    const int i = row0 * p.q_heads + (int)(blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes), lane = threadIdx.x % kLanes;
+    if (i >= row1 * p.q_heads) return;
+    const float *src = p.part + (long long)i * p.splits * kPart<D>;
+    const int n = min((int)src[D + 2], p.splits);
+    if (n <= 1) return;                        // the one chunk has written its outputs
+    float own[kFewChunks], l[kFewChunks];
+    float4_t v[kFewChunks];
+#pragma unroll
+    for (int k = 0; k < kFewChunks; ++k) {     // (behind the last the last again)
+        const float *from = src + min(k, n - 1) * kPart<D>;
+        own[k] = from[D];
+        l[k] = from[D + 1];
+        v[k] = *reinterpret_cast<const float4_t *>(from + 4 * lane);
+    }
+    float mx = kEmpty;
+#pragma unroll
+    for (int k = 0; k < kFewChunks; ++k) mx = fmaxf(mx, own[k]);
+#pragma unroll
+    for (int k = 0; k < kFewChunks; ++k) l[k] = k < n ? l[k] * __builtin_amdgcn_exp2f(own[k] - mx) : 0.0f;
+    const float sum = ((l[0] + l[4]) + (l[2] + l[6])) + ((l[1] + l[5]) + (l[3] + l[7]));
+    const float inv = sum > 0.0f || !(sum == sum) ? 1.0f / sum : 0.0f;
+    float4_t part[kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) part[k] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kFewChunks; ++k) {
+        const float w = l[k] * inv;
+        if (k < n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[k % kParts][e] = __builtin_fmaf(w, v[k][e], part[k % kParts][e]);
+        }
+    }
+    float4_t o = part[0];
+#pragma unroll
+    for (int k = 1; k < kParts; ++k) o += part[k];
+    if (kParts < 256 / kLanes) o += float4_t{0.0f, 0.0f, 0.0f, 0.0f};      // (of -0 this makes 0, as there)
+    uint2 y;
+    y.x = (uint32_t)from_float<T>(o[0]) | ((uint32_t)from_float<T>(o[1]) << 16);
+    y.y = (uint32_t)from_float<T>(o[2]) | ((uint32_t)from_float<T>(o[3]) << 16);
+    *reinterpret_cast<uint2 *>(p.out + (long long)i * D + 4 * lane) = y;
+}
+
 // Rows of a sequence and kv head from which the prompt kernel takes a call, by the width of
 // heads, the pairs of sequence and kv head, and the tiles of keys of all pairs.  The split kernel
 // reads keys and values again for every sixteen rows; the prompt kernel is slower to start, and
@@ -137,10 +189,11 @@ struct Plan {
     bool prompt, mixed;      // whether the prompt kernel is needed, and both are
     bool wide;               // eight waves to a workgroup
     int few, prompt_tiles, prompt_splits;
+    int shares;              // of a tree's rows in the prompt kernel (TreeShare)
     int row_tiles, splits, target;
     int room() const { return std::max(splits, prompt_splits); }
 };
-Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks) {
+Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int max_kv, int window, int sinks, bool tree) {
     Plan pl;
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
@@ -149,11 +202,16 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
-    pl.splits = pl.prompt_splits = 1;
+    pl.splits = pl.prompt_splits = pl.shares = 1;
     pl.wide = false;
     if (pl.prompt) {
         pl.prompt_tiles = prefill_row_tiles(seqs, rows, kv_heads, group, head_dim, max_q, pl.few, pl.mixed);
         pl.prompt_splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
+        if (tree) {
+            const TreePlan t = tree_plan(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
+            pl.shares = t.shares;
+            pl.prompt_splits = t.room;
+        }
         if (!pl.mixed) return pl;
     }
     // (the kernel steps on where the grid is cut)
@@ -186,13 +244,20 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     return pl;
 }
 
+template <typename T, int D>
+void combine_dim(const AttnArgs &p, hipStream_t s) {
+    const long long items = (long long)p.c.rows * p.q_heads;
+    if (p.splits <= kFewChunks)
+        combine_few_kernel<T, D><<<(int)((items + 1024 / D - 1) / (1024 / D)), 256, 0, s>>>(p);
+    else
+        combine_kernel<T, D><<<(int)std::min<long long>(items, kJoinGroups), 256, 0, s>>>(p);
+}
 template <typename T>
 hipError_t combine(const AttnArgs &p, int D, hipStream_t s) {
-    const int grid = (int)std::min<long long>((long long)p.c.rows * p.q_heads, kJoinGroups);
     switch (D) {
-    case 64: combine_kernel<T, 64><<<grid, 256, 0, s>>>(p); break;
-    case 128: combine_kernel<T, 128><<<grid, 256, 0, s>>>(p); break;
-    case 256: combine_kernel<T, 256><<<grid, 256, 0, s>>>(p); break;
+    case 64: combine_dim<T, 64>(p, s); break;
+    case 128: combine_dim<T, 128>(p, s); break;
+    case 256: combine_dim<T, 256>(p, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -203,7 +268,7 @@ hipError_t launch(AttnArgs p, int D, const Plan &pl, bool bf16, hipStream_t s) {
     const bool tree = p.tree != nullptr;
     if (pl.prompt) {
         p.few = pl.mixed ? pl.few : 0;
-        p.most = pl.prompt_splits;
+        p.most = tree ? pl.shares : pl.prompt_splits;
         e = (tree ? launch_tree_attention_prefill : launch_attention_prefill)(p, D, bf16, pl.prompt_tiles, pl.mixed, s);
         if (e != hipSuccess) return e;
     }
@@ -219,8 +284,8 @@ hipError_t launch(AttnArgs p, int D, const Plan &pl, bool bf16, hipStream_t s) {
 }  // namespace
 
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
-                           int max_kv, int window, int sinks) {
-    const Plan pl = plan(seqs, rows, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks);
+                           int max_kv, int window, int sinks, bool tree) {
+    const Plan pl = plan(seqs, rows, kv_heads, q_heads / kv_heads, head_dim, max_q, max_kv, window, sinks, tree);
     if (pl.room() == 1) return 0;
     return (size_t)rows * q_heads * pl.room() * (head_dim + 4) * sizeof(float);
 }
@@ -228,7 +293,7 @@ size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int he
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
                             int max_q, int max_kv, const uint32_t *tree, int tree_words, void *workspace, hipStream_t s) {
-    const Plan pl = plan(c.seqs, c.rows, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks);
+    const Plan pl = plan(c.seqs, c.rows, c.kv_heads, q_heads / c.kv_heads, head_dim, max_q, max_kv, window, sinks, tree != nullptr);
     AttnArgs p{c, q, q_stride, out, pl.room() > 1 ? (float *)workspace : nullptr, q_heads,
                q_heads / c.kv_heads, scale * kLog2e, std::min(window, kWidest), sinks, 1, pl.target, pl.room(), 0,
                tree, tree_words};

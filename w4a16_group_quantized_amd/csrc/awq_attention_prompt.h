@@ -56,6 +56,8 @@ constexpr int kWaveRows = 32, kWaves = 4;
 // keys, one sequence: 47 / 43 / 140 us at 16 tiles, 26 / 32 / 137 at 6, 24 / 32 / 140 at 4; 16
 // sequences of 32 rows over 4k: 90 / 84 / 85.
 constexpr int kLeastChunk = 6, kMostSplits = 32;
+constexpr int kLeastShare = 8;             // units of a workgroup (trees)
+constexpr int kTreeSlots = 512, kManyTreeTiles = 4 * kTreeSlots;
 constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
 
 // Heads of 256 elements: two waves share 32 rows.  Elsewhere a wave has 32 rows to itself.
@@ -91,6 +93,112 @@ __device__ __forceinline__ void add_products(float16_t &o, uint4 codes, const ha
     o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[3], o, 0, 0, 0);
 }
 
+// Drafted trees: how workgroups share the work of a kv head.  All rows of a tree see the same
+// tiles of keys, so the work is a line of units, a row tile's tile of keys each: row tiles one after
+// the other, with all of their tiles.  Workgroup k takes the units [k each, (k + 1) each), so
+// that all take the same time, whatever the lengths of the sequences: a part of a row tile's keys, or all
+// of some, or both.  A border less than kLeastChunk tiles from the border of a row tile moves there.
+struct TreeShare {
+    int seq, row_tile, start, count, chunk, chunks;    // a piece: tiles start .. start + count - 1
+    int number;
+    long long at, end, each;
+
+    // A row tile of a line of them: its sequence, number there, first unit and tiles.
+    struct RowTile {
+        long long first;
+        int seq, number, tiles;
+    };
+    // What a lane has of the 64 sequences from `from` on: the units of its sequence and of those up
+    // to it, and the sequence's tiles; and all of them.
+    struct Lane {
+        long long own, upto, all;
+        int from, tiles;
+    };
+    static __device__ __forceinline__ long long scalar(long long x) {
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+        return (long long)((uint64_t)hi << 32 | lo);
+    }
+    static __device__ __forceinline__ Lane load(const AttnArgs &p, int rows, int from) {
+        Lane l{0, 0, 0, from, 0};
+        const int lane = threadIdx.x & 63, b = from + lane;
+        if (b < p.c.seqs) {
+            const Seq s = load_seq(p.c, b);
+            const int total = s.n * p.group;
+            if (total > 0 && total >= p.few) {
+                l.tiles = max(1, visible_tiles(p, first_place<true>(s, 0), s.len - 1, s.len).count());
+                l.own = (long long)l.tiles * ((total + rows - 1) / rows);
+            }
+        }
+        l.upto = l.own;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+            const long long other = __shfl_up(l.upto, k);
+            l.upto += lane >= k ? other : 0;
+        }
+        l.all = scalar(__shfl(l.upto, 63));
+        return l;
+    }
+    // The row tile that unit u (there is one) is in; l: of the sequences from 0 on.
+    static __device__ __forceinline__ RowTile find(const AttnArgs &p, int rows, Lane l, long long u) {
+        long long before = 0;
+        while (u >= before + l.all && l.from + 64 < p.c.seqs) {
+            before += l.all;
+            l = load(p, rows, l.from + 64);
+        }
+        const int at = (int)__builtin_ctzll(__ballot(before + l.upto > u));
+        RowTile r;
+        r.tiles = __builtin_amdgcn_readlane(l.tiles, at);
+        r.seq = l.from + at;
+        r.first = before + scalar(__shfl(l.upto - l.own, at));
+        const long long in = u - r.first;
+        r.number = __builtin_amdgcn_readfirstlane(in >> 32 ? (int)(in / r.tiles) : (int)((uint32_t)in / (uint32_t)r.tiles));
+        r.first = scalar(r.first + (long long)r.number * r.tiles);
+        return r;
+    }
+    static __device__ __forceinline__ int least(const AttnArgs &p, int tiles) { return p.splits > 1 ? kLeastChunk : tiles; }
+    static __device__ __forceinline__ long long border(const AttnArgs &p, int rows, const Lane &l, long long u, long long units) {
+        if (u >= units) return units;
+        const RowTile r = find(p, rows, l, u);
+        const int far = least(p, r.tiles);
+        return u - r.first < far ? r.first : r.first + r.tiles - u < far ? r.first + r.tiles : u;
+    }
+    __device__ __forceinline__ void begin(const AttnArgs &p, int rows, int k) {
+        // all units, and the most tiles of a row tile, which has room for p.splits chunks
+        const Lane l = load(p, rows, 0);
+        long long units = l.all;
+        int most = max(1, l.tiles);
+        for (int from = 64; from < p.c.seqs; from += 64) {
+            const Lane other = load(p, rows, from);
+            units += other.all;
+            most = max(most, other.tiles);
+        }
+#pragma unroll
+        for (int i = 32; i > 0; i >>= 1) most = max(most, __shfl_xor(most, i));
+        each = max((units + p.most - 1) / p.most, (long long)kLeastShare);
+        if (p.splits > 1) each = max(each, (long long)(most / (p.splits - 1) + 1));
+        each = scalar(each);
+        number = k;
+        at = scalar(border(p, rows, l, k * each, units));
+        end = scalar(border(p, rows, l, (k + 1) * each, units));
+    }
+    __device__ __forceinline__ bool next(const AttnArgs &p, int rows) {
+        if (at >= end) return false;
+        const RowTile r = find(p, rows, load(p, rows, 0), at);
+        const long long stop = min(end, r.first + r.tiles);
+        seq = r.seq;
+        row_tile = r.number;
+        start = __builtin_amdgcn_readfirstlane((int)(at - r.first));
+        count = __builtin_amdgcn_readfirstlane((int)(stop - at));
+        // borders inside of the row tile: of workgroups lo .. hi
+        const int far = least(p, r.tiles);
+        const long long lo = (r.first + far + each - 1) / each, hi = (r.first + r.tiles - far) / each;
+        chunks = __builtin_amdgcn_readfirstlane((int)max(hi - lo + 1, 0ll) + 1);
+        chunk = __builtin_amdgcn_readfirstlane(start == 0 ? 0 : (int)(number - lo) + 1);
+        at = stop;
+        return true;
+    }
+};
+
 // BIG: pages of at least a tile, so that a tile's page and scales are the same for
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
@@ -111,10 +219,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     const int m = lane & 31, hf = lane >> 5;
     // with pairs: which 32 keys of a tile, and which half of the outputs, are the wave's
     const int side = kPairs ? wave & 1 : 0, row_wave = kPairs ? wave >> 1 : wave;
-    const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.most;
-    const int slot = blockIdx.x / (c.kv_heads * p.most);
-    int b, tile, tile_step = tiles_per_seq;
-    if (tiles_per_seq > 0) {
+    const int h = blockIdx.x % c.kv_heads;
+    int split = TREE ? 0 : blockIdx.x / c.kv_heads % p.most;
+    const int slot = TREE ? 0 : blockIdx.x / (c.kv_heads * p.most);
+    int b = 0, tile = 0, tile_step = tiles_per_seq;
+    if (TREE) {
+        tile_step = 0;
+    } else if (tiles_per_seq > 0) {
         b = seq_of_rank(c, slot / tiles_per_seq);
         tile = slot % tiles_per_seq;
     } else {
@@ -126,11 +237,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         tile = at.y;
         tile_step = 1 << 30;
     }
-    const Seq s = load_seq(c, b);
+    Seq s = TREE ? Seq{0, 0, 0} : load_seq(c, b);
     const int P = 1 << c.log2_page;
-    const int total = s.n * p.group;
+    int total = s.n * p.group;
     const int row_tiles = (total + kRows - 1) / kRows;
     const int32_t *table = c.page_table + (long long)b * c.table_width;
+    TreeShare share;
+    if constexpr (TREE) share.begin(p, kRows, blockIdx.x / c.kv_heads);
     const int gv = (lane & 3) ^ ((lane >> 3) & 3);         // sixteen-key group whose values this lane loads
     const long long slab = (long long)P * D;
 
@@ -149,14 +262,30 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     }
 
     // the longest rows first
-    for (int rt = row_tiles - 1 - tile; rt >= 0; rt -= tile_step) {
+    for (int rt = row_tiles - 1 - tile; TREE ? share.next(p, kRows) : rt >= 0; rt -= tile_step) {
+        if constexpr (TREE) {
+            b = share.seq;
+            rt = share.row_tile;
+            s = load_seq(c, b);
+            total = s.n * p.group;
+            table = c.page_table + (long long)b * c.table_width;
+        }
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
         const Tiles tiles = visible_tiles(p, first_place<TREE>(s, r0 / p.group), last_place<TREE>(s, r1 / p.group), s.len);
         // this workgroup's chunk of them
-        const int every = tiles.count(), chunks = max(1, min(p.most, every / kLeastChunk));
-        if (split >= chunks) continue;
-        const int start = (int)((long long)every * split / chunks);
-        const int count = (int)((long long)every * (split + 1) / chunks) - start;
+        int chunks, start, count;
+        if constexpr (TREE) {
+            chunks = share.chunks;
+            split = share.chunk;
+            start = share.start;
+            count = share.count;
+        } else {
+            const int every = tiles.count();
+            chunks = max(1, min(p.most, every / kLeastChunk));
+            if (split >= chunks) continue;
+            start = (int)((long long)every * split / chunks);
+            count = (int)((long long)every * (split + 1) / chunks) - start;
+        }
         // the wave's rows, and the lane's
         const int w0 = min(r0 + row_wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
         const bool idle = r0 + row_wave * kWaveRows > r1;
@@ -630,7 +759,8 @@ hipError_t launch_prompt_rows(const AttnArgs &p, int head_dim, bool bf16, int ro
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us before weights were two halves).  The kernel steps on where
     // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
-    const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.most;
+    // Trees: p.most workgroups share a kv head (TreeShare).
+    const int grid = p.c.kv_heads * (TREE ? p.most : (flat ? 1 : p.c.seqs) * row_tiles * p.most);
     if (grid == 0) return hipSuccess;
     return bf16 ? launch_dim<bhalf_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s)
                 : launch_dim<half_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s);

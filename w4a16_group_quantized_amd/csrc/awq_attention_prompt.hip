@@ -20,6 +20,20 @@ int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long k
     return (int)std::max<long long>(1, std::min<long long>({512 / groups, key_tiles / kLeastChunk, kMostSplits}));
 }
 
+// Trees: workgroups of a kv head, two to a CU in all, or where keys are not cut, one to a row tile;
+// and chunks that a row tile has room for, twice what it has on average, since sequences are not
+// equally long.
+TreePlan tree_plan(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles) {
+    const long long groups = std::max<long long>(1, (long long)(flat ? 1 : seqs) * row_tiles);   // of a kv head
+    const long long all = groups * kv_heads;
+    TreePlan t{(int)std::min<long long>(groups, (1 << 24) / kv_heads), 1};
+    if (key_tiles >= 2 * kLeastChunk && all < kManyTreeTiles) {
+        t.shares = std::max(1, kTreeSlots / kv_heads);
+        t.room = (int)std::max<long long>(3, std::min<long long>({2 * kTreeSlots / all + 1, key_tiles / kLeastChunk + 1, kMostSplits + 1}));
+    }
+    return t;
+}
+
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
     return launch_prompt_rows<false>(p, head_dim, bf16, row_tiles, flat, s);
 }

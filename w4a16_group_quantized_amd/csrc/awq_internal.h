@@ -82,7 +82,7 @@ hipError_t launch_kv_append_at(const KvView &c, int head_dim, const uint16_t *q,
                                int rope_positions, int rot, bool adjacent, const int32_t *positions,
                                int axes, const AxisMap &map, bool bf16, int max_q, hipStream_t s);
 size_t attention_workspace(int seqs, int rows, int q_heads, int kv_heads, int head_dim, int max_q,
-                           int max_kv, int window, int sinks);
+                           int max_kv, int window, int sinks, bool tree);
 hipError_t launch_attention(const KvView &c, int head_dim, const uint16_t *q, long long q_stride,
                             uint16_t *out, int q_heads, bool bf16, float scale, int window, int sinks,
                             int max_q, int max_kv, const uint32_t *tree, int tree_words, void *workspace, hipStream_t s);
