@@ -60,40 +60,44 @@ __device__ __forceinline__ int first_place(const Seq &s, int row) { return TREE 
 template <bool TREE>
 __device__ __forceinline__ int last_place(const Seq &s, int row) { return TREE ? s.len - 1 : s.first() + row; }
 
-// What a row sees.
-template <bool TREE>
-struct Sight {
-    int pos, far, sinks;     // keys up to `far` are out of sight, but for the first `sinks`
-    __device__ __forceinline__ Sight(const AttnArgs &p, const Seq &s, int token, int at)
-        : pos(at), far(p.window > 0 ? at - p.window : -0x7FFFFFFF), sinks(p.sinks) {}
-    // key j, the e-th of a group
-    __device__ __forceinline__ bool operator()(int j, int) const { return (j <= pos) & ((j > far) | (j < sinks)); }
-    __device__ __forceinline__ void group(int) {}
-};
-template <>
-struct Sight<true> {
-    const AttnArgs &p;
-    int row, first, far;
-    uint32_t bits = 0;
-    __device__ __forceinline__ Sight(const AttnArgs &args, const Seq &s, int token, int)
-        : p(args), row(s.row0 + token), first(s.first()), far(-0x7FFFFFFF) {
+// The arguments, read again where they are used: what a kernel has at its beginning it keeps in
+// scalar registers, of which its inner loop has too few for what is used before and behind it.
+// (AttnArgs is the first argument.)
+typedef const __attribute__((address_space(4))) AttnArgs *ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+    ArgsAgain a = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return a;
+}
+
+// What a drafted tree's row sees of sixteen keys: a bit for each.
+struct TreeSight {
+    int row, first, far;     // keys before the tree up to `far` are out of sight, but for the first ones
+    __device__ __forceinline__ TreeSight(const AttnArgs &p, const Seq &s, int token) : row(s.row0 + token), first(s.first()), far(-1) {
         if (p.window > 0) {
             far = first - 1 - p.window;
-            for (int i = 0; i < p.tree_words; ++i) far += __builtin_popcount(word(i));
+            const uint32_t *bits = p.tree + (long long)row * p.tree_words;
+            for (int i = 0; i < p.tree_words; ++i) far += __builtin_popcount(bits[i]);
         }
     }
-    __device__ __forceinline__ uint32_t word(int i) const {
-        return (uint32_t)i < (uint32_t)p.tree_words ? p.tree[(long long)row * p.tree_words + i] : 0u;
+    // keys j .. j + 15, of which the first `live` exist
+    __device__ __forceinline__ uint32_t sixteen(ArgsAgain a, int j, int live) const {
+        const uint32_t *bits = a->tree + (long long)row * a->tree_words;
+        const int u = j - first, words = a->tree_words;
+        const auto word = [&](int i) {         // (no condition around the load, which would be a wait)
+            const uint32_t w = bits[min(max(i, 0), words - 1)];
+            return (uint32_t)i < (uint32_t)words ? w : 0u;
+        };
+        const auto low = [](int n) { return (1u << min(max(n, 0), 16)) - 1u; };
+        const uint32_t own = __builtin_amdgcn_alignbit(word((u >> 5) + 1), word(u >> 5), u & 31);
+        uint32_t before = low(-u);
+        if (a->window > 0) before &= ~low(far < j ? 0 : far - j + 1) | low(a->sinks <= j ? 0 : a->sinks - j);
+        return (own | before) & low(live);
     }
-    __device__ __forceinline__ bool operator()(int j, int e) const {
-        return j < first ? (j > far) | (j < p.sinks) : (bits >> e & 1) != 0;
-    }
-    // before the keys of a group of sixteen, from its first key on: their rows' bits (those of
-    // tokens before the tree have none)
-    __device__ __forceinline__ void group(int j) {
-        const int u = j - first;
-        bits = __builtin_amdgcn_alignbit(word((u >> 5) + 1), word(u >> 5), u & 31) & 0xFFFFu;
-    }
+};
+
+struct NoSight {
+    __device__ __forceinline__ NoSight(const AttnArgs &, const Seq &, int) {}
 };
 
 // The sequence with the rank-th most tokens, among up to 64 of them (equal ones in
@@ -220,6 +224,37 @@ __device__ __forceinline__ void live_bytes(int live, uint32_t keep[4]) {
     }
 }
 
+// ---- tiles of keys in LDS (kernels of many rows) ----
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+// A barrier that waits for no load in flight.
+__device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
+__device__ __forceinline__ void to_lds16(const void *src, uint4 *dst) {
+    __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// LDS piece of (row, 16-byte piece), C pieces a row.
+template <int C>
+__device__ __forceinline__ int piece(int row, int at) {
+    return row * C + (C >= 8 ? at ^ (row & 7) : at ^ ((row >> 1) & 3));
+}
+
+// The outputs of 32 elements, and sixteen codes of each times weights w (their leading
+// parts in w[0] and w[1], their remainders in w[2] and w[3]).
+__device__ __forceinline__ void add_products(float16_t &o, uint4 codes, const half8_t w[4]) {
+    const half8_t a = e4m3x8_to_half(codes.x, codes.y), b = e4m3x8_to_half(codes.z, codes.w);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[0], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[2], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[1], o, 0, 0, 0);
+    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[3], o, 0, 0, 0);
+}
+
 // A partial result of a chunk of keys, in the workspace: D outputs (over the sum), the
 // maximum, the sum and (of chunk 0) the number of chunks.
 template <int D>
@@ -229,16 +264,17 @@ constexpr int kPart = D + 4;
 hipError_t launch_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
 hipError_t launch_tree_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
 
-// Rows by rows of 32 to a wave, for prompts (awq_attention_prompt.h).
+// Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
 // row_tiles: of each sequence, or with `flat` of all of them, one after the other.
 int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat);
 int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
-// Drafted trees there: workgroups that share a kv head, and chunks that a row tile has room for.
-struct TreePlan {
-    int shares, room;
-};
-TreePlan tree_plan(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles);
 hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
-hipError_t launch_tree_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s);
+// The same for drafted trees (awq_tree_attention_prefill.hip), and how its work is shared:
+// p.most workgroups (of so many waves) to a kv head, and chunks that a row tile has room for.
+struct TreePlan {
+    int shares, room, waves;
+};
+TreePlan tree_plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, bool mixed, int few, long long key_tiles);
+hipError_t launch_tree_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int waves, hipStream_t s);
 
 }  // namespace awq

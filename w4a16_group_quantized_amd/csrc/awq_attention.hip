@@ -1,6 +1,6 @@
 // awq_attention and awq_tree_attention: which kernel takes a call, how its keys are cut into
 // chunks, and the kernel that joins these.  awq_attention_split.h has the formula and the
-// kernel of few rows, awq_attention_prompt.h that of many.
+// kernel of few rows, awq_attention_prefill.hip and awq_tree_attention_prefill.hip those of many.
 #include <algorithm>
 
 #include "awq_attention.h"
@@ -189,7 +189,7 @@ struct Plan {
     bool prompt, mixed;      // whether the prompt kernel is needed, and both are
     bool wide;               // eight waves to a workgroup
     int few, prompt_tiles, prompt_splits;
-    int shares;              // of a tree's rows in the prompt kernel (TreeShare)
+    TreePlan tree;           // of a tree's rows in the prompt kernel
     int row_tiles, splits, target;
     int room() const { return std::max(splits, prompt_splits); }
 };
@@ -202,15 +202,15 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;
-    pl.splits = pl.prompt_splits = pl.shares = 1;
+    pl.splits = pl.prompt_splits = 1;
+    pl.tree = {};
     pl.wide = false;
     if (pl.prompt) {
         pl.prompt_tiles = prefill_row_tiles(seqs, rows, kv_heads, group, head_dim, max_q, pl.few, pl.mixed);
         pl.prompt_splits = prefill_splits(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
         if (tree) {
-            const TreePlan t = tree_plan(seqs, kv_heads, pl.prompt_tiles, pl.mixed, tiles);
-            pl.shares = t.shares;
-            pl.prompt_splits = t.room;
+            pl.tree = tree_plan(seqs, rows, kv_heads, group, head_dim, max_q, pl.mixed, pl.few, tiles);
+            pl.prompt_splits = pl.tree.room;
         }
         if (!pl.mixed) return pl;
     }
@@ -268,8 +268,8 @@ hipError_t launch(AttnArgs p, int D, const Plan &pl, bool bf16, hipStream_t s) {
     const bool tree = p.tree != nullptr;
     if (pl.prompt) {
         p.few = pl.mixed ? pl.few : 0;
-        p.most = tree ? pl.shares : pl.prompt_splits;
-        e = (tree ? launch_tree_attention_prefill : launch_attention_prefill)(p, D, bf16, pl.prompt_tiles, pl.mixed, s);
+        p.most = tree ? pl.tree.shares : pl.prompt_splits;
+        e = tree ? launch_tree_attention_prefill(p, D, bf16, pl.tree.waves, s) : launch_attention_prefill(p, D, bf16, pl.prompt_tiles, pl.mixed, s);
         if (e != hipSuccess) return e;
     }
     if (!pl.prompt || pl.mixed) {

@@ -1,4 +1,4 @@
-// awq_attention, awq_tree_attention for many rows (prompts, chunks of prompts, large trees): see
+// awq_attention for many rows (prompts, chunks of prompts): see
 // awq_attention_split.h for the formula and the transposed products.
 //
 // A workgroup of four waves takes 128 rows (64 with heads of 256; row r of a kv head: token r / group,
@@ -41,9 +41,7 @@
 // maximum that they refer to is moved only when a row exceeds it by 2^4, so the
 // largest is 2^15, and rescaling the outputs is rare after the first tiles.  (The difference
 // is compared: mx + 2^4 rounds up by half a step of 2^26 and more.)
-//
-// TREE (awq_tree_attention): the last tokens are a drafted tree's rows; see Sight.
-#pragma once
+#include <algorithm>
 
 #include "awq_attention.h"
 #include "awq_internal.h"
@@ -56,153 +54,16 @@ constexpr int kWaveRows = 32, kWaves = 4;
 // keys, one sequence: 47 / 43 / 140 us at 16 tiles, 26 / 32 / 137 at 6, 24 / 32 / 140 at 4; 16
 // sequences of 32 rows over 4k: 90 / 84 / 85.
 constexpr int kLeastChunk = 6, kMostSplits = 32;
-constexpr int kLeastShare = 8;             // units of a workgroup (trees)
-constexpr int kTreeSlots = 512, kManyTreeTiles = 4 * kTreeSlots;
 constexpr float kWeightBits = 11.0f, kSlack = 4.0f;
 
 // Heads of 256 elements: two waves share 32 rows.  Elsewhere a wave has 32 rows to itself.
 constexpr bool in_pairs(int head_dim) { return head_dim > 128; }
 constexpr int rows_of(int head_dim) { return kWaveRows * (in_pairs(head_dim) ? kWaves / 2 : kWaves); }
 
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-// A barrier that waits for no load in flight.
-__device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
-__device__ __forceinline__ void to_lds16(const void *src, uint4 *dst) {
-    __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
-}
-__device__ __forceinline__ float lane_value(float x, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
-
-// LDS piece of (row, 16-byte piece), C pieces a row.
-template <int C>
-__device__ __forceinline__ int piece(int row, int at) {
-    return row * C + (C >= 8 ? at ^ (row & 7) : at ^ ((row >> 1) & 3));
-}
-
-// The outputs of 32 elements, and sixteen codes of each times weights w (their leading
-// parts in w[0] and w[1], their remainders in w[2] and w[3]).
-__device__ __forceinline__ void add_products(float16_t &o, uint4 codes, const half8_t w[4]) {
-    const half8_t a = e4m3x8_to_half(codes.x, codes.y), b = e4m3x8_to_half(codes.z, codes.w);
-    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[0], o, 0, 0, 0);
-    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, w[2], o, 0, 0, 0);
-    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[1], o, 0, 0, 0);
-    o = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, w[3], o, 0, 0, 0);
-}
-
-// Drafted trees: how workgroups share the work of a kv head.  All rows of a tree see the same
-// tiles of keys, so the work is a line of units, a row tile's tile of keys each: row tiles one after
-// the other, with all of their tiles.  Workgroup k takes the units [k each, (k + 1) each), so
-// that all take the same time, whatever the lengths of the sequences: a part of a row tile's keys, or all
-// of some, or both.  A border less than kLeastChunk tiles from the border of a row tile moves there.
-struct TreeShare {
-    int seq, row_tile, start, count, chunk, chunks;    // a piece: tiles start .. start + count - 1
-    int number;
-    long long at, end, each;
-
-    // A row tile of a line of them: its sequence, number there, first unit and tiles.
-    struct RowTile {
-        long long first;
-        int seq, number, tiles;
-    };
-    // What a lane has of the 64 sequences from `from` on: the units of its sequence and of those up
-    // to it, and the sequence's tiles; and all of them.
-    struct Lane {
-        long long own, upto, all;
-        int from, tiles;
-    };
-    static __device__ __forceinline__ long long scalar(long long x) {
-        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-        return (long long)((uint64_t)hi << 32 | lo);
-    }
-    static __device__ __forceinline__ Lane load(const AttnArgs &p, int rows, int from) {
-        Lane l{0, 0, 0, from, 0};
-        const int lane = threadIdx.x & 63, b = from + lane;
-        if (b < p.c.seqs) {
-            const Seq s = load_seq(p.c, b);
-            const int total = s.n * p.group;
-            if (total > 0 && total >= p.few) {
-                l.tiles = max(1, visible_tiles(p, first_place<true>(s, 0), s.len - 1, s.len).count());
-                l.own = (long long)l.tiles * ((total + rows - 1) / rows);
-            }
-        }
-        l.upto = l.own;
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) {
-            const long long other = __shfl_up(l.upto, k);
-            l.upto += lane >= k ? other : 0;
-        }
-        l.all = scalar(__shfl(l.upto, 63));
-        return l;
-    }
-    // The row tile that unit u (there is one) is in; l: of the sequences from 0 on.
-    static __device__ __forceinline__ RowTile find(const AttnArgs &p, int rows, Lane l, long long u) {
-        long long before = 0;
-        while (u >= before + l.all && l.from + 64 < p.c.seqs) {
-            before += l.all;
-            l = load(p, rows, l.from + 64);
-        }
-        const int at = (int)__builtin_ctzll(__ballot(before + l.upto > u));
-        RowTile r;
-        r.tiles = __builtin_amdgcn_readlane(l.tiles, at);
-        r.seq = l.from + at;
-        r.first = before + scalar(__shfl(l.upto - l.own, at));
-        const long long in = u - r.first;
-        r.number = __builtin_amdgcn_readfirstlane(in >> 32 ? (int)(in / r.tiles) : (int)((uint32_t)in / (uint32_t)r.tiles));
-        r.first = scalar(r.first + (long long)r.number * r.tiles);
-        return r;
-    }
-    static __device__ __forceinline__ int least(const AttnArgs &p, int tiles) { return p.splits > 1 ? kLeastChunk : tiles; }
-    static __device__ __forceinline__ long long border(const AttnArgs &p, int rows, const Lane &l, long long u, long long units) {
-        if (u >= units) return units;
-        const RowTile r = find(p, rows, l, u);
-        const int far = least(p, r.tiles);
-        return u - r.first < far ? r.first : r.first + r.tiles - u < far ? r.first + r.tiles : u;
-    }
-    __device__ __forceinline__ void begin(const AttnArgs &p, int rows, int k) {
-        // all units, and the most tiles of a row tile, which has room for p.splits chunks
-        const Lane l = load(p, rows, 0);
-        long long units = l.all;
-        int most = max(1, l.tiles);
-        for (int from = 64; from < p.c.seqs; from += 64) {
-            const Lane other = load(p, rows, from);
-            units += other.all;
-            most = max(most, other.tiles);
-        }
-#pragma unroll
-        for (int i = 32; i > 0; i >>= 1) most = max(most, __shfl_xor(most, i));
-        each = max((units + p.most - 1) / p.most, (long long)kLeastShare);
-        if (p.splits > 1) each = max(each, (long long)(most / (p.splits - 1) + 1));
-        each = scalar(each);
-        number = k;
-        at = scalar(border(p, rows, l, k * each, units));
-        end = scalar(border(p, rows, l, (k + 1) * each, units));
-    }
-    __device__ __forceinline__ bool next(const AttnArgs &p, int rows) {
-        if (at >= end) return false;
-        const RowTile r = find(p, rows, load(p, rows, 0), at);
-        const long long stop = min(end, r.first + r.tiles);
-        seq = r.seq;
-        row_tile = r.number;
-        start = __builtin_amdgcn_readfirstlane((int)(at - r.first));
-        count = __builtin_amdgcn_readfirstlane((int)(stop - at));
-        // borders inside of the row tile: of workgroups lo .. hi
-        const int far = least(p, r.tiles);
-        const long long lo = (r.first + far + each - 1) / each, hi = (r.first + r.tiles - far) / each;
-        chunks = __builtin_amdgcn_readfirstlane((int)max(hi - lo + 1, 0ll) + 1);
-        chunk = __builtin_amdgcn_readfirstlane(start == 0 ? 0 : (int)(number - lo) + 1);
-        at = stop;
-        return true;
-    }
-};
-
 // BIG: pages of at least a tile, so that a tile's page and scales are the same for
 // all lanes and its addresses are scalar arithmetic (about 150 of 450 vector
 // instructions a tile less).
-template <typename T, int D, bool BIG, bool TREE>
+template <typename T, int D, bool BIG>
 __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int tiles_per_seq) {      // 0: flat
     constexpr int kC = D / 16;                 // pieces of a key
     constexpr int kP = D / 32;                 // pairs of pieces of a key; 32-element blocks of a value
@@ -219,13 +80,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     const int m = lane & 31, hf = lane >> 5;
     // with pairs: which 32 keys of a tile, and which half of the outputs, are the wave's
     const int side = kPairs ? wave & 1 : 0, row_wave = kPairs ? wave >> 1 : wave;
-    const int h = blockIdx.x % c.kv_heads;
-    int split = TREE ? 0 : blockIdx.x / c.kv_heads % p.most;
-    const int slot = TREE ? 0 : blockIdx.x / (c.kv_heads * p.most);
-    int b = 0, tile = 0, tile_step = tiles_per_seq;
-    if (TREE) {
-        tile_step = 0;
-    } else if (tiles_per_seq > 0) {
+    const int h = blockIdx.x % c.kv_heads, split = blockIdx.x / c.kv_heads % p.most;
+    const int slot = blockIdx.x / (c.kv_heads * p.most);
+    int b, tile, tile_step = tiles_per_seq;
+    if (tiles_per_seq > 0) {
         b = seq_of_rank(c, slot / tiles_per_seq);
         tile = slot % tiles_per_seq;
     } else {
@@ -237,13 +95,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
         tile = at.y;
         tile_step = 1 << 30;
     }
-    Seq s = TREE ? Seq{0, 0, 0} : load_seq(c, b);
+    const Seq s = load_seq(c, b);
     const int P = 1 << c.log2_page;
-    int total = s.n * p.group;
+    const int total = s.n * p.group;
     const int row_tiles = (total + kRows - 1) / kRows;
     const int32_t *table = c.page_table + (long long)b * c.table_width;
-    TreeShare share;
-    if constexpr (TREE) share.begin(p, kRows, blockIdx.x / c.kv_heads);
     const int gv = (lane & 3) ^ ((lane >> 3) & 3);         // sixteen-key group whose values this lane loads
     const long long slab = (long long)P * D;
 
@@ -262,37 +118,21 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     }
 
     // the longest rows first
-    for (int rt = row_tiles - 1 - tile; TREE ? share.next(p, kRows) : rt >= 0; rt -= tile_step) {
-        if constexpr (TREE) {
-            b = share.seq;
-            rt = share.row_tile;
-            s = load_seq(c, b);
-            total = s.n * p.group;
-            table = c.page_table + (long long)b * c.table_width;
-        }
+    for (int rt = row_tiles - 1 - tile; rt >= 0; rt -= tile_step) {
         const int r0 = rt * kRows, r1 = min(r0 + kRows, total) - 1;
-        const Tiles tiles = visible_tiles(p, first_place<TREE>(s, r0 / p.group), last_place<TREE>(s, r1 / p.group), s.len);
+        const Tiles tiles = visible_tiles(p, s.first() + r0 / p.group, s.first() + r1 / p.group, s.len);
         // this workgroup's chunk of them
-        int chunks, start, count;
-        if constexpr (TREE) {
-            chunks = share.chunks;
-            split = share.chunk;
-            start = share.start;
-            count = share.count;
-        } else {
-            const int every = tiles.count();
-            chunks = max(1, min(p.most, every / kLeastChunk));
-            if (split >= chunks) continue;
-            start = (int)((long long)every * split / chunks);
-            count = (int)((long long)every * (split + 1) / chunks) - start;
-        }
+        const int every = tiles.count(), chunks = max(1, min(p.most, every / kLeastChunk));
+        if (split >= chunks) continue;
+        const int start = (int)((long long)every * split / chunks);
+        const int count = (int)((long long)every * (split + 1) / chunks) - start;
         // the wave's rows, and the lane's
         const int w0 = min(r0 + row_wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
         const bool idle = r0 + row_wave * kWaveRows > r1;
-        const int lo = first_place<TREE>(s, w0 / p.group), hi = last_place<TREE>(s, w1 / p.group);
+        const int lo = s.first() + w0 / p.group, hi = s.first() + w1 / p.group;
         const int r = min(w0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
-        Sight<TREE> sight(p, s, token, s.first() + token);
+        const int pos = s.first() + token;
         const uint16_t *qrow = p.q + (long long)(s.row0 + token) * p.q_stride + head * D + 16 * hf;
         float up = p.scale < 0.0f ? -1.0f : 1.0f, down = fabsf(p.scale);
         if constexpr (!__is_same(T, half_t)) {
@@ -401,10 +241,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     (p.window > 0 && j0 <= hi - p.window && j0 + kTile > p.sinks)) {
                     const int jg = j0 + 32 * side + 16 * hf;
                     const int live = live_keys(j0, 2 * side + hf, ok);
-                    sight.group(jg);
+                    const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const bool see = (e < live) & sight(jg + e, e);
+                        const int j = jg + e;
+                        const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
                         acc[e] = see ? acc[e] : -__builtin_inff();
                     }
                 }
@@ -568,10 +409,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
                     for (int u = 0; u < 2; ++u) {
                         const int jg = j0 + 32 * u + 16 * hf;
                         const int live = live_keys(j0, 2 * u + hf, ok);
-                        sight.group(jg);
+                        const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const bool see = (e < live) & sight(jg + e, e);
+                            const int j = jg + e;
+                            const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
                             acc[u][e] = see ? acc[u][e] : -__builtin_inff();
                         }
                     }
@@ -733,38 +575,52 @@ __global__ void __launch_bounds__(64 * kWaves, 2) prefill_kernel(AttnArgs p, int
     }
 }
 
-template <typename T, int D, bool TREE>
+template <typename T, int D>
 void launch_page(const AttnArgs &p, int grid, int tiles_per_seq, hipStream_t s) {
     if ((1 << p.c.log2_page) >= kTile)
-        prefill_kernel<T, D, true, TREE><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
+        prefill_kernel<T, D, true><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
     else
-        prefill_kernel<T, D, false, TREE><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
+        prefill_kernel<T, D, false><<<grid, 64 * kWaves, 0, s>>>(p, tiles_per_seq);
 }
 
-template <typename T, bool TREE>
+template <typename T>
 hipError_t launch_dim(const AttnArgs &p, int D, int grid, int tiles_per_seq, hipStream_t s) {
     switch (D) {
-    case 64: launch_page<T, 64, TREE>(p, grid, tiles_per_seq, s); break;
-    case 128: launch_page<T, 128, TREE>(p, grid, tiles_per_seq, s); break;
-    case 256: launch_page<T, 256, TREE>(p, grid, tiles_per_seq, s); break;
+    case 64: launch_page<T, 64>(p, grid, tiles_per_seq, s); break;
+    case 128: launch_page<T, 128>(p, grid, tiles_per_seq, s); break;
+    case 256: launch_page<T, 256>(p, grid, tiles_per_seq, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
-template <bool TREE>
-hipError_t launch_prompt_rows(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
+}  // namespace
+
+int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat) {
+    const int each = rows_of(head_dim);
+    if (flat)                                  // all that there can be
+        return (int)((long long)rows * group / each + std::min<long long>(seqs, (long long)rows * group / few));
+    const long long tiles = ((long long)max_q * group + each - 1) / each;
+    const long long pairs = (long long)kv_heads * seqs;                          // below 2^20
+    return (int)std::max<long long>(1, std::min<long long>(tiles, ((1 << 24) - 1) / (kMostSplits * pairs)));
+}
+
+// Chunks of the keys where row tiles are too few to fill the GPU (two workgroups to a CU).
+int prefill_splits(int seqs, int kv_heads, int row_tiles, bool flat, long long key_tiles) {
+    const long long groups = std::max<long long>(1, (long long)(flat ? 1 : seqs) * kv_heads * row_tiles);
+    return (int)std::max<long long>(1, std::min<long long>({512 / groups, key_tiles / kLeastChunk, kMostSplits}));
+}
+
+hipError_t launch_attention_prefill(const AttnArgs &p, int head_dim, bool bf16, int row_tiles, bool flat, hipStream_t s) {
     // The kv head fastest: with a multiple of eight of them, the row tiles that read the same
     // keys meet in one XCD's cache.  Then the row tiles of a sequence, and the sequences, the
     // longest first, so that the last workgroups to start are short (four sequences of 512 rows,
     // one of them over twice the keys of the others: 1080 -> 693 us before weights were two halves).  The kernel steps on where
     // the grid is cut.  Flat: the row tiles of the sequences that have `few` rows or more.
-    // Trees: p.most workgroups share a kv head (TreeShare).
-    const int grid = p.c.kv_heads * (TREE ? p.most : (flat ? 1 : p.c.seqs) * row_tiles * p.most);
+    const int grid = p.c.kv_heads * (flat ? 1 : p.c.seqs) * row_tiles * p.most;
     if (grid == 0) return hipSuccess;
-    return bf16 ? launch_dim<bhalf_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s)
-                : launch_dim<half_t, TREE>(p, head_dim, grid, flat ? 0 : row_tiles, s);
+    return bf16 ? launch_dim<bhalf_t>(p, head_dim, grid, flat ? 0 : row_tiles, s)
+                : launch_dim<half_t>(p, head_dim, grid, flat ? 0 : row_tiles, s);
 }
 
-}  // namespace
 }  // namespace awq

@@ -28,7 +28,7 @@
 // combine_kernel (awq_attention.hip) joins the chunks' partial results (fp32, in the
 // workspace) where there is more than one chunk.
 //
-// TREE (awq_tree_attention): the last tokens are a drafted tree's rows; see Sight.
+// TREE (awq_tree_attention): the last tokens are a drafted tree's rows; see TreeSight.
 #pragma once
 
 #include <type_traits>
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
         // this lane's row
         const int r = min(r0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
-        Sight<TREE> sight(p, s, token, s.first() + token);
+        const int pos = s.first() + token;
+        const std::conditional_t<TREE, TreeSight, NoSight> sight(p, s, token);
         const uint16_t *qrow = p.q + (long long)(s.row0 + token) * p.q_stride + head * D;
         // bf16 rows are brought into fp16's range by a power of two of their own (exact but for
         // elements 2^-38 below the largest)
@@ -255,11 +256,18 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
             const bool whole = live == 16 && j0 + kTile <= lo + 1 &&
                                (p.window <= 0 || j0 > hi - p.window || j0 + kTile <= p.sinks);
             if (!__all(whole)) {
-                sight.group(jg);
+                if constexpr (TREE) {
+                    const uint32_t see = sight.sixteen(args_again(), jg, live);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const bool see = (e < live) & sight(jg + e, e);
-                    x[e] = see ? x[e] : -__builtin_inff();
+                    for (int e = 0; e < 16; ++e) x[e] = see >> e & 1 ? x[e] : -__builtin_inff();
+                } else {
+                    const int far = p.window > 0 ? pos - p.window : -0x7FFFFFFF;      // keys up to it are out of sight
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = jg + e;
+                        const bool see = (e < live) & (j <= pos) & ((j > far) | (j < p.sinks));
+                        x[e] = see ? x[e] : -__builtin_inff();
+                    }
                 }
                 // codes of slots that hold no token may be anything, NaN among it
                 uint32_t keep[4];
