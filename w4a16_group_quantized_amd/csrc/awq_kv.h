@@ -24,6 +24,15 @@ struct KvView {
 struct AxisMap {
     uint64_t bits[4];
     void set(int f, int axis) { bits[f / 32] |= (uint64_t)axis << (2 * (f % 32)); }
+    // whether more fours of n frequencies are of several axes than borders of sections can make
+    bool in_turn(int n) const {
+        int mixed = 0;
+        for (int f = 0; f < n; f += 4) {
+            const uint32_t four = (uint32_t)(bits[f / 32] >> (2 * (f % 32))) & 0xFFu;
+            mixed += four != (four & 3u) * 0x55u;
+        }
+        return mixed > 3;
+    }
     __device__ __forceinline__ uint8_t at(int f) const {
         const uint64_t w = f < 64 ? (f < 32 ? bits[0] : bits[1]) : (f < 96 ? bits[2] : bits[3]);
         return (uint8_t)(w >> (2 * (f % 32)) & 3);

@@ -11,7 +11,7 @@ hipError_t launch_kv_append(const KvView &c, int head_dim, const uint16_t *q, lo
                             int rope_positions, int rot, bool adjacent, bool bf16, int max_q,
                             hipStream_t s) {
     const AppendArgs p{c, q, k, v, q_stride, k_stride, v_stride, q_out, rope, rope_positions, rot, q_heads, nullptr, 0, {}};
-    return launch_append<false>(p, head_dim, adjacent, bf16, max_q, s);
+    return launch_append<0>(p, head_dim, adjacent, bf16, max_q, s);
 }
 
 }  // namespace awq

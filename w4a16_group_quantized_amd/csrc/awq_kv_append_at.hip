@@ -9,7 +9,8 @@ hipError_t launch_kv_append_at(const KvView &c, int head_dim, const uint16_t *q,
                                int rope_positions, int rot, bool adjacent, const int32_t *positions,
                                int axes, const AxisMap &map, bool bf16, int max_q, hipStream_t s) {
     const AppendArgs p{c, q, k, v, q_stride, k_stride, v_stride, q_out, rope, rope_positions, rot, q_heads, positions, axes, map};
-    return launch_append<true>(p, head_dim, adjacent, bf16, max_q, s);
+    if (map.in_turn(rot / 2)) return launch_append_in_turn(p, head_dim, adjacent, bf16, max_q, s);
+    return launch_append<kSections>(p, head_dim, adjacent, bf16, max_q, s);
 }
 
 }  // namespace awq

@@ -27,7 +27,7 @@
 // One workgroup owns one (page, kv head), for the page's new tokens: nobody else
 // writes that slab or its scales, so no atomics.  Bound: HBM for prompts, launch latency for single tokens.
 //
-// AT (awq_kv_append_at): the rows' rotary positions are given, up to four of each row, and
+// AT, not 0 (awq_kv_append_at): the rows' rotary positions are given, up to four of each row, and
 // frequency f takes the one that the map names; places in the cache stay those of the
 // sequence.  A position behind the table turns by NaN, so such a token comes out as one
 // that is not finite.
@@ -40,10 +40,6 @@
 #include "awq_kv.h"
 
 namespace awq {
-namespace {
-
-constexpr int kMaxPage = 256, kMaxRot = 256;
-constexpr int kMinExp = -64;
 
 struct AppendArgs {
     KvView c;
@@ -56,6 +52,13 @@ struct AppendArgs {
     int axes;
     AxisMap map;
 };
+hipError_t launch_append_in_turn(const AppendArgs &p, int head_dim, bool adjacent, bool bf16, int max_q, hipStream_t s);
+
+namespace {
+
+constexpr int kMaxPage = 256, kMaxRot = 256;
+enum { kSections = 1, kInTurn = 2 };        // AT: how axes share the frequencies, mostly
+constexpr int kMinExp = -64;
 
 // The scale of a largest magnitude: 2^e, see the top.
 __device__ __forceinline__ float scale_for(float amax) {
@@ -124,12 +127,39 @@ __device__ __forceinline__ auto table_row(const float *row, int rot) {
 }
 
 // The same where each frequency takes the table's row of the position on its axis.  Sections of
-// the frequencies leave four of them on one axis: then it is one load for the four.
+// the frequencies leave four of them on one axis: then it is one load for the four, and at a border
+// one for each.  With the axes in turn it is one for each axis that they are on (4 x 2048 tokens 58.4
+// us; as at borders 64.5.  For sections 57.3 and 53.5, and both in one kernel cost 16384 tokens 10 us).
+template <bool TURN>
 __device__ __forceinline__ void given_turns(const AppendArgs &p, const uint8_t *axis, long long row, int f, float4 &c, float4 &s) {
     const float none = std::numeric_limits<float>::quiet_NaN();
     const int32_t *at = p.positions + row * p.axes;
     const uint32_t four = *reinterpret_cast<const uint32_t *>(axis + f);
-    if (four == (four & 0xFF) * 0x01010101u) {
+    if constexpr (TURN) {
+        int pos[4];                                    // (all on the way at once; behind the last axis the last again)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) pos[a] = at[min(a, p.axes - 1)];
+        float cs[4] = {}, ss[4] = {};
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            bool on[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) on[e] = (four >> (8 * e) & 0xFF) == (uint32_t)a;
+            if (on[0] | on[1] | on[2] | on[3]) {
+                const bool in = (uint32_t)pos[a] < (uint32_t)p.rope_positions;
+                const float *from = p.rope + (long long)(in ? pos[a] : 0) * p.rot + f;
+                const float4 x = *reinterpret_cast<const float4 *>(from), y = *reinterpret_cast<const float4 *>(from + p.rot / 2);
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    cs[e] = on[e] ? (in ? xs[e] : none) : cs[e];
+                    ss[e] = on[e] ? (in ? ys[e] : none) : ss[e];
+                }
+            }
+        }
+        c = make_float4(cs[0], cs[1], cs[2], cs[3]);
+        s = make_float4(ss[0], ss[1], ss[2], ss[3]);
+    } else if (four == (four & 0xFF) * 0x01010101u) {
         const int pos = at[four & 0xFF];
         const bool in = (uint32_t)pos < (uint32_t)p.rope_positions;
         const float *from = p.rope + (long long)(in ? pos : 0) * p.rot + f;
@@ -196,7 +226,7 @@ __device__ __forceinline__ void turn_unit(float x[16], int c0, int c1, int rot, 
 // (sequence, kv head) take its pages, the others its queries: those are two thirds
 // of a prompt's bytes at four query heads to a kv head, and with them in the pages'
 // workgroups the last round of these was long.
-template <typename T, int D, bool ADJ, int kThreads, int kKeys, bool AT>
+template <typename T, int D, bool ADJ, int kThreads, int kKeys, int AT>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int pages) {     // 0: flat
     constexpr int U = D / 16;                          // units of a head row
     constexpr int kValues = kKeys / 2;                 // tiles of values, 4 slots by 8 elements, a thread holds
@@ -211,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
     // positions in [from, to) have a place in the page table and a row in the rotation's table
     // (first, that of row 0, may be below 0: rows without a place)
     const auto from_of = [](const Seq &s) { return max(s.first(), 0); };
-    const auto to_of = [&](const Seq &s) { return p.rot && !AT ? min(s.len, p.rope_positions) : s.len; };
+    const auto to_of = [&](const Seq &s) { return p.rot && AT == 0 ? min(s.len, p.rope_positions) : s.len; };
     int b = blockIdx.z, piece = blockIdx.x, blocks = gridDim.x - pages;
     if (pages == 0) {
         const auto pages_of = [&](const Seq &s) {
@@ -231,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
     const int group = p.q_heads / c.kv_heads;
     const int first = s.first(), from = from_of(s), to = to_of(s);
     if (from >= to) return;
-    if constexpr (AT) {                                // (read behind a barrier of both kinds of work)
+    if constexpr (AT != 0) {                                // (read behind a barrier of both kinds of work)
         if (tid < p.rot / 2) axis[tid] = p.map.at(tid);
     }
     if (piece >= pages) {
@@ -262,12 +292,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
             };
             load(0);
             __syncthreads();                           // the rows of the step before are done with
-            if constexpr (AT) {
+            if constexpr (AT != 0) {
                 const int quads = p.rot / 8;           // of frequencies
                 for (int i = tid; i < items / width * quads; i += kThreads) {
                     const int t = i / quads, f = i % quads * 4;
                     float4 c, s;
-                    given_turns(p, axis, row + t, f, c, s);
+                    given_turns<AT == kInTurn>(p, axis, row + t, f, c, s);
                     *reinterpret_cast<float4 *>(rows + t * p.rot + f) = c;
                     *reinterpret_cast<float4 *>(rows + t * p.rot + p.rot / 2 + f) = s;
                 }
@@ -343,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
             unpack8<T>(r[1], x + 8);
             int c0, c1;
             unit_chunks<D, ADJ>(i % U, p.rot, c0, c1);
-            if constexpr (AT)
-                turn_unit<ADJ>(x, c0, c1, p.rot, [&](int f, float4 &c, float4 &s) { given_turns(p, axis, row + i / U, f, c, s); });
+            if constexpr (AT != 0)
+                turn_unit<ADJ>(x, c0, c1, p.rot, [&](int f, float4 &c, float4 &s) { given_turns<AT == kInTurn>(p, axis, row + i / U, f, c, s); });
             else if (p.rot)
                 turn_unit<ADJ>(x, c0, c1, p.rot, table_row(p.rope + (long long)(lo + i / U) * p.rot, p.rot));
         };
@@ -526,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs p, int p
     }
 }
 
-template <typename T, int D, bool AT>
+template <typename T, int D, int AT>
 hipError_t launch(const AppendArgs &p, bool adjacent, bool few, int most, int touched, hipStream_t s) {
     const int threads = few ? 128 : 256, tokens = 8 * threads / D;       // of a workgroup of queries
     dim3 grid(touched + (p.q ? (most + tokens - 1) / tokens : 0), p.c.kv_heads, p.c.seqs);
@@ -553,7 +583,7 @@ hipError_t launch(const AppendArgs &p, bool adjacent, bool few, int most, int to
     return hipGetLastError();
 }
 
-template <typename T, bool AT>
+template <typename T, int AT>
 hipError_t launch_dim(const AppendArgs &p, int D, bool adjacent, bool few, int most, int touched, hipStream_t s) {
     switch (D) {
     case 64: return launch<T, 64, AT>(p, adjacent, few, most, touched, s);
@@ -563,7 +593,7 @@ hipError_t launch_dim(const AppendArgs &p, int D, bool adjacent, bool few, int m
     return hipErrorInvalidValue;
 }
 
-template <bool AT>
+template <int AT>
 hipError_t launch_append(const AppendArgs &p, int head_dim, bool adjacent, bool bf16, int max_q, hipStream_t s) {
     // pages that a sequence's rows can touch (the kernel steps on if there are more)
     const int most = max_q < 1 ? 1 : max_q > p.c.rows ? p.c.rows : max_q;
