@@ -69,6 +69,15 @@ def test_large_trees(dtype, dim, page, heads, new, lens):
     check(t, trees(t, 0.2)[1])
 
 
+@pytest.mark.parametrize("dtype,dim,page,heads", [("fp16", 64, 16, (8, 1)), ("bf16", 128, 64, (8, 1)), ("fp16", 256, 32, (16, 1))])
+@pytest.mark.parametrize("seqs", [64, 65, 150])
+def test_many_large_trees(dtype, dim, page, heads, seqs):
+    """More sequences than a wave has lanes, of many lengths, some without rows."""
+    new = [0 if b % 7 == 3 else 20 + b * 5 % 24 for b in range(seqs)]
+    t = kc.Batch(9, dtype, new, [n + b * 37 % 150 for b, n in enumerate(new)], *heads, dim, page).fill()
+    check(t, trees(t, 0.3)[1])
+
+
 @pytest.mark.parametrize("dim,page,heads", [(64, 16, (8, 2)), (128, 64, (8, 2)), (256, 128, (2, 1)), (128, 32, (5, 5))])
 @pytest.mark.parametrize("new,lens", [([1, 5, 16], [300, 5, 777]), ([130, 70], [130, 500])])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])

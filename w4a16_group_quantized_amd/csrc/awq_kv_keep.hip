@@ -400,17 +400,19 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
     }
 }
 
-// Kept rows of a sequence from which many waves share it.
-constexpr int kMany = 64;
+// Kept rows of a sequence from which many waves share it (half of 8 x 8192 tokens of 8 heads 845 -> 94 us;
+// 4 of 16 rows of 32 sequences 9.9 / 7.6), and the sequences times heads up to which its launch, of
+// up to 20 workgroups for each, has less than 2^32 threads.
+constexpr int kMany = 64, kManyPairs = 1 << 19;
 
 template <int D>
 void launch(const KeepArgs &p, hipStream_t s) {
-    if (p.width <= kMany) {
+    const int pairs = p.c.kv_heads * p.c.seqs;
+    if (p.width <= kMany || pairs > kManyPairs) {
         few_kernel<D><<<dim3(p.c.kv_heads, p.c.seqs), kFewThreads, 0, s>>>(p);
         return;
     }
     constexpr int pieces = D / kKeyWidth + D / kRows;
-    const int pairs = p.c.kv_heads * p.c.seqs;
     static_assert(pieces % (kThreads / 64) == 0, "a piece to a wave");
     many_kernel<D, false><<<dim3(pairs, pieces / (kThreads / 64)), kThreads, 0, s>>>(p);
     many_kernel<D, true><<<pairs, kThreads, 0, s>>>(p);

@@ -2,7 +2,15 @@
 // products, and awq_attention_prefill.hip for the tiles in LDS and how keys are dealt to the
 // products; the arithmetic of a row is the same here.
 //
-// @HEAD@
+// What differs: all rows of a tree see the same tiles of keys, so workgroups go over several row tiles,
+// in equal shares of all the work (TreeShare); and which of a tile's keys a row sees is bits, from the
+// mask's words, needed for the tiles at the tree (and at a window's border) alone.
+//
+// Bound: vector instructions, 390 or so a wave for 32 rows by 64 keys of 128 elements beside 48
+// products, which hold the vector port up for 11 cycles each.  16 trees of up to 64 rows over up to 8191
+// keys, 32 heads on 8: 193 us (74 at the rate of a large matrix product); one of 48 rows, 64 heads on 8,
+// over 131000 keys: 330 us (172).  Eight waves in two groups, one at its products while the other
+// is at its weights: 279 us where this takes 257 (16 trees of 64 rows over 8192 keys).
 #include <algorithm>
 
 #include "awq_attention.h"
@@ -31,7 +39,7 @@ int waves_of(int head_dim, long long rows) {
 // the other, with all of their tiles.  Workgroup k takes the units [k each, (k + 1) each), so
 // that all take the same time, whatever the lengths of the sequences: a part of a row tile's keys, or all
 // of some, or both.  A border less than kLeastChunk tiles from the border of a row tile moves there.
-// 16 trees of 32 to 64 rows over 4k to 8k keys: @O@ -> @S@ us.  Units are of
+// 16 trees of 32 to 64 rows over 4k to 8k keys: a grid over sequences, row tiles and chunks 211 us, this 199.  Units are of
 // 2^shift tiles, so that there are no more than 2^30.
 struct TreeShare {
     int seq, row_tile, start, count, chunk, chunks;    // a piece: tiles start .. start + count - 1

@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const int32_t *pare
 hipError_t launch_tree_rows(const int32_t *parents, const KvView &c, int max_q, uint32_t *mask, int words, int32_t *positions, hipStream_t s) {
     const long long items = (long long)max_q * words;
     // two words to a thread: with eight, one tree of 512 rows takes 11.9 us for 6.6, 256 of them the same
-    const dim3 grid((unsigned)std::min<long long>((items + 2 * kThreads - 1) / (2 * kThreads), 4096), c.seqs);
+    // (a launch has less than 2^32 threads; the kernel steps on)
+    const long long most = std::min(4096, std::max(1, (1 << 23) / c.seqs));
+    const dim3 grid((unsigned)std::min((items + 2 * kThreads - 1) / (2 * kThreads), most), c.seqs);
     if (max_q <= 1024)
         tree_rows_kernel<1024><<<grid, kThreads, 0, s>>>(parents, c, mask, words, positions);
     else
