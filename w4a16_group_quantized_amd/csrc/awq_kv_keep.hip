@@ -210,9 +210,10 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
     constexpr int kGroups = kBlock / 64, kEach = kBlock / kThreads, kPages = kBlock / kLeastPage;
     // by place in the block: the page that its token comes from (-1: none, kStays: nothing is written),
     // the slot there, what its codes are multiplied by
-    __shared__ int from[kBlock], slot[kBlock], to[kPages], limits[2];
+    __shared__ int from[kBlock], slot[kBlock], to[2][kPages], limits[2];
     __shared__ float fk[kBlock], fv[kBlock];
-    __shared__ uint32_t most[2][2][kPages];    // scales as bits (they are positive), of this block and the next
+    __shared__ uint32_t most[2][2][kPages];    // scales as bits (they are positive)
+    // (most and to, of this block and the next, which a wave may begin while others are at this one)
     const KvView &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 atomicMax(&most[odd][1][x >> lp], __builtin_bit_cast(uint32_t, va));
             }
         }
-        if (tid < kBlock >> lp) to[tid] = base + (tid << lp) >= end || own1 < 0 || own1 >= c.pages ? -1 : own1;
+        if (tid < kBlock >> lp) to[odd][tid] = base + (tid << lp) >= end || own1 < 0 || own1 >= c.pages ? -1 : own1;
         __syncthreads();                       // (and every wave is done with the block before)
         if (tid < 2 * kPages) most[odd ^ 1][tid / kPages][tid % kPages] = 0u;
         if constexpr (!SCALES) {
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 const int x = n * kThreads + tid, place = base + x, tok = token(base, n, tok1[n]);
                 const float ka = __builtin_bit_cast(float, most[odd][0][x >> lp]), va = __builtin_bit_cast(float, most[odd][1][x >> lp]);
                 const float a = ks1[n] == ka ? 1.0f : ks1[n] / ka, v = vs1[n] == va ? 1.0f : vs1[n] / va;
-                const bool stays = tok < 0 || to[x >> lp] < 0 || (tok == place && a == 1.0f && v == 1.0f);
+                const bool stays = tok < 0 || to[odd][x >> lp] < 0 || (tok == place && a == 1.0f && v == 1.0f);
                 from[x] = stays ? kStays : id1[n];
                 slot[x] = tok & (P - 1);
                 fk[x] = a;
@@ -341,9 +342,9 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
         ask_tokens(base + 3 * kBlock, tok3);
         if constexpr (SCALES) {
             // (later blocks' are of later pages)
-            if (tid < kBlock >> lp && to[tid] >= 0 && most[odd][0][tid] != 0u) {
-                c.k_scales[(long long)to[tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][0][tid]);
-                c.v_scales[(long long)to[tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][1][tid]);
+            if (tid < kBlock >> lp && to[odd][tid] >= 0 && most[odd][0][tid] != 0u) {
+                c.k_scales[(long long)to[odd][tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][0][tid]);
+                c.v_scales[(long long)to[odd][tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][1][tid]);
             }
             __syncthreads();
             continue;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 if (id != kStays) {
                     const float f = fk[x];
                     const uint32_t none = 0x7F7F7F7Fu;
-                    *reinterpret_cast<uint4 *>(c.k + ((long long)to[x >> lp] * c.kv_heads + h) * slab + (x & (P - 1)) * D + at) =
+                    *reinterpret_cast<uint4 *>(c.k + ((long long)to[odd][x >> lp] * c.kv_heads + h) * slab + (x & (P - 1)) * D + at) =
                         id < 0 ? make_uint4(none, none, none, none)
                                : make_uint4(rescaled(r[n].x, f), rescaled(r[n].y, f), rescaled(r[n].z, f), rescaled(r[n].w, f));
                 }
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 const int x = 64 * n + lane, id = from[x];
                 const bool put = id != kStays;
                 const float f = fv[x];
-                uint8_t *v = c.v + ((long long)to[x >> lp] * c.kv_heads + h) * slab + d * P + (x & (P - 1));
+                uint8_t *v = c.v + ((long long)to[odd][x >> lp] * c.kv_heads + h) * slab + d * P + (x & (P - 1));
 #pragma unroll
                 for (int e = 0; e < kRows; ++e) r[n][e] = id < 0 ? 0u : rescaled(r[n][e], f) & 0xFFu;
                 // four places to a word, where all four are written (pages are of whole words)
