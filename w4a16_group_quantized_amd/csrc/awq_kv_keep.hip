@@ -15,13 +15,18 @@
 // written.
 //
 // many_kernel: keys, and each element's row of the values, do not meet, so waves share a sequence
-// and kv head by pieces of the elements, each through all of its tokens, with no wait for
-// another: 16 elements of the keys, or 4 rows of the values, byte by byte, 64 tokens to an
-// instruction, and all of a block of 512 tokens on the way before the first is written.  The scales
-// are what they share: only the codes move, and a second launch goes over the scales alone.
+// and kv head by pieces of the elements, each through all of its tokens: 16 elements of the keys, or 4
+// rows of the values, and all of a block of 256 tokens on the way before the first is written.  A
+// value's codes lie side by side by token, so what a block needs of a row is runs of sixteen codes: these
+// are loaded, and each lane takes a word's four out of LDS (half of 8 x 8192 tokens: byte after byte
+// from HBM 93 us, so 69); where tokens are of more runs than LDS holds, fewer than a quarter or so of
+// them, byte by byte.  The scales are what waves share: only the codes move, and a second launch
+// goes over the scales alone.
 //
 // Nobody else writes a sequence's slabs or scales: the same bits each time.
 // Bound: latency of a block (kept, page, scales, codes: four loads in a row), blocks one after the other.
+// Half of 8 x 8192 tokens of 8 heads of 128: 61 us, 2.2 TB/s (25 of them without any codes' loads and
+// stores; asking for a block's codes before the last block's are written: 65).
 #include <algorithm>
 
 #include "awq_internal.h"
@@ -31,10 +36,12 @@ namespace awq {
 namespace {
 
 constexpr int kFewThreads = 256, kMaxPage = 256, kAtOnce = 4;
-constexpr int kThreads = 256;
-constexpr int kBlock = 512;                // tokens on the way: whole pages
+constexpr int kThreads = 256, kScaleThreads = 1024;
+constexpr int kBlock = 256;                // tokens on the way: whole pages; of the scales' launch
+constexpr int kScaleBlock = 2048;
 constexpr int kLeastPage = 16;
 constexpr int kKeyWidth = 16, kRows = 4;   // elements of a piece of the keys; rows of a piece of the values
+constexpr int kRuns = 64;                  // runs of sixteen slots that a block's tokens may come from, for LDS to hold them
 constexpr int kStays = -2;
 
 struct KeepArgs {
@@ -202,16 +209,40 @@ __device__ __forceinline__ uint32_t words_of(const uint32_t (&r)[4]) {
     return out;
 }
 
+// The largest of sixteen lanes' numbers, none below 0.
+__device__ __forceinline__ float most_of_16(float x) {
+    int y = __builtin_bit_cast(int, x);
+    y = max(y, __builtin_amdgcn_update_dpp(y, y, 0x128, 0xF, 0xF, false));     // eight lanes on, of sixteen
+    y = max(y, __builtin_amdgcn_update_dpp(y, y, 0x124, 0xF, 0xF, false));     // four
+    y = max(y, __builtin_amdgcn_update_dpp(y, y, 0x122, 0xF, 0xF, false));
+    y = max(y, __builtin_amdgcn_update_dpp(y, y, 0x121, 0xF, 0xF, false));
+    return __builtin_bit_cast(float, y);
+}
+
+// All waves' reads and writes of LDS are done; those of HBM go on.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");
+}
+
+constexpr int pieces_of(int head_dim) { return head_dim / kKeyWidth + head_dim / kRows; }
+
 // SCALES: only these, and the lengths; otherwise only the codes, a piece to a wave: gridDim.y
 // workgroups share a sequence and kv head.
-template <int D, bool SCALES>
-__global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
+template <int D, int kThreads, int kBlock, bool SCALES>
+__global__ void __launch_bounds__(kThreads, SCALES ? 4 : 3) many_kernel(KeepArgs p) {
     constexpr int kWaves = kThreads / 64;
     constexpr int kGroups = kBlock / 64, kEach = kBlock / kThreads, kPages = kBlock / kLeastPage;
     // by place in the block: the page that its token comes from (-1: none, kStays: nothing is written),
     // the slot there, what its codes are multiplied by
-    __shared__ int from[kBlock], slot[kBlock], to[2][kPages], limits[2];
-    __shared__ float fk[kBlock], fv[kBlock];
+    __shared__ __align__(16) int from[kBlock];
+    __shared__ int slot[kBlock], to[2][kPages], limits[2];
+    __shared__ __align__(16) float fk[kBlock], fv[kBlock];
+    // runs of sixteen slots that tokens come from: number of a group's, page, first slot, the values' codes;
+    // and where in these a token's are
+    __shared__ int runs[kGroups], run_page[kRuns], run_slot[kRuns];
+    __shared__ __align__(8) uint16_t code_at[kBlock];
+    __shared__ uint4 codes[kWaves][kRows][kRuns];
     __shared__ uint32_t most[2][2][kPages];    // scales as bits (they are positive)
     // (most and to, of this block and the next, which a wave may begin while others are at this one)
     const KvView &c = p.c;
@@ -292,29 +323,29 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
     ask_pages(start + kBlock, tok2, id2, own2);
     ask_scales(start, tok1, id1, ks1, vs1);
     for (int base = start, odd = 0; base < end; base += kBlock, odd ^= 1) {
-        // the largest scales of each page's tokens
-        const int width = min(P, 64);
+        // the largest scales of each page's tokens, sixteen of them to an atomic
+        uint64_t begins[kEach] = {};           // lanes whose token is the first of a run
+        int all_runs = 0;
 #pragma unroll
         for (int n = 0; n < kEach; ++n) {
             const int id = page(base, n, tok1[n], id1[n]);
-            float ka = id < 0 ? 0.0f : ks1[n], va = id < 0 ? 0.0f : vs1[n];
-            ks1[n] = ka;
-            vs1[n] = va;
+            ks1[n] = id < 0 ? 0.0f : ks1[n];
+            vs1[n] = id < 0 ? 0.0f : vs1[n];
             id1[n] = id;
-#pragma unroll
-            for (int k = 32; k > 0; k >>= 1) {
-                const float a = __shfl_xor(ka, k), v = __shfl_xor(va, k);
-                ka = k < width ? fmaxf(ka, a) : ka;
-                va = k < width ? fmaxf(va, v) : va;
-            }
+            const float ka = most_of_16(ks1[n]), va = most_of_16(vs1[n]);
             const int x = n * kThreads + tid;
-            if ((lane & (width - 1)) == 0) {
+            if constexpr (!SCALES) {
+                const int run = token(base, n, tok1[n]) >> 4, last = __shfl_up(run, 1);
+                begins[n] = __ballot(run >= 0 && (lane == 0 || last != run));
+                if (lane == 0) runs[n * kWaves + wave] = __builtin_popcountll(begins[n]);
+            }
+            if ((lane & 15) == 0) {
                 atomicMax(&most[odd][0][x >> lp], __builtin_bit_cast(uint32_t, ka));
                 atomicMax(&most[odd][1][x >> lp], __builtin_bit_cast(uint32_t, va));
             }
         }
         if (tid < kBlock >> lp) to[odd][tid] = base + (tid << lp) >= end || own1 < 0 || own1 >= c.pages ? -1 : own1;
-        __syncthreads();                       // (and every wave is done with the block before)
+        lds_barrier();                       // (and every wave is done with the block before)
         if (tid < 2 * kPages) most[odd ^ 1][tid / kPages][tid % kPages] = 0u;
         if constexpr (!SCALES) {
 #pragma unroll
@@ -327,8 +358,21 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 slot[x] = tok & (P - 1);
                 fk[x] = a;
                 fv[x] = v;
+                // (the sum of the runs of all groups in all_runs)
+                int run = __builtin_popcountll(begins[n] & (2ull << lane) - 1) - 1;
+                all_runs = 0;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    run += g < n * kWaves + wave ? runs[g] : 0;
+                    all_runs += runs[g];
+                }
+                code_at[x] = (uint16_t)(16 * max(run, 0) + (tok & 15));
+                if ((begins[n] >> lane & 1) && run < kRuns) {
+                    run_page[run] = max(id1[n], 0);
+                    run_slot[run] = tok & (P - 1) & ~15;
+                }
             }
-            __syncthreads();
+            lds_barrier();
         }
 #pragma unroll
         for (int n = 0; n < kEach; ++n) {
@@ -346,10 +390,11 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                 c.k_scales[(long long)to[odd][tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][0][tid]);
                 c.v_scales[(long long)to[odd][tid] * c.kv_heads + h] = __builtin_bit_cast(float, most[odd][1][tid]);
             }
-            __syncthreads();
+            lds_barrier();
             continue;
         }
         const int piece = blockIdx.y * kWaves + wave;
+        if (piece >= pieces_of(D)) continue;
         if (piece < D / kKeyWidth) {
             const int at = piece * kKeyWidth;
             uint4 r[kGroups];
@@ -369,6 +414,53 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
                                : make_uint4(rescaled(r[n].x, f), rescaled(r[n].y, f), rescaled(r[n].z, f), rescaled(r[n].w, f));
                 }
             }
+        } else if (all_runs <= kRuns) {
+            // The runs' codes to LDS, from which a lane takes the four of a word.
+            const int d = (piece - D / kKeyWidth) * kRows;
+            uint4 r[kRuns / 64][kRows];
+#pragma unroll
+            for (int n = 0; n < kRuns / 64; ++n) {
+                const int run = min(64 * n + lane, all_runs - 1);
+                const uint8_t *v = c.v + ((long long)run_page[run] * c.kv_heads + h) * slab + d * P + run_slot[run];
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) r[n][e] = *reinterpret_cast<const uint4 *>(v + e * P);
+            }
+#pragma unroll
+            for (int n = 0; n < kRuns / 64; ++n)
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) codes[wave][e][64 * n + lane] = r[n][e];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int n = 0; n < kBlock / 256; ++n) {
+                const int x = 256 * n + 4 * lane;
+                const int4 id = *reinterpret_cast<const int4 *>(from + x);
+                const float4 f = *reinterpret_cast<const float4 *>(fv + x);
+                const ushort4 at = *reinterpret_cast<const ushort4 *>(code_at + x);
+                const bool put[4] = {id.x != kStays, id.y != kStays, id.z != kStays, id.w != kStays};
+                const uint32_t same = (f.x == 1.0f ? 0xFFu : 0u) | (f.y == 1.0f ? 0xFF00u : 0u) | (f.z == 1.0f ? 0xFF0000u : 0u) | (f.w == 1.0f ? 0xFF000000u : 0u);
+                const uint32_t live = (id.x < 0 ? 0u : 0xFFu) | (id.y < 0 ? 0u : 0xFF00u) | (id.z < 0 ? 0u : 0xFF0000u) | (id.w < 0 ? 0u : 0xFF000000u);
+                uint8_t *v = c.v + ((long long)to[odd][x >> lp] * c.kv_heads + h) * slab + d * P + (x & (P - 1));
+                const uint8_t *bytes = reinterpret_cast<const uint8_t *>(codes[wave]);
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) {
+                    const uint8_t *row = bytes + e * 16 * kRuns;
+                    uint32_t w = row[at.x] | row[at.y] << 8 | row[at.z] << 16 | (uint32_t)row[at.w] << 24;
+                    if (same != 0xFFFFFFFFu) {
+                        float y[4];
+                        from_e4m3x4(w, y);
+                        w = (w & same) | (to_e4m3x4(y[0] * f.x, y[1] * f.y, y[2] * f.z, y[3] * f.w) & ~same);
+                    }
+                    w &= live;
+                    if (put[0] & put[1] & put[2] & put[3]) {
+                        *reinterpret_cast<uint32_t *>(v + e * P) = w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (put[k]) v[e * P + k] = (uint8_t)(w >> (8 * k));
+                    }
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
         } else {
             const int d = (piece - D / kKeyWidth) * kRows;
             uint32_t r[kGroups][kRows];
@@ -401,7 +493,7 @@ __global__ void __launch_bounds__(kThreads) many_kernel(KeepArgs p) {
     }
 }
 
-// Kept rows of a sequence from which many waves share it (half of 8 x 8192 tokens of 8 heads 845 -> 94 us;
+// Kept rows of a sequence from which many waves share it (half of 8 x 8192 tokens of 8 heads 845 -> 61 us;
 // 4 of 16 rows of 32 sequences 9.9 / 7.6), and the sequences times heads up to which its launch, of
 // up to 20 workgroups for each, has less than 2^32 threads.
 constexpr int kMany = 64, kManyPairs = 1 << 19;
@@ -413,10 +505,9 @@ void launch(const KeepArgs &p, hipStream_t s) {
         few_kernel<D><<<dim3(p.c.kv_heads, p.c.seqs), kFewThreads, 0, s>>>(p);
         return;
     }
-    constexpr int pieces = D / kKeyWidth + D / kRows;
-    static_assert(pieces % (kThreads / 64) == 0, "a piece to a wave");
-    many_kernel<D, false><<<dim3(pairs, pieces / (kThreads / 64)), kThreads, 0, s>>>(p);
-    many_kernel<D, true><<<pairs, kThreads, 0, s>>>(p);
+    constexpr int kWaves = kThreads / 64;
+    many_kernel<D, kThreads, kBlock, false><<<dim3(pairs, (pieces_of(D) + kWaves - 1) / kWaves), kThreads, 0, s>>>(p);
+    many_kernel<D, kScaleThreads, kScaleBlock, true><<<pairs, kScaleThreads, 0, s>>>(p);
 }
 
 }  // namespace
