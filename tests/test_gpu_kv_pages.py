@@ -70,6 +70,24 @@ def test_evictions(dim, page, share):
     keep(t, some, [len(x) for x in some])
 
 
+@pytest.mark.parametrize("dim,page,dead", [(64, 16, False), (128, 64, True), (256, 256, False), (64, 32, True), (128, 128, True)])
+@pytest.mark.parametrize("new,counts", [([3000, 1500], [120, 70]), ([1100, 900, 40], [500, 899, 1]), ([2000], [300])])
+def test_many_kept_rows(dim, page, dead, new, counts):
+    """More rows than one workgroup takes, few and many of a stretch, after tokens that stay, with
+    scales far apart and, among others, pages that are none and codes that are NaN."""
+    lens = [n + 21 * b for b, n in enumerate(new)]
+    t = kc.Batch(8, "fp16", new, lens, 2, 2, dim, page).fill()
+    t.ks.copy_(torch.exp2(torch.randint(-12, 0, t.ks.shape, generator=t.g).float()))
+    t.vs.copy_(torch.exp2(torch.randint(-12, 0, t.vs.shape, generator=t.g).float()))
+    if dead:
+        t.table[0, 3], t.table[0, 1] = -1, t.pages
+        for j in range(0, lens[0], 7):
+            id = int(t.table[0, j // page])
+            if 0 <= id < t.pages:
+                t.k[id, 1, j % page] = 0x7F
+    keep(t, [subset(n, m, t.g) for n, m in zip(new, counts)], counts)
+
+
 @pytest.mark.parametrize("page", [16, 64])
 def test_scales_far_apart(page):
     """Codes that become subnormal, or nothing, under the larger scale of a neighbour."""
