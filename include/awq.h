@@ -516,8 +516,8 @@ awq_status awq_tree_rows(const int32_t *parents, uint32_t *mask, int32_t mask_wo
  * row counts as standing at position i = (tokens before the rows) + (bits set in its
  * mask) - 1, and of the tokens j before the rows it sees those with j > i - w or
  * j < sinks; the rows' own tokens are not subject to the window.  (Bits past the
- * sequence's rows name no token, but count.)  A chain (row t sees rows 0 .. t)
- * gives awq_attention's outputs.
+ * sequence's rows name no token, but count.)  A chain (row t sees rows 0 .. t) gives
+ * awq_attention's outputs, but for the order of sums.
  * Everything else, the workspace included, is as with awq_attention.
  */
 size_t awq_tree_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,
@@ -575,8 +575,8 @@ awq_status awq_kv_keep(const int32_t *kept, int32_t kept_width, const int32_t *c
  * All arrays are device memory, outputs apart from inputs (AWQ_ERROR_INVALID_VALUE
  * where table_out or lens_out is the batch's).  0 <= new_seqs <= 65535, new_seqs *
  * table_width < 2^31.  The pages' contents and q_starts are not looked at; a page
- * number that names no page goes on as -1.
- *   workspace: as with awq_attention.
+ * number that names no page goes on as -1.  With new_seqs 0 nothing is written.
+ *   workspace: as with awq_attention (small tables need none: the query says 0).
  */
 size_t awq_kv_fork_workspace_bytes(int32_t new_seqs, const awq_kv_cache *cache, const awq_kv_batch *batch);
 

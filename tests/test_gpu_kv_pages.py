@@ -88,6 +88,38 @@ def test_many_kept_rows(dim, page, dead, new, counts):
     keep(t, [subset(n, m, t.g) for n, m in zip(new, counts)], counts)
 
 
+def test_cache_beyond_4_gib():
+    """Pages whose codes lie past 2^32 bytes: copied, and compacted from one to another."""
+    heads, page, dim, pages = 8, 256, 256, 8300
+    cache = binding.new_kv_cache(pages, page, heads, dim, DEV)
+    assert cache.k.numel() > 1 << 32
+    k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    rows = torch.randint(0, 0x7E, (3, heads, page, dim), generator=g, device=DEV, dtype=torch.uint8)
+    last = [pages - 1, pages - 2, pages - 3]
+    for i in range(3):
+        k[i], v[i] = rows[i], rows[i].transpose(1, 2)
+        k[last[i]], v[last[i]] = 0x7F, 0x7F
+    cache.k_scales[:3], cache.v_scales[:3] = 0.5, 0.25
+    cache.k_scales[pages - 3:], cache.v_scales[pages - 3:] = 7.0, 7.0
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    binding.kv_copy(ints([[i, last[i]] for i in range(3)]), cache)
+    for i in range(3):
+        assert torch.equal(k[last[i]], rows[i]) and torch.equal(v[last[i]], rows[i].transpose(1, 2))
+    assert bool((cache.k_scales[pages - 3:] == 0.5).all()) and bool((cache.v_scales[pages - 3:] == 0.25).all())
+    tokens = rows.transpose(0, 1).flatten(1, 2)                              # [heads][3 pages][dim]
+    batch = binding.KvBatch(ints([last]), ints([3 * page]), ints([0, 3 * page]), 3 * page, 3 * page)
+    for kept in (list(range(0, 3 * page, 3)), [1, 200]):                     # many; then few of those
+        n = len(kept)
+        lens = binding.kv_keep(ints([kept]), ints([n]), cache, batch)
+        assert lens.tolist() == [n]
+        tokens = torch.cat([tokens[:, kept], tokens[:, n:]], 1)
+        for i in range(3):
+            have = tokens[:, i * page: (i + 1) * page]
+            assert torch.equal(k[last[i]], have) and torch.equal(v[last[i]], have.transpose(1, 2))
+            assert torch.equal(k[i], rows[i]) and torch.equal(v[i], rows[i].transpose(1, 2))
+
+
 @pytest.mark.parametrize("page", [16, 64])
 def test_scales_far_apart(page):
     """Codes that become subnormal, or nothing, under the larger scale of a neighbour."""
