@@ -8,11 +8,10 @@
 //
 // Remainders (heads of up to 128 elements): they are a weight's 2^-12 at most, so e5m2 is enough for
 // them, and a product of e5m2 with the values' codes as they are, of all 64 keys at once, takes
-// the time of two of halves where four were.  What e5m2 rounds off is 2^-15 of a weight
-// (half a step of 2^-3 of 2^-12), to either side alike, and nothing more above 2^-16, its least subnormal,
-// where a row's largest weight is 2^11 to 2^15.  The error against 64 bits is fp16's own rounding as before, 2.08e-4;
-// 4.6% of the outputs are not the exact result's rounding, where 0.2% were.  16 trees of up to 64 rows
-// over up to 8191 keys 191 -> 184 us, one of 48 over 131000 322 -> 309.
+// the time of two of halves where four were.  What e5m2 rounds off is 2^-15 of a weight, to
+// either side alike; weights below 2^-5, 2^-16 of a row's largest and less, are halves (2^-12).  The error against
+// 64 bits stays fp16's own rounding, 2.08e-4; 4.6% of the outputs are not the exact result's
+// rounding, where 0.2% were.  16 trees of 64 rows over 8k keys 237 -> 221 us, one of 48 over 131000 339 -> 305.
 //
 // Bound: vector and matrix instructions, one after the other: 390 or so of a wave for 32 rows by 64 keys of 128
 // elements beside 32 products of halves and four of 64 keys, which hold the vector port up for 11 cycles each.  16
