@@ -96,7 +96,7 @@ def test_draft_accept_fork_through_quantized_layers():
 class Step:
     """A step's buffers: three sequences that fork among each other, with trees of n rows each."""
 
-    def __init__(self, seed, n, dtype, dim, page, ctx, heads=(8, 2)):
+    def __init__(self, seed, n, dtype, dim, page, ctx, heads=(6, 2)):
         self.n, self.heads, self.dim = n, heads, dim
         self.t = kc.Batch(seed, dtype, [n] * 3, [c + n for c in ctx], *heads, dim, page).fill(ctx)
         self.t.width += 12
