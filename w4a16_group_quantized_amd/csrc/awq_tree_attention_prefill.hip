@@ -15,8 +15,8 @@
 //
 // Bound: vector and matrix instructions, one after the other: 390 or so of a wave for 32 rows by 64 keys of 128
 // elements beside 32 products of halves and four of 64 keys, which hold the vector port up for 11 cycles each.  16
-// trees of up to 64 rows over up to 8191 keys, 32 heads on 8: 184 us (74 at the rate of a large matrix product); one
-// of 48 rows, 64 heads on 8, over 131000 keys: 309 us (172).  Eight waves in two groups, one at its products
+// trees of up to 64 rows over up to 8191 keys, 32 heads on 8: 169 to 181 us (74 at the rate of a large matrix product); one
+// of 48 rows, 64 heads on 8, over 131000 keys: 304 to 310 us (172).  Eight waves in two groups, one at its products
 // while the other is at its weights: 279 us where this took 257 (16 trees of 64 rows over 8192 keys, then).
 #include <algorithm>
 
