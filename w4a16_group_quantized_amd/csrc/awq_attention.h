@@ -264,6 +264,10 @@ constexpr int kPart = D + 4;
 hipError_t launch_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
 hipError_t launch_tree_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
 
+// Trees' keys are cut from as many tiles, or fewer where row tiles (of all kv heads) do not fill the
+// GPU: 16 trees of 60 rows of 32 heads on 8 over 1000 keys 71 us cut, 45 not.
+constexpr int kTreeCutTiles = 24, kTreeFullTiles = 256;
+
 // Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).
 // row_tiles: of each sequence, or with `flat` of all of them, one after the other.
 int prefill_row_tiles(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, int few, bool flat);

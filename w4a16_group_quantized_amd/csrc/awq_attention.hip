@@ -217,14 +217,24 @@ __global__ void __launch_bounds__(256) combine_wave_kernel(AttnArgs p) {
 //   16 x 2, 16k               67/55    120/78   175/105   178/113   333/201   661/376
 //   16 x 8, 500               16/25     28/28     40/29     51/30     96/39    187/70
 //   16 x 8, 4000              54/57    101/79   146/114   192/124   375/184   750/341
-int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim) {
+//
+// Drafted trees have a kernel of their own for many rows, which takes over earlier (sequences x kv heads,
+// rows times heads of a kv head, keys, us of the split / tree kernel): 16 x 8, 56 rows, 8000 100 / 81; 80, 4000 73 / 70; 160, 2000
+// 72 / 70; 1 x 8, 96, 8000 32 / 27; heads of 64, 112, 8000 24 / 22; 320, 2000 37 / 26.  And where
+// its row tiles fill the GPU without a cut: 16 x 8, 240 rows, 500 46 / 29; 1000 65 / 45; 160,
+// 1000 44 / 57; but 8 x 8, 256 rows, 1000 36 / 50.  Heads of 256 as prompts.
+int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim, bool tree, long long most) {
     static const int rows[3][2][5] = {{{80, 80, 80, 144, 512}, {96, 128, 768, 768, 768}},
                                       {{72, 72, 72, 120, 288}, {64, 96, 256, 384, 768}},
                                       {{24, 24, 24, 72, 96}, {24, 24, 40, 72, 288}}};
+    static const int tree_rows[2][2][5] = {{{80, 80, 80, 96, 256}, {96, 128, 768, 768, 768}},
+                                           {{60, 72, 72, 80, 288}, {48, 80, 256, 384, 768}}};
     const long long pairs = (long long)seqs * kv_heads, all = pairs * tiles;
     const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
     const int at = all >= 12000 ? 0 : all >= 3000 ? 1 : all >= 1500 ? 2 : all >= 400 ? 3 : 4;
-    return (int)std::max<long long>(rows[width][seqs >= kXcds][at], (width == 2 ? 320 : 640) / pairs);
+    int from = (tree && width < 2 ? tree_rows : rows)[width][seqs >= kXcds][at];
+    if (tree && width == 1 && tiles >= 8 && tiles < kTreeCutTiles && pairs * ((most + 127) / 128) >= kTreeFullTiles) from = std::min(from, 200);
+    return (int)std::max<long long>(from, (width == 2 ? 320 : 640) / pairs);
 }
 
 // The grid of a call: the most chunks, whose number is found on the device, and the
@@ -247,7 +257,7 @@ Plan plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, 
     long long keys = max_kv;
     if (window > 0) keys = std::min(keys, (long long)window + max_q + std::min(sinks, max_kv) + 2 * kTile);
     const long long tiles = (keys + kTile - 1) / kTile;
-    pl.few = prompt_rows(seqs, kv_heads, tiles, head_dim);
+    pl.few = prompt_rows(seqs, kv_heads, tiles, head_dim, tree, (long long)max_q * group);
     pl.prompt = (long long)max_q * group >= pl.few;
     pl.mixed = pl.prompt && rows_differ(seqs, rows, max_q);
     pl.row_tiles = pl.target = 0;

@@ -737,7 +737,7 @@ TreePlan tree_plan(int seqs, int rows, int kv_heads, int group, int head_dim, in
                                                           : ((long long)max_q * group + each - 1) / each * seqs);
     const long long all = groups * kv_heads;
     TreePlan t{(int)std::min<long long>(groups, ((1 << 24) - 1) / kv_heads), 1, waves};
-    if (key_tiles >= 2 * kLeastChunk && all < kManyTreeTiles) {
+    if (key_tiles >= (all < kTreeFullTiles ? 2 * kLeastChunk : kTreeCutTiles) && all < kManyTreeTiles) {
         t.shares = std::max(1, slots / kv_heads);
         t.room = (int)std::max<long long>(3, std::min<long long>({2 * slots / all + 1, key_tiles / kLeastChunk + 1, kMostSplits + 1}));
     }
