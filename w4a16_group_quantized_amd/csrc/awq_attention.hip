@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(256) combine_wave_kernel(AttnArgs p) {
 // Drafted trees have a kernel of their own for many rows, which takes over earlier (sequences x kv heads,
 // rows times heads of a kv head, keys, us of the split / tree kernel): 16 x 8, 56 rows, 8000 100 / 81; 80, 4000 73 / 70; 160, 2000
 // 72 / 70; 1 x 8, 96, 8000 32 / 27; heads of 64, 112, 8000 24 / 22; 320, 2000 37 / 26.  And where
-// its row tiles fill the GPU without a cut: 16 x 8, 240 rows, 500 46 / 29; 1000 65 / 45; 160,
+// its row tiles fill the GPU without a cut: 64 x 8, 240 rows, 100 89 / 55; 16 x 8, 500 46 / 29; 1000 65 / 45; 160,
 // 1000 44 / 57; but 8 x 8, 256 rows, 1000 36 / 50.  Heads of 256 as prompts.
 int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim, bool tree, long long most) {
     static const int rows[3][2][5] = {{{80, 80, 80, 144, 512}, {96, 128, 768, 768, 768}},
@@ -233,7 +233,7 @@ int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim, bool tree
     const int width = head_dim > 128 ? 2 : head_dim > 64 ? 1 : 0;
     const int at = all >= 12000 ? 0 : all >= 3000 ? 1 : all >= 1500 ? 2 : all >= 400 ? 3 : 4;
     int from = (tree && width < 2 ? tree_rows : rows)[width][seqs >= kXcds][at];
-    if (tree && width == 1 && tiles >= 8 && tiles < kTreeCutTiles && pairs * ((most + 127) / 128) >= kTreeFullTiles) from = std::min(from, 200);
+    if (tree && width == 1 && tiles < kTreeCutTiles && pairs * ((most + 127) / 128) >= kTreeFullTiles) from = std::min(from, 200);
     return (int)std::max<long long>(from, (width == 2 ? 320 : 640) / pairs);
 }
 
