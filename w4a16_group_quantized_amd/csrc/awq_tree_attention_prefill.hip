@@ -731,13 +731,24 @@ hipError_t launch_dim(const AttnArgs &p, int D, int waves, hipStream_t s) {
 // and chunks that a row tile has room for, twice what it has on average, since sequences are not
 // equally long.
 TreePlan tree_plan(int seqs, int rows, int kv_heads, int group, int head_dim, int max_q, bool mixed, int few, long long key_tiles) {
-    const int waves = waves_of(head_dim, (long long)max_q * group), each = rows_of(head_dim, waves), slots = kTreeWaves / waves;
+    int waves = waves_of(head_dim, (long long)max_q * group);
     // row tiles of a kv head: all that there can be, or of sequences of max_q rows
-    const long long groups = std::max<long long>(1, mixed ? (long long)rows * group / each + std::min<long long>(seqs, (long long)rows * group / few)
-                                                          : ((long long)max_q * group + each - 1) / each * seqs);
-    const long long all = groups * kv_heads;
+    const auto row_tiles = [&]() {
+        const int each = rows_of(head_dim, waves);
+        return std::max<long long>(1, mixed ? (long long)rows * group / each + std::min<long long>(seqs, (long long)rows * group / few)
+                                            : ((long long)max_q * group + each - 1) / each * seqs);
+    };
+    const auto cut = [&]() {
+        const long long all = row_tiles() * kv_heads;
+        return key_tiles >= (all < kTreeFullTiles ? 2 * kLeastChunk : kTreeCutTiles) && all < kManyTreeTiles;
+    };
+    // (where keys are not cut, sequences of fewer rows than the longest gain nothing from two waves: 32 trees of up
+    // to 40 rows of 32 heads on 8 over up to 1000 keys 70 us, with four 53)
+    if (waves == 2 && (long long)max_q * group > 64 && !cut()) waves = 4;
+    const int slots = kTreeWaves / waves;
+    const long long groups = row_tiles(), all = groups * kv_heads;
     TreePlan t{(int)std::min<long long>(groups, ((1 << 24) - 1) / kv_heads), 1, waves};
-    if (key_tiles >= (all < kTreeFullTiles ? 2 * kLeastChunk : kTreeCutTiles) && all < kManyTreeTiles) {
+    if (cut()) {
         t.shares = std::max(1, slots / kv_heads);
         t.room = (int)std::max<long long>(3, std::min<long long>({2 * slots / all + 1, key_tiles / kLeastChunk + 1, kMostSplits + 1}));
     }
