@@ -1,22 +1,15 @@
 // awq_tree_attention for many rows: see awq_attention_split.h for the formula and the transposed
-// products, and awq_attention_prefill.hip for the tiles in LDS, how keys are dealt to the
-// products, and the arithmetic of a row, which is the same here but for the remainders of weights.
+// products, and awq_attention_prefill.hip for the tiles in LDS and how keys are dealt to the
+// products; the arithmetic of a row is the same here, weights of two halves in it.
 //
 // What differs: all rows of a tree see the same tiles of keys, so workgroups go over several row tiles,
 // in equal shares of all the work (TreeShare); and which of a tile's keys a row sees is bits, from the
 // mask's words, needed for the tiles at the tree (and at a window's border) alone.
 //
-// Remainders (heads of up to 128 elements): they are a weight's 2^-12 at most, so e5m2 is enough for
-// them, and a product of e5m2 with the values' codes as they are, of all 64 keys at once, takes
-// the time of two of halves where four were.  What e5m2 rounds off is 2^-15 of a weight, to
-// either side alike; weights below 2^-5, 2^-16 of a row's largest and less, are halves (2^-12).  The error against
-// 64 bits stays fp16's own rounding, 2.08e-4; 4.6% of the outputs are not the exact result's
-// rounding, where 0.2% were.  16 trees of 64 rows over 8k keys 237 -> 221 us, one of 48 over 131000 339 -> 305.
-//
 // Bound: vector and matrix instructions, one after the other: 390 or so of a wave for 32 rows by 64 keys of 128
-// elements beside 32 products of halves and four of 64 keys, which hold the vector port up for 11 cycles each.  16
-// trees of up to 64 rows over up to 8191 keys, 32 heads on 8: 169 to 181 us (74 at the rate of a large matrix product); one
-// of 48 rows, 64 heads on 8, over 131000 keys: 304 to 310 us (172).  Eight waves in two groups, one at its products
+// elements beside 48 products, which hold the vector port up for 11 cycles each.  16 trees of up to 64 rows
+// over up to 8191 keys, 32 heads on 8: 179 us (74 at the rate of a large matrix product); one of 48 rows, 64
+// heads on 8, over 131000 keys: 331 us (172).  Eight waves in two groups, one at its products
 // while the other is at its weights: 279 us where this took 257 (16 trees of 64 rows over 8192 keys, then).
 #include <algorithm>
 
@@ -39,20 +32,6 @@ constexpr int rows_of(int head_dim, int waves) { return kWaveRows * (in_pairs(he
 // fifth): 16 trees over 8k keys, four / two: 64 rows times heads 127 / 97 us, 160 211 / 196, 256 240 / 264.
 int waves_of(int head_dim, long long rows) {
     return !in_pairs(head_dim) && 6 * ((rows + 63) / 64 * 64) < 5 * ((rows + 127) / 128 * 128) ? 2 : 4;
-}
-
-typedef int int8v_t __attribute__((ext_vector_type(8)));
-
-// Two weights as halves, and what their roundings leave.  (The halves are conversions, which
-// read a and b first: no wait is due between their powers and these.)
-__device__ __forceinline__ void lead_and_left(float a, float b, uint32_t &lead, float &left_a, float &left_b) {
-    const half2_t h = {(half_t)a, (half_t)b};
-    lead = __builtin_bit_cast(uint32_t, h);
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(left_a) : "v"(lead), "v"(a));
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(left_b) : "v"(lead), "v"(b));
-}
-__device__ __forceinline__ int e5m2x4(float a, float b, float c, float d) {
-    return __builtin_amdgcn_cvt_pk_bf8_f32(c, d, __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false), true);
 }
 
 // Drafted trees: how workgroups share the work of a kv head.  All rows of a tree see the same
@@ -595,28 +574,24 @@ __global__ void __launch_bounds__(64 * W, 2) tree_kernel(AttnArgs p) {
                         back[u] = 0.0f;
                     }
                 }
-                half8_t w[2][2];               // leading parts
-                int8v_t rests;                 // remainders, e5m2
+                half8_t w[2][4];               // leading parts, remainders
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float base = kWeightBits + to_unit[u] - shift;
                     float sum = 0.0f;
-                    uint32_t lead[8];
+                    uint32_t lead[8], rest[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        float f[4], r[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e + k], ks[u], base));
-                            sum += f[k];
-                        }
-                        lead_and_left(f[0], f[1], lead[e / 2], r[0], r[1]);
-                        lead_and_left(f[2], f[3], lead[e / 2 + 1], r[2], r[3]);
-                        rests[4 * u + e / 4] = e5m2x4(r[0], r[1], r[2], r[3]);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], ks[u], base));
+                        const float g = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e + 1], ks[u], base));
+                        sum += f;
+                        sum += g;
+                        lead_and_rest(f, g, lead[e / 2], rest[e / 2]);
                     }
+                    settle(rest);
                     l += sum * back[u];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) w[u][e] = halves8(lead + 4 * e);
+                    for (int e = 0; e < 4; ++e) w[u][e] = halves8((e < 2 ? lead : rest) + 4 * (e & 1));
                 }
 #pragma unroll
                 for (int e = 0; e < kP; ++e) {
@@ -625,12 +600,8 @@ __global__ void __launch_bounds__(64 * W, 2) tree_kernel(AttnArgs p) {
                         v0 = vb[piece<4>(32 * e + 32 + m, hf)];
                         v1 = vb[piece<4>(32 * e + 32 + m, 2 + hf)];
                     }
-                    const int8v_t codes = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-                    o[e] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes, rests, o[e], 0, 1, 0, 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.x, a0.y), w[0][0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a0.z, a0.w), w[0][1], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.x, a1.y), w[1][0], o[e], 0, 0, 0);
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_half(a1.z, a1.w), w[1][1], o[e], 0, 0, 0);
+                    add_products(o[e], a0, w[0]);
+                    add_products(o[e], a1, w[1]);
                 }
             };
 
