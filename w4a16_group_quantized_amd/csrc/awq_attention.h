@@ -52,9 +52,8 @@ __device__ __forceinline__ Tiles visible_tiles(const AttnArgs &p, int lo, int hi
 
 // A drafted tree's rows see all tokens before the tree (under a window those that are near
 // enough, or first), and of the tree the rows that their bits name, in any order.  So tiles
-// go from those that a row right behind these tokens' last sees to the last token.  The last
-// token's number, which bounds every row's place, stands for the place where only time
-// depends on it.
+// go from those that a row on these tokens' last sees to the last token.  (Of a row's place no more
+// is known here: it goes by the bits set, which may be more than the sequence has rows.)
 template <bool TREE>
 __device__ __forceinline__ int first_place(const Seq &s, int row) { return TREE ? s.first() - 1 : s.first() + row; }
 template <bool TREE>
@@ -72,7 +71,7 @@ __device__ __forceinline__ ArgsAgain args_again() {
 
 // What a drafted tree's row sees of sixteen keys: a bit for each.
 struct TreeSight {
-    int row, first, far;     // keys before the tree up to `far` are out of sight, but for the first ones
+    int row, first, far;     // keys before the tree up to `far` are out of the row's sight, but for the first ones
     __device__ __forceinline__ TreeSight(const AttnArgs &p, const Seq &s, int token) : row(s.row0 + token), first(s.first()), far(-1) {
         if (p.window > 0) {
             far = first - 1 - p.window;

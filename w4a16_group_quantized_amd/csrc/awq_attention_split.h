@@ -253,8 +253,9 @@ __global__ void __launch_bounds__(64 * W, D > 128 ? 1 : D > 64 ? 2 : 4) split_ke
                 ask(min(i + 2 * W, t1 - 1));
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const bool whole = live == 16 && j0 + kTile <= lo + 1 &&
-                               (p.window <= 0 || j0 > hi - p.window || j0 + kTile <= p.sinks);
+            int hidden = hi - p.window;        // keys up to it are out of sight of some of the rows
+            if constexpr (TREE) hidden = sight.far;            // (of the lane's)
+            const bool whole = live == 16 && j0 + kTile <= lo + 1 && (p.window <= 0 || j0 > hidden || j0 + kTile <= p.sinks);
             if (!__all(whole)) {
                 if constexpr (TREE) {
                     const uint32_t see = sight.sixteen(args_again(), jg, live);

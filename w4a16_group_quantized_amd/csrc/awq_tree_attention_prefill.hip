@@ -237,10 +237,16 @@ __global__ void __launch_bounds__(64 * W, 2) tree_kernel(AttnArgs p) {
         const int w0 = min(r0 + row_wave * kWaveRows, r1), w1 = min(w0 + kWaveRows - 1, r1);
         const bool idle = r0 + row_wave * kWaveRows > r1;
         const int lo = first_place<true>(s, 0), hi = s.len - 1;
-        const int seen_from = p.window > 0 ? hi - p.window + 1 : 0;            // keys that no window hides from a row
         const int r = min(w0 + m, r1);
         const int token = r / p.group, head = h * p.group + r % p.group;
         const TreeSight sight(p, s, token);
+        int seen_from = 0;                     // keys that no window hides from one of the wave's rows
+        if (p.window > 0) {
+            seen_from = sight.far + 1;
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) seen_from = max(seen_from, __shfl_xor(seen_from, k));
+            seen_from = __builtin_amdgcn_readfirstlane(seen_from);
+        }
         const uint16_t *qrow = p.q + (long long)(s.row0 + token) * p.q_stride + head * D + 16 * hf;
         float up = p.scale < 0.0f ? -1.0f : 1.0f, down = fabsf(p.scale);
         if constexpr (!__is_same(T, half_t)) {
