@@ -15,6 +15,7 @@
 
 #include "awq_attention.h"
 #include "awq_internal.h"
+#include "awq_tree_share.h"
 
 namespace awq {
 namespace {
@@ -142,12 +143,9 @@ struct TreeShare {
             all += __builtin_amdgcn_readlane(sum_up(m * units_of(other)), 63);
         }
         // a row tile has room for p.splits chunks
-        each = max((int)(((uint32_t)all + p.most - 1) / (uint32_t)p.most), units_of(kLeastShare));
-        if (p.splits > 1) each = max(each, units_of(most) / (p.splits - 1) + 1);
-        each = __builtin_amdgcn_readfirstlane(each);
-        // (k each <= all + most shares: below 2^31)
-        at = __builtin_amdgcn_readfirstlane(border(p, rows, l, k * each, all));
-        end = __builtin_amdgcn_readfirstlane(border(p, rows, l, (k + 1) * each, all));
+        each = __builtin_amdgcn_readfirstlane(share_units(all, p.most, units_of(kLeastShare), units_of(most), p.splits));
+        at = __builtin_amdgcn_readfirstlane(border(p, rows, l, share_border(k, each, all), all));
+        end = __builtin_amdgcn_readfirstlane(border(p, rows, l, share_border(k + 1, each, all), all));
     }
     // (What is not used while tiles are multiplied is kept in vector registers meanwhile, where there are some.)
     __device__ __forceinline__ void keep() {
@@ -169,8 +167,7 @@ struct TreeShare {
         count = ((stop - r.first) << shift) - start;   // (the last unit may be short: the caller's to cut)
         // borders inside of the row tile: of workgroups lo .. hi
         const int far = least(p, r.units);
-        const int lo = (int)((uint32_t)(r.first + far + each - 1) / (uint32_t)each);
-        const int last = r.first + r.units - far, hi = last < 0 ? -1 : (int)((uint32_t)last / (uint32_t)each);
+        const int lo = first_share_from(r.first + far, each), hi = last_share_upto(r.first + r.units - far, each);
         chunks = max(hi - lo + 1, 0) + 1;
         chunk = start == 0 ? 0 : number - lo + 1;
         at = stop;
