@@ -867,8 +867,6 @@ def kv_fork(from_: torch.Tensor, grow: torch.Tensor, cache: KvCache, batch: KvBa
         base = _new(at[3] + 1, torch.int32, device, stream)
         out = (base.as_strided((n, width), (width, 1)), base.as_strided((n,), (1,), at[1]), base.as_strided((n, 2), (2, 1), at[2]),
                base.as_strided((1,), (1,), at[3]))
-        if n == 0:
-            out[3].zero_()
         ptr = [base.data_ptr() + 4 * x for x in at]
     else:
         for t, x, name in zip(out, shapes, ("table", "lens", "copies", "missing")):
@@ -891,6 +889,9 @@ def kv_fork(from_: torch.Tensor, grow: torch.Tensor, cache: KvCache, batch: KvBa
         wp, nbytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
     _kv_call(device, stream, lib.awq_kv_fork, _kv_ints(from_, device, "from_"), _kv_ints(grow, device, "grow"), n, hp, c, b, *ptr,
              wp, nbytes)
+    if n == 0:                               # the call writes nothing then; none is missing
+        with torch.cuda.stream(stream):
+            out[3].zero_()
     return out
 
 
