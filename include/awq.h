@@ -516,8 +516,11 @@ awq_status awq_tree_rows(const int32_t *parents, uint32_t *mask, int32_t mask_wo
  * row counts as standing at position i = (tokens before the rows) + (bits set in its
  * mask) - 1, and of the tokens j before the rows it sees those with j > i - w or
  * j < sinks; the rows' own tokens are not subject to the window.  (Bits past the
- * sequence's rows name no token, but count.)  A chain (row t sees rows 0 .. t) gives
- * awq_attention's outputs, but for the order of sums.
+ * sequence's rows name no token, but count: under a window a row that sees all n
+ * rows has n bits set, not all of a word's.)  A chain (row t sees rows 0 .. t) gives
+ * awq_attention's outputs, but for the order of sums, without a window or with
+ * one of at least the sequence's rows; under a shorter one row t >= w sees its
+ * sequence's rows 0 .. t - w too, which awq_attention hides from it (sinks aside).
  * Everything else, the workspace included, is as with awq_attention.
  */
 size_t awq_tree_attention_workspace_bytes(int32_t q_heads, int32_t window, int32_t sinks,

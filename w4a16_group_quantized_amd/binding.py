@@ -814,7 +814,8 @@ def tree_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask: torch.
                    workspace: torch.Tensor | None = None) -> torch.Tensor:
     """attention where each row sees the tokens before its sequence's rows (with ``window`` > 0
     the last ones of them, and the first ``sinks``), and of these rows those whose bits are set
-    in ``mask`` int32 [rows][words] (see tree_rows)."""
+    in ``mask`` int32 [rows][words] (see tree_rows).  The window ends at the row's position, which
+    goes by the bits that are set, and does not hide any of these rows."""
     if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
         raise ValueError(f"mask must be [{q.shape[0]}][words], got {list(mask.shape)}")
     extra = (_kv_ints(mask, cache._device, "mask"), mask.shape[1])
