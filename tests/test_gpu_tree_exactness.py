@@ -235,3 +235,15 @@ def test_signed_sums(dtype, dim, page, heads, new, lens):
     bits, words = bits_of_trees(t)
     want, size, reach = dc.tree_attention(t, bits)
     within(run(t, bits, words), want, fine_tolerance(t, want, size, reach, 448 * float(t.vs.max())))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,page", [(64, 64), (128, 16), (256, 64)])
+@pytest.mark.parametrize("new,lens", [([6, 2], [420, 240]), ([180, 240], [420, 240])])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+def test_a_scale_argument(dtype, dim, page, new, lens, scale):
+    t = one_hot(kc.Batch(65, dtype, new, lens, 8, 2, dim, page)).fill()
+    bits, words = bits_of_trees(t)
+    want, size, reach = dc.tree_attention(t, bits, scale)
+    within(run(t, bits, words, scale=scale), want, fine_tolerance(t, want, size, reach, 448 * float(t.vs.max())))
