@@ -264,7 +264,7 @@ hipError_t launch_attention_split(const AttnArgs &p, int head_dim, bool bf16, bo
 hipError_t launch_tree_attention_split(const AttnArgs &p, int head_dim, bool bf16, bool wide, int row_tiles, hipStream_t s);
 
 // Trees' keys are cut from as many tiles, or fewer where row tiles (of all kv heads) do not fill the
-// GPU: 16 trees of 60 rows of 32 heads on 8 over 1000 keys 71 us cut, 45 not.
+// GPU: 16 trees of 60 rows of 32 heads on 8 over 1000 keys 73 us cut, 47 not.
 constexpr int kTreeCutTiles = 24, kTreeFullTiles = 256;
 
 // Rows by rows of 32 to a wave, for prompts (awq_attention_prefill.hip).

@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(256) combine_wave_kernel(AttnArgs p) {
 //   16 x 8, 4000              54/57    101/79   146/114   192/124   375/184   750/341
 //
 // Drafted trees have a kernel of their own for many rows, which takes over earlier (sequences x kv heads,
-// rows times heads of a kv head, keys, us of the split / tree kernel): 16 x 8, 56 rows, 8000 100 / 81; 80, 4000 73 / 70; 160, 2000
-// 72 / 70; 1 x 8, 96, 8000 32 / 27; heads of 64, 112, 8000 24 / 22; 320, 2000 37 / 26.  And where
-// its row tiles fill the GPU without a cut: 64 x 8, 240 rows, 100 89 / 55; 16 x 8, 500 46 / 29; 1000 65 / 45; 160,
-// 1000 44 / 57; but 8 x 8, 256 rows, 1000 36 / 50.  Heads of 256 as prompts.
+// rows times heads of a kv head, keys, us of the split / tree kernel): 16 x 8, 56 rows, 8000 108 / 89; 80, 4000 78 / 76; 160, 2000
+// 73 / 73; 1 x 8, 96, 8000 33 / 28; heads of 64, 112, 8000 24 / 22; 320, 2000 38 / 26.  And where
+// its row tiles fill the GPU without a cut: 64 x 8, 240 rows, 100 88 / 55; 16 x 8, 500 46 / 30; 1000 64 / 46; 160,
+// 1000 45 / 44; but 8 x 8, 256 rows, 1000 37 / 51.  Heads of 256 as prompts, and those of 64 with eight sequences and
+// more (16 x 8, 96 rows, 8000 78 / 90).
 int prompt_rows(int seqs, int kv_heads, long long tiles, int head_dim, bool tree, long long most) {
     static const int rows[3][2][5] = {{{80, 80, 80, 144, 512}, {96, 128, 768, 768, 768}},
                                       {{72, 72, 72, 120, 288}, {64, 96, 256, 384, 768}},

@@ -8,8 +8,8 @@
 //
 // Bound: vector and matrix instructions, one after the other: 390 or so of a wave for 32 rows by 64 keys of 128
 // elements beside 48 products, which hold the vector port up for 11 cycles each.  16 trees of up to 64 rows
-// over up to 8191 keys, 32 heads on 8: 179 us (74 at the rate of a large matrix product); one of 48 rows, 64
-// heads on 8, over 131000 keys: 331 us (172).  Eight waves in two groups, one at its products
+// over up to 8191 keys, 32 heads on 8: 170 to 187 us (74 at the rate of a large matrix product); one of 48 rows, 64
+// heads on 8, over 131000 keys: 318 to 343 us (172).  Eight waves in two groups, one at its products
 // while the other is at its weights: 279 us where this took 257 (16 trees of 64 rows over 8192 keys, then).
 #include <algorithm>
 
@@ -717,7 +717,7 @@ TreePlan tree_plan(int seqs, int rows, int kv_heads, int group, int head_dim, in
         return key_tiles >= (all < kTreeFullTiles ? 2 * kLeastChunk : kTreeCutTiles) && all < kManyTreeTiles;
     };
     // (where keys are not cut, sequences of fewer rows than the longest gain nothing from two waves: 32 trees of up
-    // to 40 rows of 32 heads on 8 over up to 1000 keys 70 us, with four 53)
+    // to 40 rows of 32 heads on 8 over up to 1000 keys 73 us, with four 57)
     if (waves == 2 && (long long)max_q * group > 64 && !cut()) waves = 4;
     const int slots = kTreeWaves / waves;
     const long long groups = row_tiles(), all = groups * kv_heads;
